@@ -67,7 +67,9 @@ enum {
                              the output of the call is not valid          */
   PFKV_ST_NO_PAGES = 16u, /* page allocator: fewer free pages than asked  */
   PFKV_ST_NOT_HELD = 32u, /* page allocator: the page is not handed out   */
-  PFKV_ST_DUPLICATE = 64u /* page allocator: id listed twice in one call  */
+  PFKV_ST_DUPLICATE = 64u, /* page allocator: id listed twice in one call;
+                              fork: the child is made or forked from twice  */
+  PFKV_ST_BAD_ROW = 128u  /* fork: a row outside the block table           */
 };
 
 /* Return codes. */
@@ -321,6 +323,89 @@ int pfkv_page_free(void *state, const int32_t *pages, int32_t n, uint32_t *page_
  * earlier entry; flagged entries get tags_out 0 and change nothing. */
 int pfkv_page_realloc(void *state, uint32_t *page_tags, const int32_t *pages, int32_t n, uint32_t *tags_out,
                       uint32_t *page_status, void *stream);
+
+/*
+ * Pages held by several requests.  page_refs : int32 [num_pages], caller
+ * owned and zeroed once, counts each page's holders beyond the first; fork
+ * and release (and compact, which moves it along) are the only writers.  A
+ * pool whose pages are shared gives pages back with pfkv_page_release:
+ * pfkv_page_free and pfkv_page_realloc take a page away from every holder at
+ * once (their mappings then fail the tag check when the page is handed on)
+ * and leave page_refs as it is.
+ */
+
+/* page_copy -- copies pages of a cache to other pages of the same cache: the
+ * first slots[i] slots (NULL: all) of every head of page src_pages[i], K and
+ * V, and in PER_TOKEN mode their scales, become those of page dst_pages[i].
+ * Codes and values are copied bit for bit; the rest of the page, and every
+ * tag, is left as it was.
+ * page_status : uint32 [n_pages]; PAGE_OOB (an id outside the pool) and
+ * BAD_LEN (slots[i] outside [0, page_size]) skip the entry, else 0.
+ * Destination pages must be distinct, and none may be a source of the same
+ * call (a page copied to itself is left alone). */
+int pfkv_page_copy(const pfkv_cache *cache, const int32_t *src_pages, const int32_t *dst_pages,
+                   const int32_t *slots, int32_t n_pages, uint32_t *page_status, void *stream);
+
+/* page_fork -- row children[i] of the block table gets the first lens[i]
+ * tokens of row parents[i], without copying full pages: the child's entries
+ * (and tags, where block_tags is given) of the full pages are the parent's,
+ * and each of these pages has one more holder.  Where lens[i] ends inside a
+ * page, that page's filled slots are copied into a fresh page, taken from
+ * `state` as by pfkv_page_alloc (its tag advances), so that parent and child
+ * go on appending apart.  Later entries of the child's row are left as they
+ * were; what the row named before must have been given back by the caller.
+ *   state       : the page allocator of this cache's pages
+ *   page_tags   : the cache's tag array, writable
+ *   block_table, block_tags : [batch][max_pages], updated in place;
+ *                 block_tags may be NULL without TAG_CHECK
+ *   fork_status : uint32 [n]; 0, or the reasons why entry i did nothing:
+ *     BAD_ROW   a row outside [0, batch)
+ *     BAD_LEN   lens[i] outside [0, max_pages * page_size]
+ *     PAGE_OOB, NOT_HELD   a page of the parent's context is outside the pool
+ *               or not handed out (PAGE_OOB also for all entries when `state`
+ *               has another number of pages than the cache)
+ *     STALE_TAG (TAG_CHECK) a page's tag differs from the parent's mapping
+ *     DUPLICATE the child is also the child of an earlier entry, or the
+ *               parent of any entry of the call
+ *     NO_PAGES  the sound entries together need more fresh pages than are
+ *               free: none of them is done, and nothing is taken
+ * Fresh pages are taken in list order. */
+int pfkv_page_fork(void *state, uint32_t *page_tags, int32_t *page_refs, const pfkv_cache *cache,
+                   const int32_t *parents, const int32_t *children, const int32_t *lens, int32_t n,
+                   int32_t *block_table, uint32_t *block_tags, int32_t batch, int32_t max_pages, uint32_t flags,
+                   uint32_t *fork_status, void *stream);
+
+/* page_release -- each listed page loses one holder; the page returns to the
+ * free list with its last one.  A page may be listed once per holder.  Where
+ * no page is shared this is pfkv_page_free.  page_status[i]: 0, PAGE_OOB, or
+ * NOT_HELD (not handed out, or given back by all its holders earlier in the
+ * list).  n must be below 2^30. */
+int pfkv_page_release(void *state, int32_t *page_refs, const int32_t *pages, int32_t n, uint32_t *page_status,
+                      void *stream);
+
+/* page_compact -- moves held pages with the highest ids into the lowest free
+ * pages until the H held pages are 0 .. H - 1, or max_moves pages have moved:
+ * the m-th highest held page goes to the m-th lowest free one.  Contents,
+ * per-token scales and holder counts move along; the destination's tag
+ * advances, as on every hand-out; the free list is put in the order of a
+ * fresh state (the smallest id handed out first).
+ *   block_table, block_tags : [batch][max_pages].  Every live entry that names
+ *                 a moved page gets the new id and the new tag; with
+ *                 block_tags an entry whose tag differs from the page's is
+ *                 stale and stays as it is (block_tags NULL: all are taken).
+ *   used        : int32 [batch], live entries of each row (NULL: all)
+ *   page_refs   : may be NULL when no page is shared
+ *   moved_src, moved_dst : int32 [max_moves], the moves in order (sources
+ *                 decreasing, destinations increasing); entries past
+ *                 *n_moved are left as they were
+ *   n_moved     : int32, the number of moves (0 when `state` has another
+ *                 number of pages than the cache: nothing is done)
+ * Mappings of the moved pages that are kept elsewhere must be renamed by the
+ * caller, who has the moves. */
+int pfkv_page_compact(void *state, uint32_t *page_tags, int32_t *page_refs, const pfkv_cache *cache,
+                      int32_t *block_table, uint32_t *block_tags, const int32_t *used, int32_t batch,
+                      int32_t max_pages, int32_t max_moves, int32_t *moved_src, int32_t *moved_dst, int32_t *n_moved,
+                      void *stream);
 
 /*
  * calibrate_scales -- per-head FP8 scales s[h] = fp32(amax/448) over

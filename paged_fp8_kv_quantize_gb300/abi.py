@@ -28,6 +28,7 @@ ST_TIMEOUT = 8
 ST_NO_PAGES = 16
 ST_NOT_HELD = 32
 ST_DUPLICATE = 64
+ST_BAD_ROW = 128
 
 EXPORTS = (
     "pfkv_kv_append_quantize",
@@ -42,6 +43,10 @@ EXPORTS = (
     "pfkv_page_alloc",
     "pfkv_page_free",
     "pfkv_page_realloc",
+    "pfkv_page_copy",
+    "pfkv_page_fork",
+    "pfkv_page_release",
+    "pfkv_page_compact",
     "pfkv_calibrate_scales",
     "pfkv_e4m3_encode",
     "pfkv_strerror",
@@ -107,6 +112,14 @@ def _load():
     L.pfkv_page_free.argtypes = [P, P, i32, P, P]
     L.pfkv_page_realloc.restype = ctypes.c_int
     L.pfkv_page_realloc.argtypes = [P, P, P, i32, P, P, P]
+    L.pfkv_page_copy.restype = ctypes.c_int
+    L.pfkv_page_copy.argtypes = [cp, P, P, P, i32, P, P]
+    L.pfkv_page_fork.restype = ctypes.c_int
+    L.pfkv_page_fork.argtypes = [P, P, P, cp, P, P, P, i32, P, P, i32, i32, u32, P, P]
+    L.pfkv_page_release.restype = ctypes.c_int
+    L.pfkv_page_release.argtypes = [P, P, P, i32, P, P]
+    L.pfkv_page_compact.restype = ctypes.c_int
+    L.pfkv_page_compact.argtypes = [P, P, P, cp, P, P, P, i32, i32, i32, P, P, P, P]
     L.pfkv_calibrate_scales.restype = ctypes.c_int
     L.pfkv_calibrate_scales.argtypes = [P, i64, i32, i32, P, P]
     L.pfkv_e4m3_encode.restype = ctypes.c_int
@@ -150,6 +163,18 @@ def _dev(t, name, dtype=None):
         raise ValueError(f"{name} must be contiguous")
     if dtype is not None and t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    return t
+
+
+def _vec(t, name, n, dtype=torch.int32):
+    """An optional contiguous device tensor of n elements on the current device."""
+    if t is None:
+        return None
+    _dev(t, name, dtype)
+    if t.numel() != n:
+        raise ValueError(f"{name} must have {n} elements, got {t.numel()}")
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, not on the current device")
     return t
 
 
@@ -330,11 +355,28 @@ def handoff_bf16_to_fp8(src: PagedCache, dst: PagedCache, src_pages, dst_pages, 
     return page_status
 
 
+def page_copy(cache: PagedCache, src_pages, dst_pages, slots=None, page_status=None, stream=None):
+    """Copy pages src_pages[i] to dst_pages[i] of the same cache, the first slots[i] slots of each (None: all)."""
+    n = src_pages.numel()
+    _vec(dst_pages, "dst_pages", n)
+    _vec(slots, "slots", n)
+    if page_status is None:
+        page_status = torch.empty(n, dtype=torch.int32, device=src_pages.device)
+    d = cache.desc()
+    rc = lib.pfkv_page_copy(ctypes.byref(d), _ptr(_vec(src_pages, "src_pages", n)), _ptr(dst_pages), _ptr(slots), n,
+                            _ptr(_vec(page_status, "page_status", n)), _stream(stream))
+    _check("pfkv_page_copy", rc)
+    return page_status
+
+
 class PageAllocator:
     """Device-resident free list over num_pages pages (pfkv_page_allocator_*).
 
-    Every hand-out (alloc, realloc) advances the page's tag in the cache's
-    page_tags; the returned tags go into the new owner's block_tags."""
+    Every hand-out (alloc, realloc, a fork's fresh page, a compaction's
+    destination) advances the page's tag in the cache's page_tags; the
+    returned tags go into the new owner's block_tags.  `refs` counts each
+    page's holders beyond the first: pages that fork has shared are given
+    back with release, not free."""
 
     def __init__(self, num_pages, held_pages=None, device="cuda", stream=None):
         self.num_pages = int(num_pages)
@@ -349,6 +391,8 @@ class PageAllocator:
         rc = lib.pfkv_page_allocator_init(_ptr(self.state), nbytes, self.num_pages, _ptr(hp) if n_held else None,
                                           n_held, _stream(stream))
         _check("pfkv_page_allocator_init", rc)
+        with torch.cuda.stream(stream):  # None: the current one
+            self.refs = torch.zeros(self.num_pages, dtype=torch.int32, device=device)
 
     def alloc(self, n, page_tags, stream=None):
         """-> (pages int32 [n], tags int32 [n] (uint32 bits), status int32 [1]) on the device."""
@@ -377,6 +421,53 @@ class PageAllocator:
                                    _ptr(tags), _ptr(st), _stream(stream))
         _check("pfkv_page_realloc", rc)
         return tags, st
+
+    def fork(self, cache, parents, children, lens, block_table, block_tags=None, flags=0, fork_status=None,
+             stream=None):
+        """Rows children[i] of block_table (and block_tags) get the first lens[i] tokens of rows parents[i]: full
+        pages shared, the partly filled last one copied into a fresh page (pfkv_page_fork).  -> fork_status [n]"""
+        n = parents.numel()
+        B, MP = block_table.shape
+        if fork_status is None:
+            fork_status = torch.empty(n, dtype=torch.int32, device=parents.device)
+        d = cache.desc()
+        rc = lib.pfkv_page_fork(
+            _ptr(self.state), _ptr(_vec(cache.page_tags, "page_tags", cache.P)), _ptr(self.refs), ctypes.byref(d),
+            _ptr(_vec(parents, "parents", n)), _ptr(_vec(children, "children", n)), _ptr(_vec(lens, "lens", n)), n,
+            _ptr(_vec(block_table, "block_table", B * MP)), _ptr(_vec(block_tags, "block_tags", B * MP)), B, MP,
+            int(flags), _ptr(_vec(fork_status, "fork_status", n)), _stream(stream))
+        _check("pfkv_page_fork", rc)
+        return fork_status
+
+    def release(self, pages, page_status=None, stream=None):
+        """Take one holder off each listed page; a page returns to the free list with its last (pfkv_page_release)."""
+        n = pages.numel()
+        if page_status is None:
+            page_status = torch.empty(n, dtype=torch.int32, device=pages.device)
+        rc = lib.pfkv_page_release(_ptr(self.state), _ptr(self.refs), _ptr(_vec(pages, "pages", n)), n,
+                                   _ptr(_vec(page_status, "page_status", n)), _stream(stream))
+        _check("pfkv_page_release", rc)
+        return page_status
+
+    def compact(self, cache, block_table, block_tags=None, used=None, max_moves=None, stream=None):
+        """Move the highest held pages into the lowest free ones and rename them in block_table (and block_tags),
+        the first used[b] entries of each row (pfkv_page_compact).
+        -> (moved_src, moved_dst, n_moved [1]) on the device; the lists are filled up to n_moved."""
+        B, MP = block_table.shape
+        room = self.num_pages // 2  # no pool needs more moves
+        m = room if max_moves is None else min(int(max_moves), room)
+        dev = self.state.device
+        src = torch.empty(max(m, 1), dtype=torch.int32, device=dev)[:m]
+        dst = torch.empty(max(m, 1), dtype=torch.int32, device=dev)[:m]
+        n_moved = torch.empty(1, dtype=torch.int32, device=dev)
+        d = cache.desc()
+        rc = lib.pfkv_page_compact(
+            _ptr(self.state), _ptr(_vec(cache.page_tags, "page_tags", cache.P)), _ptr(self.refs), ctypes.byref(d),
+            _ptr(_vec(block_table, "block_table", B * MP)), _ptr(_vec(block_tags, "block_tags", B * MP)),
+            _ptr(_vec(used, "used", B)), B, MP, m, _ptr(src) if m else None, _ptr(dst) if m else None, _ptr(n_moved),
+            _stream(stream))
+        _check("pfkv_page_compact", rc)
+        return src, dst, n_moved
 
     def free_count(self):
         """Reads the state's free count (synchronises with the device)."""

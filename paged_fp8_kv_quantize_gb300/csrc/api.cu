@@ -313,6 +313,60 @@ int pfkv_page_realloc(void *state, uint32_t *page_tags, const int32_t *pages, in
   return launch_page_realloc(state, page_tags, pages, n, tags_out, page_status, static_cast<cudaStream_t>(stream));
 }
 
+int pfkv_page_copy(const pfkv_cache *cache, const int32_t *src_pages, const int32_t *dst_pages, const int32_t *slots,
+                   int32_t n_pages, uint32_t *page_status, void *stream) {
+  int rc = check_cache(cache);
+  if (rc) return rc;
+  if (n_pages < 0) return PFKV_ERR_SHAPE;
+  if (n_pages == 0) return PFKV_OK;
+  if (!src_pages || !dst_pages || !page_status) return PFKV_ERR_NULL;
+  return launch_page_copy(*cache, src_pages, dst_pages, slots, n_pages, page_status,
+                          static_cast<cudaStream_t>(stream));
+}
+
+int pfkv_page_fork(void *state, uint32_t *page_tags, int32_t *page_refs, const pfkv_cache *cache,
+                   const int32_t *parents, const int32_t *children, const int32_t *lens, int32_t n,
+                   int32_t *block_table, uint32_t *block_tags, int32_t batch, int32_t max_pages, uint32_t flags,
+                   uint32_t *fork_status, void *stream) {
+  int rc = check_cache(cache);
+  if (rc) return rc;
+  if (!state || !page_tags || !page_refs) return PFKV_ERR_NULL;
+  if (n < 0 || batch < 0 || max_pages < 1 || (uint64_t)batch * (uint64_t)max_pages > (1ull << 40))
+    return PFKV_ERR_SHAPE;
+  if (!aligned256(state)) return PFKV_ERR_ALIGN;
+  if (n == 0) return PFKV_OK;
+  if (!parents || !children || !lens || !block_table || !fork_status) return PFKV_ERR_NULL;
+  if ((flags & PFKV_FLAG_TAG_CHECK) && !block_tags) return PFKV_ERR_NULL;
+  return launch_page_fork(state, page_tags, page_refs, *cache, parents, children, lens, n, block_table, block_tags,
+                          batch, max_pages, flags, fork_status, static_cast<cudaStream_t>(stream));
+}
+
+int pfkv_page_release(void *state, int32_t *page_refs, const int32_t *pages, int32_t n, uint32_t *page_status,
+                      void *stream) {
+  if (!state || !page_refs) return PFKV_ERR_NULL;
+  if (n < 0 || n >= (1 << 30)) return PFKV_ERR_SHAPE;
+  if (!aligned256(state)) return PFKV_ERR_ALIGN;
+  if (n == 0) return PFKV_OK;
+  if (!pages || !page_status) return PFKV_ERR_NULL;
+  return launch_page_release(state, page_refs, pages, n, page_status, static_cast<cudaStream_t>(stream));
+}
+
+int pfkv_page_compact(void *state, uint32_t *page_tags, int32_t *page_refs, const pfkv_cache *cache,
+                      int32_t *block_table, uint32_t *block_tags, const int32_t *used, int32_t batch,
+                      int32_t max_pages, int32_t max_moves, int32_t *moved_src, int32_t *moved_dst, int32_t *n_moved,
+                      void *stream) {
+  int rc = check_cache(cache);
+  if (rc) return rc;
+  if (!state || !page_tags || !n_moved) return PFKV_ERR_NULL;
+  if (batch < 0 || max_pages < 1 || max_moves < 0 || (uint64_t)batch * (uint64_t)max_pages > (1ull << 40))
+    return PFKV_ERR_SHAPE;
+  if (!aligned256(state)) return PFKV_ERR_ALIGN;
+  if (batch > 0 && !block_table) return PFKV_ERR_NULL;
+  if (max_moves > 0 && (!moved_src || !moved_dst)) return PFKV_ERR_NULL;
+  return launch_page_compact(state, page_tags, page_refs, *cache, block_table, block_tags, used, batch, max_pages,
+                             max_moves, moved_src, moved_dst, n_moved, static_cast<cudaStream_t>(stream));
+}
+
 int pfkv_calibrate_scales(const void *rows, int64_t n_rows, int32_t num_heads, int32_t head_dim, float *scale,
                           void *stream) {
   if (n_rows < 0 || num_heads < 1 || head_dim < 1 || num_heads > 65535) return PFKV_ERR_SHAPE;

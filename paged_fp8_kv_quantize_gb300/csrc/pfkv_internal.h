@@ -98,6 +98,15 @@ int launch_page_alloc(void *state, uint32_t *page_tags, int n, int *pages_out, u
 int launch_page_free(void *state, const int *pages, int n, uint32_t *page_status, cudaStream_t s);
 int launch_page_realloc(void *state, uint32_t *page_tags, const int *pages, int n, uint32_t *tags_out,
                         uint32_t *page_status, cudaStream_t s);
+int launch_page_copy(const pfkv_cache &c, const int *src_pages, const int *dst_pages, const int *slots, int n_pages,
+                     uint32_t *page_status, cudaStream_t s);
+int launch_page_fork(void *state, uint32_t *page_tags, int *page_refs, const pfkv_cache &c, const int *parents,
+                     const int *children, const int *lens, int n, int *block_table, uint32_t *block_tags, int batch,
+                     int max_pages, uint32_t flags, uint32_t *status, cudaStream_t s);
+int launch_page_release(void *state, int *page_refs, const int *pages, int n, uint32_t *page_status, cudaStream_t s);
+int launch_page_compact(void *state, uint32_t *page_tags, int *page_refs, const pfkv_cache &c, int *block_table,
+                        uint32_t *block_tags, const int *used, int batch, int max_pages, int max_moves,
+                        int *moved_src, int *moved_dst, int *n_moved, cudaStream_t s);
 int launch_calibrate(const void *rows, int64_t n_rows, int heads, int dim, float *scale, cudaStream_t s);
 int launch_encode(const float *x, uint8_t *codes, int64_t n, cudaStream_t s);
 
@@ -109,6 +118,24 @@ int decode_precheck(int want_dtype, const pfkv_cache *c, int32_t Hq, int32_t bat
 int cuda_fail(cudaError_t e, const char *where);
 inline int cuda_ok(cudaError_t e, const char *where = "kernel launch") {
   return e == cudaSuccess ? PFKV_OK : cuda_fail(e, where);
+}
+
+// Launches kern as a programmatic dependent of the stream's previous kernel:
+// it may be scheduled while that one drains, and waits for it to finish
+// (griddepcontrol.wait) before it touches memory.
+template <typename Kern, typename... Args>
+cudaError_t launch_dependent(Kern kern, dim3 grid, int threads, size_t smem, cudaStream_t s, Args... args) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
 }  // namespace pfkv
