@@ -69,7 +69,11 @@ enum {
   PFKV_ST_NOT_HELD = 32u, /* page allocator: the page is not handed out   */
   PFKV_ST_DUPLICATE = 64u, /* page allocator: id listed twice in one call;
                               fork: the child is made or forked from twice  */
-  PFKV_ST_BAD_ROW = 128u  /* fork: a row outside the block table           */
+  PFKV_ST_BAD_ROW = 128u, /* fork: a row outside the block table           */
+  PFKV_ST_BAD_GROUP = 256u,     /* shared prefix: no such group, or its
+                                   prefix does not fit the table           */
+  PFKV_ST_PREFIX_DIFFERS = 512u /* shared prefix: a page that is not the
+                                   group's                                 */
 };
 
 /* Return codes. */
@@ -257,6 +261,60 @@ int pfkv_paged_decode_step(const pfkv_cache *cache, const void *k_new, const voi
                            const uint32_t *block_tags, int32_t batch, int32_t max_pages, float softmax_scale,
                            uint32_t flags, int32_t max_splits, void *workspace, size_t workspace_bytes, float *out,
                            uint32_t *status, void *stream);
+
+/*
+ * paged_decode_attention_prefix -- single-token decode attention of a batch
+ * in which groups of requests share a long prefix (a system prompt, a
+ * document, the samples of one prompt): the pages that a group shares are
+ * read once for all its requests, their query rows together as one matrix,
+ * and each request's own pages as by paged_decode_attention.  The result is
+ * that of paged_decode_attention on the same tables; pfkv_page_fork makes
+ * such tables.
+ *   prefix_group : int32 [batch], the request's group in [0, n_groups), or -1
+ *                  for a request without one; the requests of a group may
+ *                  stand anywhere in the batch
+ *   prefix_pages : int32 [n_groups], whole pages that a group shares: the
+ *                  first prefix_pages[g] entries of its requests' rows of
+ *                  block_table are the same ids (0: none)
+ *   k_new, v_new : bf16 [batch][num_kv_heads][head_dim], or both NULL.  Given,
+ *                  request b's new token is written to position
+ *                  seq_lens[b] - 1 first, as by paged_decode_step; that
+ *                  position must lie past the prefix.
+ *   out          : [batch][num_q_heads][head_dim], fp32 or bf16 (out_dtype,
+ *                  PFKV_OUT_*).  fp32 keeps what paged_decode_attention does
+ *                  (probabilities carried to about 22 bits); a bf16 output
+ *                  carries them to 11 (FP8 cache) or 16 (BF16 cache) bits,
+ *                  below its own rounding.
+ *   workspace    : pfkv_prefix_workspace_bytes(cache, batch, num_q_heads,
+ *                  n_groups, max_splits) bytes, 256-byte aligned
+ *   status[b]    : that of paged_decode_attention, and
+ *     BAD_GROUP      prefix_group[b] outside [-1, n_groups), or its
+ *                    prefix_pages outside [0, max_pages]
+ *     BAD_LEN        also a length below the prefix, or (with k_new) a new
+ *                    token inside it
+ *     PREFIX_DIFFERS an entry of the prefix is another page than the group's
+ *                    first request (in batch order) has there
+ *   As elsewhere, a request with a data fault gets zeros and does not touch
+ *   the others of its group.
+ * The other arguments are those of paged_decode_attention.  Supported: its
+ * grouped-query shapes (head_dim 64 or 128, FP8 with either scale mode, or
+ * BF16) with up to 4096 groups.  The latent stream is not
+ * (PFKV_ERR_UNSUPPORTED): its decode is bound by its products, which sharing
+ * does not lessen.  batch * num_q_heads may not reach 2^31 (PFKV_ERR_SHAPE).
+ */
+enum { PFKV_OUT_FP32 = 0, PFKV_OUT_BF16 = 1 };
+
+/* Host-only; SIZE_MAX for sizes a call would refuse. */
+size_t pfkv_prefix_workspace_bytes(const pfkv_cache *cache, int32_t batch, int32_t num_q_heads, int32_t n_groups,
+                                   int32_t max_splits);
+
+int pfkv_paged_decode_attention_prefix(const pfkv_cache *cache, const void *k_new, const void *v_new, const void *q,
+                                       int32_t num_q_heads, const int32_t *seq_lens, const int32_t *block_table,
+                                       const uint32_t *block_tags, int32_t batch, int32_t max_pages,
+                                       const int32_t *prefix_group, const int32_t *prefix_pages, int32_t n_groups,
+                                       float softmax_scale, uint32_t flags, int32_t max_splits, void *workspace,
+                                       size_t workspace_bytes, void *out, int32_t out_dtype, uint32_t *status,
+                                       void *stream);
 
 /*
  * handoff_bf16_to_fp8 -- quantize whole pages of a BF16 cache into an FP8

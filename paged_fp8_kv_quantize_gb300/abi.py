@@ -29,6 +29,8 @@ ST_NO_PAGES = 16
 ST_NOT_HELD = 32
 ST_DUPLICATE = 64
 ST_BAD_ROW = 128
+ST_BAD_GROUP = 256
+ST_PREFIX_DIFFERS = 512
 
 EXPORTS = (
     "pfkv_kv_append_quantize",
@@ -37,6 +39,8 @@ EXPORTS = (
     "pfkv_paged_decode_attention_bf16",
     "pfkv_paged_decode_attention_fp8_noalloc",
     "pfkv_paged_decode_step",
+    "pfkv_prefix_workspace_bytes",
+    "pfkv_paged_decode_attention_prefix",
     "pfkv_handoff_bf16_to_fp8",
     "pfkv_page_allocator_bytes",
     "pfkv_page_allocator_init",
@@ -100,6 +104,11 @@ def _load():
     L.pfkv_paged_decode_step.restype = ctypes.c_int
     L.pfkv_paged_decode_step.argtypes = [cp, P, P, P, i32, P, P, P, i32, i32, ctypes.c_float, u32, i32, P, sz, P, P,
                                          P]
+    L.pfkv_prefix_workspace_bytes.restype = sz
+    L.pfkv_prefix_workspace_bytes.argtypes = [cp, i32, i32, i32, i32]
+    L.pfkv_paged_decode_attention_prefix.restype = ctypes.c_int
+    L.pfkv_paged_decode_attention_prefix.argtypes = [cp, P, P, P, i32, P, P, P, i32, i32, P, P, i32, ctypes.c_float,
+                                                     u32, i32, P, sz, P, i32, P, P]
     L.pfkv_handoff_bf16_to_fp8.restype = ctypes.c_int
     L.pfkv_handoff_bf16_to_fp8.argtypes = [cp, cp, P, P, i32, P, P]
     L.pfkv_page_allocator_bytes.restype = sz
@@ -305,6 +314,52 @@ def paged_decode_step(cache, k_new, v_new, q, seq_lens, block_table, block_tags,
         _ptr(workspace), workspace.numel(), _ptr(_dev(out, "out", torch.float32)),
         _ptr(_dev(status, "status", torch.int32)), _stream(stream))
     _check("pfkv_paged_decode_step", rc)
+    return out, status
+
+
+def prefix_workspace_bytes(cache: PagedCache, batch, num_q_heads, n_groups, max_splits=64) -> int:
+    d = cache.desc()
+    return int(lib.pfkv_prefix_workspace_bytes(ctypes.byref(d), int(batch), int(num_q_heads), int(n_groups),
+                                               int(max_splits)))
+
+
+_OUT_DTYPES = {torch.float32: 0, torch.bfloat16: 1}  # PFKV_OUT_*
+
+
+def paged_decode_attention_prefix(cache, q, seq_lens, block_table, block_tags, prefix_group, prefix_pages,
+                                  softmax_scale, flags=0, max_splits=64, k_new=None, v_new=None, workspace=None,
+                                  out=None, out_dtype=torch.float32, status=None, stream=None):
+    """Decode attention of a batch whose groups share prefixes, each shared page read once
+    (pfkv_paged_decode_attention_prefix).  With k_new / v_new the new tokens are appended first."""
+    B, Hq, D = q.shape
+    MP = block_table.shape[1]
+    n_groups = prefix_pages.numel()
+    dev = q.device
+    if D != cache.D:
+        raise ValueError(f"q must have head_dim {cache.D}, got {D}")
+    if workspace is None:
+        n = prefix_workspace_bytes(cache, B, Hq, n_groups, max_splits)
+        if n >= 1 << 62:
+            raise PfkvError("pfkv_prefix_workspace_bytes", -2)
+        workspace = torch.empty(n, dtype=torch.uint8, device=dev)
+    if out is None:
+        out = torch.empty(B, Hq, cache.Dv, dtype=out_dtype, device=dev)
+    if out.dtype not in _OUT_DTYPES:
+        raise ValueError(f"out must be torch.float32 or torch.bfloat16, got {out.dtype}")
+    if status is None:
+        status = torch.empty(B, dtype=torch.int32, device=dev)
+    rows = B * cache.H * cache.D
+    d = cache.desc()
+    rc = lib.pfkv_paged_decode_attention_prefix(
+        ctypes.byref(d), _ptr(_vec(k_new, "k_new", rows, torch.bfloat16)),
+        _ptr(_vec(v_new, "v_new", rows, torch.bfloat16)), _ptr(_vec(q, "q", B * Hq * D, torch.bfloat16)), Hq,
+        _ptr(_vec(seq_lens, "seq_lens", B)), _ptr(_vec(block_table, "block_table", B * MP)),
+        _ptr(_vec(block_tags, "block_tags", B * MP)), B, MP, _ptr(_vec(prefix_group, "prefix_group", B)),
+        _ptr(_vec(prefix_pages, "prefix_pages", n_groups)), n_groups, float(softmax_scale), int(flags),
+        int(max_splits), _ptr(_dev(workspace, "workspace", torch.uint8)), workspace.numel(),
+        _ptr(_vec(out, "out", B * Hq * D, out.dtype)), _OUT_DTYPES[out.dtype],
+        _ptr(_vec(status, "status", B)), _stream(stream))
+    _check("pfkv_paged_decode_attention_prefix", rc)
     return out, status
 
 

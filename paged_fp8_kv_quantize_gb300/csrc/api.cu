@@ -63,6 +63,7 @@ static bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 
 // any model's; they bound the workspace arithmetic).
 constexpr int kMaxQHeads = 65536;
 constexpr int kMaxHeadDim = 4096;
+constexpr int kMaxPrefixGroups = 4096;  // one shared-memory counter each in the plan
 
 static bool is_latent(const pfkv_cache *c) {
   return c->kv_shared && c->num_kv_heads == 1 && c->head_dim == 576 && c->v_head_dim == 512;
@@ -105,24 +106,39 @@ int decode_precheck(int want_dtype, const pfkv_cache *c, int32_t Hq, int32_t bat
   return PFKV_OK;
 }
 
+// A shared-prefix call's own arguments.
+struct PrefixCall {
+  const int32_t *group_of, *group_pages;
+  int32_t n_groups, out_dtype;
+};
+
 static int decode_common(int want_dtype, const pfkv_cache *c, const void *q, int32_t Hq, const int32_t *seq_lens,
                          const int32_t *block_table, const uint32_t *block_tags, int32_t batch, int32_t max_pages,
                          float softmax_scale, uint32_t flags, int32_t max_splits, void *ws, size_t ws_bytes,
-                         float *out, uint32_t *status, void *stream, const void *k_new = nullptr,
-                         const void *v_new = nullptr) {
+                         void *out, uint32_t *status, void *stream, const void *k_new = nullptr,
+                         const void *v_new = nullptr, const PrefixCall *prefix = nullptr) {
   const int rc = decode_precheck(want_dtype, c, Hq, batch, max_pages, max_splits);
   if (rc) return rc;
   // the kernels' page arithmetic assumes at most 2^40 pages in one call
   if ((uint64_t)batch * (uint64_t)max_pages > (1ull << 40)) return PFKV_ERR_SHAPE;
   if (!isfinite(softmax_scale)) return PFKV_ERR_SHAPE;
+  if (prefix) {
+    if (prefix->out_dtype != PFKV_OUT_FP32 && prefix->out_dtype != PFKV_OUT_BF16) return PFKV_ERR_DTYPE;
+    // the join has a block per (request, query head)
+    if (prefix->n_groups < 0 || (int64_t)batch * Hq > 0x7fffffff) return PFKV_ERR_SHAPE;
+    if (prefix->n_groups > kMaxPrefixGroups || c->kv_shared) return PFKV_ERR_UNSUPPORTED;
+  }
   if (batch == 0) return PFKV_OK;
+  if (prefix && (!prefix->group_of || (prefix->n_groups > 0 && !prefix->group_pages))) return PFKV_ERR_NULL;
   if (!q || !seq_lens || !block_table || !out || !status || !ws) return PFKV_ERR_NULL;
   if ((flags & PFKV_FLAG_TAG_CHECK) && (!c->page_tags || !block_tags)) return PFKV_ERR_NULL;
   if (Hq % c->num_kv_heads) return PFKV_ERR_SHAPE;
   if (!aligned16(q) || !aligned16(out)) return PFKV_ERR_ALIGN;
   if (c->page_size % 16 || c->page_size > 256) return PFKV_ERR_UNSUPPORTED;
   const WsLayout L = ws_layout(batch, Hq, c->v_head_dim, max_splits, is_latent(c));
-  if (ws_bytes < L.total) return PFKV_ERR_WORKSPACE;
+  const size_t need = prefix ? prefix_ws_bytes(L.total, batch, Hq, c->num_kv_heads, c->head_dim, prefix->n_groups)
+                             : L.total;
+  if (ws_bytes < need) return PFKV_ERR_WORKSPACE;
   if ((reinterpret_cast<uintptr_t>(ws) & 255u) != 0) return PFKV_ERR_ALIGN;
 
   DecodeArgs a;
@@ -141,7 +157,7 @@ static int decode_common(int want_dtype, const pfkv_cache *c, const void *q, int
   a.split_count = reinterpret_cast<int *>(w + L.split_count);
   a.part_ml = reinterpret_cast<float2 *>(w + L.part_ml);
   a.part_o = reinterpret_cast<float *>(w + L.part_o);
-  a.out = out; a.status = status;
+  a.out = static_cast<float *>(out); a.status = status;
   a.append = k_new != nullptr;
   a.k_new = static_cast<const uint16_t *>(k_new);
   a.v_new = static_cast<const uint16_t *>(v_new);
@@ -151,6 +167,8 @@ static int decode_common(int want_dtype, const pfkv_cache *c, const void *q, int
   a.min_chunk_pages = 1;
   a.n_ctas = 0;
   a.st_groups = 1;
+  a.skip = nullptr;
+  a.join = 0;
   a.piece_cost = 0;
   a.part_st = reinterpret_cast<uint32_t *>(w + L.part_st);
   a.cta_abort = reinterpret_cast<int *>(w + L.cta_abort);
@@ -165,6 +183,9 @@ static int decode_common(int want_dtype, const pfkv_cache *c, const void *q, int
   }
   if (c->head_dim != 64 && c->head_dim != 128) return PFKV_ERR_UNSUPPORTED;
   if (c->dtype == PFKV_DTYPE_BF16 && c->scale_mode != PFKV_SCALE_PER_HEAD) return PFKV_ERR_SHAPE;
+  if (prefix)
+    return launch_prefix_decode(a, L.total, w, prefix->group_of, prefix->group_pages, prefix->n_groups,
+                                prefix->out_dtype == PFKV_OUT_BF16, s);
   return launch_gqa_decode(a, s);
 }
 
@@ -253,6 +274,32 @@ int pfkv_paged_decode_step(const pfkv_cache *cache, const void *k_new, const voi
   return decode_common(cache->dtype, cache, q, num_q_heads, seq_lens, block_table, block_tags, batch, max_pages,
                        softmax_scale, flags, max_splits, workspace, workspace_bytes, out, status, stream,
                        batch > 0 ? k_new : nullptr, cache->kv_shared ? nullptr : v_new);
+}
+
+size_t pfkv_prefix_workspace_bytes(const pfkv_cache *cache, int32_t batch, int32_t num_q_heads, int32_t n_groups,
+                                   int32_t max_splits) {
+  const size_t n = pfkv_decode_workspace_bytes(cache, batch, num_q_heads, max_splits);
+  if (n == 0 || n == SIZE_MAX || n_groups < 0) return n == SIZE_MAX ? n : 0;
+  if (n_groups > kMaxPrefixGroups || cache->num_kv_heads < 1 || num_q_heads % cache->num_kv_heads ||
+      cache->head_dim < 1 || cache->head_dim > kMaxHeadDim)
+    return SIZE_MAX;
+  return prefix_ws_bytes(n, batch, num_q_heads, cache->num_kv_heads, cache->head_dim, n_groups);
+}
+
+int pfkv_paged_decode_attention_prefix(const pfkv_cache *cache, const void *k_new, const void *v_new, const void *q,
+                                       int32_t num_q_heads, const int32_t *seq_lens, const int32_t *block_table,
+                                       const uint32_t *block_tags, int32_t batch, int32_t max_pages,
+                                       const int32_t *prefix_group, const int32_t *prefix_pages, int32_t n_groups,
+                                       float softmax_scale, uint32_t flags, int32_t max_splits, void *workspace,
+                                       size_t workspace_bytes, void *out, int32_t out_dtype, uint32_t *status,
+                                       void *stream) {
+  if (!cache) return PFKV_ERR_NULL;
+  if (!k_new != !v_new) return PFKV_ERR_NULL;  // both or neither
+  if (k_new && (!aligned16(k_new) || !aligned16(v_new))) return PFKV_ERR_ALIGN;
+  const PrefixCall p{prefix_group, prefix_pages, n_groups, out_dtype};
+  return decode_common(cache->dtype, cache, q, num_q_heads, seq_lens, block_table, block_tags, batch, max_pages,
+                       softmax_scale, flags, max_splits, workspace, workspace_bytes, out, status, stream, k_new,
+                       v_new, &p);
 }
 
 int pfkv_handoff_bf16_to_fp8(const pfkv_cache *src, const pfkv_cache *dst, const int32_t *src_pages,

@@ -241,8 +241,9 @@ __global__ void __launch_bounds__(Cfg<kFp8, kD, kG, kNCW>::kThreads, Cfg<kFp8, k
           a.split_count[b] = cur.nb;
         }
       }
-      const int *trow = a.block_table + (size_t)b * a.MP;
-      const uint32_t *tagrow = a.block_tags + (size_t)b * a.MP;
+      const size_t row0 = (size_t)b * a.MP + (a.skip ? __ldg(&a.skip[b]) : 0);
+      const int *trow = a.block_table + row0;
+      const uint32_t *tagrow = a.block_tags + row0;
       uint32_t st_bits = 0;
       // Decode step: the item holding the request's last page writes the new
       // token's K and V rows of head g into that page before copying it.
@@ -562,8 +563,8 @@ __global__ void __launch_bounds__(Cfg<kFp8, kD, kG, kNCW>::kThreads, Cfg<kFp8, k
           if (per_token) {
             const uint32_t svs = smem_base + stg[t] * sp.stage_bytes + 2 * S * C::kRowBytes + 4 * S +
                                  4 * ((tok_base[t] - (tok_base[t] / S) * S) + gid);
-            vs0 = lds_f32(svs);
-            vs1 = lds_f32(svs + 32);
+            vs0 = tok_base[t] + gid < d.L ? lds_f32(svs) : 0.f;
+            vs1 = tok_base[t] + gid + 8 < d.L ? lds_f32(svs + 32) : 0.f;
           }
           uint32_t pb[C::kNP][2];
 #pragma unroll
@@ -595,6 +596,15 @@ __global__ void __launch_bounds__(Cfg<kFp8, kD, kG, kNCW>::kThreads, Cfg<kFp8, k
                 wv[r][4 * c] = v.x; wv[r][4 * c + 1] = v.y; wv[r][4 * c + 2] = v.z; wv[r][4 * c + 3] = v.w;
               }
             }
+          }
+          // slots past the length hold anything, NaN among it, and a weight of
+          // zero does not silence that
+          if (tok_base[t] + 16 > d.L) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+              if (tok_base[t] + 2 * tq + (r & 1) + 8 * (r >> 1) >= d.L)
+#pragma unroll
+                for (int c = 0; c < C::kSegV / 4; ++c) wv[r][c] = 0u;
           }
 #pragma unroll
           for (int mt = 0; mt < C::kKsteps; ++mt) {
@@ -685,7 +695,7 @@ __global__ void __launch_bounds__(Cfg<kFp8, kD, kG, kNCW>::kThreads, Cfg<kFp8, k
       float ofac = 1.f;
       if constexpr (kFp8) ofac = (per_token ? 1.f : __ldg(&a.v_scale[hg.kv])) / C::kPScale;
       float *out_bg = a.out + ((size_t)d.b * a.Hq + hg.first) * kD;  // rows of this (request, head group)
-      if (d.nb == 1) {
+      if (d.nb == 1 && !a.join) {
         // the item covers the whole request: finish it here
         for (int idx = t; idx < hg.count * kD; idx += kCT) {
           const int jh = idx / kD, dd = idx - jh * kD;
@@ -768,9 +778,8 @@ struct SplitShape {
 };
 
 template <bool kFp8, int kD, int kG>
-int run_split(const DecodeArgs &a_in, cudaStream_t s, const CUtensorMap &mk, const CUtensorMap &mv) {
+int run_split(DecodeArgs &a, cudaStream_t s, const CUtensorMap &mk, const CUtensorMap &mv) {
   using C = Cfg<kFp8, kD, kG, kNCW>;
-  DecodeArgs a = a_in;
   const bool per_token = kFp8 && a.scale_mode == PFKV_SCALE_PER_TOKEN;
   auto kern = gqa_split_kernel<kFp8, kD, kG, kNCW>;
   static SplitShape cache[4];
@@ -838,7 +847,7 @@ int run_split(const DecodeArgs &a_in, cudaStream_t s, const CUtensorMap &mk, con
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   int rc = cuda_ok(cudaLaunchKernelEx(&cfg, kern, mk, mv, a, sh.nst), "split kernel launch");
-  if (rc) return rc;
+  if (rc || a.join) return rc;
   // the narrow merge shape when the wide one would give fewer than two
   // blocks per SM (a few requests, many pieces each)
   const bool narrow = (long long)a.B * a.Hkv * merge_col_blocks<kD, kG>() < 2LL * num_sms();
@@ -861,8 +870,7 @@ int run_split(const DecodeArgs &a_in, cudaStream_t s, const CUtensorMap &mk, con
 // head slots; a group of Gs heads takes the next of these and leaves the
 // other slots as zero-query padding whose results are never written.
 template <bool kFp8, int kD>
-int dispatch_g(const DecodeArgs &a_in, cudaStream_t s, const CUtensorMap &mk, const CUtensorMap &mv) {
-  DecodeArgs a = a_in;
+int dispatch_g(DecodeArgs &a, cudaStream_t s, const CUtensorMap &mk, const CUtensorMap &mv) {
   a.kv_sub = (a.G + 7) / 8;
   a.Gs = (a.G + a.kv_sub - 1) / a.kv_sub;
   if ((long long)a.Hkv * a.kv_sub > kMaxCtas) return PFKV_ERR_UNSUPPORTED;
@@ -878,7 +886,7 @@ int dispatch_g(const DecodeArgs &a_in, cudaStream_t s, const CUtensorMap &mk, co
 
 }  // namespace
 
-int launch_gqa_decode(const DecodeArgs &a, cudaStream_t s) {
+int launch_gqa_split(DecodeArgs &a, cudaStream_t s) {
   CUtensorMap mk, mv;
   int rc = make_pool_map(&mk, a.k_pool, a.dtype, a.D, a.S, a.Hkv, a.P);
   if (rc) return rc;
@@ -888,6 +896,11 @@ int launch_gqa_decode(const DecodeArgs &a, cudaStream_t s) {
   if (a.D == 128) return fp8 ? dispatch_g<true, 128>(a, s, mk, mv) : dispatch_g<false, 128>(a, s, mk, mv);
   if (a.D == 64) return fp8 ? dispatch_g<true, 64>(a, s, mk, mv) : dispatch_g<false, 64>(a, s, mk, mv);
   return PFKV_ERR_UNSUPPORTED;
+}
+
+int launch_gqa_decode(const DecodeArgs &a, cudaStream_t s) {
+  DecodeArgs own = a;
+  return launch_gqa_split(own, s);
 }
 
 }  // namespace pfkv

@@ -70,6 +70,12 @@ struct DecodeArgs {
   // latent-stream path: the query terms and per-head factors (see ws_layout)
   uint8_t *qterms;
   float *qfac;
+  // Shared-prefix decode: request b's pages begin at table entry skip[b], and
+  // seq_lens counts the tokens from there on (NULL: 0).  join: every piece
+  // leaves a partial result (a one-piece request is not finished in the split
+  // kernel), and the caller's own kernel merges.
+  const int *skip;
+  int join;
   int piece_cost;  // cut rule: pages' worth of time one piece costs beyond its pages
   uint32_t *part_st;
   int *cta_abort;
@@ -85,6 +91,11 @@ int num_sms();
 
 // launchers (return PFKV_* codes)
 int launch_gqa_decode(const DecodeArgs &a, cudaStream_t s);
+// The split kernel alone (join must be set); fills in the launch's n_ctas and st_groups.
+int launch_gqa_split(DecodeArgs &a, cudaStream_t s);
+size_t prefix_ws_bytes(size_t first, int batch, int q_heads, int kv_heads, int dim, int n_groups);
+int launch_prefix_decode(const DecodeArgs &d, size_t ws_first, uint8_t *ws, const int *group_of,
+                         const int *group_pages, int n_groups, int out_bf16, cudaStream_t s);
 int launch_latent_decode(const DecodeArgs &a, cudaStream_t s);
 int launch_append(const pfkv_cache &c, const void *k_new, const void *v_new, int n_rows, const int *row_req,
                   const int *positions, const int *block_table, const uint32_t *block_tags, int batch,

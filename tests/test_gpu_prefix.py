@@ -1,0 +1,319 @@
+"""Shared-prefix decode attention against the fp64 oracle, which knows nothing
+of groups: every request by itself over its whole table."""
+import numpy as np
+import pytest
+import torch
+
+from gpu_helpers import dev_bf16, dev_i32
+from paged_fp8_kv_quantize_gb300 import abi, synth
+from prefix_helpers import BF16, FP8, FP8_TOKEN, PrefixCase
+
+pytestmark = pytest.mark.gpu
+
+OUT = {"fp32": torch.float32, "bf16": torch.bfloat16}
+
+
+@pytest.mark.parametrize("out", list(OUT))
+@pytest.mark.parametrize("cache", [FP8, FP8_TOKEN, BF16])
+@pytest.mark.parametrize("dim", [64, 128])
+def test_types(cache, dim, out):
+    """Members scattered over the batch, a request of its own, a group without
+    a prefix, one without members, one with a single request."""
+    c = PrefixCase(1, [0, 2, -1, 0, 1, 0, 4, 2], [5, 0, 11, 3, 2], [1, 17, 40, 16, 33, 90, 5, 300], q_heads=8,
+                   kv_heads=2, dim=dim, page=16, cache=cache)
+    c.assert_matches(OUT[out], abi.FLAG_TAG_CHECK)
+
+
+@pytest.mark.parametrize("q_heads,kv_heads", [(1, 1), (3, 3), (8, 4), (9, 3), (20, 4), (14, 2), (16, 2), (32, 2), (24, 1)])
+def test_head_layouts(q_heads, kv_heads):
+    c = PrefixCase(2, [0] * 7 + [1] * 3, [9, 4], [3, 50, 1, 16, 15, 17, 200, 8, 31, 64], q_heads=q_heads,
+                   kv_heads=kv_heads, dim=64, page=16)
+    c.assert_matches()
+
+
+@pytest.mark.parametrize("page", [16, 48, 64, 112, 256])
+@pytest.mark.parametrize("pages", [1, 3, 20])
+def test_page_sizes(page, pages):
+    c = PrefixCase(3, [0, 0, 1, 0], [pages, 1], [1, page, page + 1, 2 * page - 1], q_heads=8, kv_heads=2, dim=128,
+                   page=page, cache=FP8_TOKEN)
+    c.assert_matches(flags=abi.FLAG_TAG_CHECK)
+
+
+@pytest.mark.parametrize("members", [1, 2, 15, 16, 17, 31, 32, 33, 63, 64, 65, 130])
+def test_row_counts(members):
+    """Rows on both sides of the row block's and the instruction's edges."""
+    c = PrefixCase(4, [0] * members, [13], [1 + 7 * (i % 5) for i in range(members)], q_heads=16, kv_heads=2, dim=64,
+                   page=16)
+    c.assert_matches()
+
+
+@pytest.mark.parametrize("cache,out", [(FP8, "fp32"), (FP8, "bf16"), (FP8_TOKEN, "fp32"), (BF16, "fp32"), (BF16, "bf16")])
+def test_long_prefix_in_many_pieces(cache, out):
+    """A prefix that every CTA takes a part of; a peaked softmax."""
+    c = PrefixCase(5, [0] * 20 + [1] * 5, [700, 90], [1 + 37 * i for i in range(25)], q_heads=16, kv_heads=2, dim=128,
+                   page=16, cache=cache, spread=4.0)
+    c.assert_matches(OUT[out])
+
+
+@pytest.mark.parametrize("max_splits", [1, 2, 3, 256])
+def test_split_bounds(max_splits):
+    c = PrefixCase(6, [0, 0, -1, 1], [40, 7], [1, 2000, 900, 17], q_heads=8, kv_heads=2, dim=64, page=16)
+    c.assert_matches(max_splits=max_splits)
+
+
+def test_nothing_shared_and_everything_shared():
+    c = PrefixCase(7, [-1] * 5, [], [1, 16, 100, 33, 7], q_heads=8, kv_heads=2, dim=64, page=16)
+    c.assert_matches(where="no groups")
+    c = PrefixCase(8, [0] * 5, [4], [0] * 5, q_heads=8, kv_heads=2, dim=64, page=16)
+    c.assert_matches(where="no own tokens")
+    c = PrefixCase(9, [0], [1], [0], q_heads=1, kv_heads=1, dim=128, page=16, cache=BF16)
+    c.assert_matches(where="one request, one page")
+    none = abi.paged_decode_attention_prefix(
+        c.device(), torch.empty(0, 1, 128, dtype=torch.bfloat16, device="cuda"), dev_i32(np.zeros(0, np.int32)),
+        dev_i32(np.zeros((0, 3), np.int32)), None, dev_i32(np.zeros(0, np.int32)), dev_i32(c.pages), 0.1)
+    assert none[0].shape == (0, 1, 128)
+
+
+def test_more_groups_than_a_warp_holds():
+    n = 150
+    rng = np.random.default_rng(10)
+    c = PrefixCase(10, rng.integers(-1, n, size=120).tolist(), rng.integers(0, 9, size=n).tolist(),
+                   rng.integers(1, 40, size=120).tolist(), q_heads=4, kv_heads=2, dim=64, page=16)
+    c.assert_matches(flags=abi.FLAG_TAG_CHECK)
+
+
+def test_same_as_the_plain_decode():
+    c = PrefixCase(11, [0] * 9 + [-1], [30], [20 * i + 1 for i in range(10)], q_heads=32, kv_heads=8, dim=128, page=16)
+    got = c.assert_matches()
+    plain, st = abi.paged_decode_attention(c.gpu, dev_bf16(c.q), dev_i32(c.lens), dev_i32(c.table), dev_i32(c.tags),
+                                           c.tau)
+    out, _, mag = c.want()
+    assert ((got - plain).abs().cpu().numpy() <= 2 * c.tolerance(out, mag, torch.float32)).all()
+    again, _ = c.call()
+    assert torch.equal(got, again)  # the same call gives the same bits
+
+
+def test_faults_stay_with_their_requests():
+    group = [0, 0, 0, 0, 0, 1, 1, 1, 2, 2, -2, 3, 0, -1, 9]
+    c = PrefixCase(12, [g if -1 <= g < 3 else -1 for g in group], [6, 4, 5], [20 + i for i in range(15)], q_heads=8,
+                   kv_heads=2, dim=64, page=16)
+    c.group[:] = group
+    c.pages = np.array([6, 4, 5, 99], np.int32)
+    want = np.zeros(15, np.uint32)
+    c.tags[1, 2] ^= 1  # a stale mapping inside the prefix
+    want[1] = abi.ST_STALE_TAG
+    c.table[2, 3] = c.table[6, 2]  # another page than its group's
+    c.tags[2, 3] = c.tags[6, 2]
+    want[2] = abi.ST_PREFIX_DIFFERS
+    c.table[3, 0] = c.P  # outside the pool
+    want[3] = abi.ST_PAGE_OOB | abi.ST_PREFIX_DIFFERS
+    c.lens[4] = 6 * 16 - 1  # ends inside the prefix
+    want[4] = abi.ST_BAD_LEN
+    c.tags[5, 0] ^= 1  # the group's first request itself
+    want[5] = abi.ST_STALE_TAG
+    c.table[7, 4] = -1  # an own page
+    want[7] = abi.ST_PAGE_OOB
+    c.lens[8] = 0
+    want[8] = abi.ST_BAD_LEN
+    want[10] = abi.ST_BAD_GROUP
+    want[11] = abi.ST_BAD_GROUP  # 99 pages do not fit the table
+    c.tags[12, 6] ^= 1  # an own page's stale mapping
+    want[12] = abi.ST_STALE_TAG
+    want[14] = abi.ST_BAD_GROUP
+    got, st = c.call(flags=abi.FLAG_TAG_CHECK)
+    assert st.cpu().numpy().view(np.uint32).tolist() == want.tolist()
+    assert not got[torch.from_numpy(want != 0).cuda()].any()
+    fine = np.flatnonzero(want == 0)
+    out, _, mag = c.want()
+    tol = c.tolerance(out, mag, torch.float32)
+    assert (np.abs(got.cpu().numpy() - out)[fine] <= tol[fine]).all()
+    # the same tables without the tag check
+    _, st = c.call()
+    want[want == abi.ST_STALE_TAG] = 0
+    assert st.cpu().numpy().view(np.uint32).tolist() == want.tolist()
+
+
+def test_first_request_with_a_page_outside_the_pool():
+    """The page is never fetched; the group's other requests have another page there."""
+    c = PrefixCase(13, [0, 0, 0, -1], [3], [5, 6, 7, 8], q_heads=4, kv_heads=1, dim=64, page=16)
+    for bad in (-7, c.P, 2**31 - 1):
+        keep = c.table[0, 1]
+        c.table[0, 1] = bad
+        got, st = c.call()
+        assert st.tolist() == [abi.ST_PAGE_OOB] + [abi.ST_PREFIX_DIFFERS] * 2 + [0]
+        assert not got[:3].any() and got[3].any()
+        c.table[:3, 1] = bad  # all of them
+        _, st = c.call()
+        assert st.tolist() == [abi.ST_PAGE_OOB] * 3 + [0]
+        c.table[:3, 1] = keep
+
+
+@pytest.mark.parametrize("cache,page", [(FP8, 16), (FP8_TOKEN, 32), (BF16, 16)])
+def test_step_appends_then_attends(cache, page):
+    c = PrefixCase(14, [0, 0, -1, 1, 0], [3, 2], [1, page, 2 * page + 3, 40, 0], q_heads=8, kv_heads=2, dim=128,
+                   page=page, cache=cache)
+    k = synth.bf16_bits(c.rng.standard_normal((5, 2, 128), dtype=np.float32))
+    v = synth.bf16_bits(c.rng.standard_normal((5, 2, 128), dtype=np.float32))
+    c.device()
+    got, st = c.call(flags=abi.FLAG_TAG_CHECK, k_new=dev_bf16(k), v_new=dev_bf16(v))
+    assert st.tolist() == [0, 0, 0, 0, abi.ST_BAD_LEN]  # the last one's new token would fall inside the prefix
+    keep = c.lens[4]
+    c.lens[4] = 0
+    pos = np.maximum(c.lens - 1, 0)
+    pos[4] = -1
+    c.ref.append(k, v, pos, c.table, c.tags, flags=abi.FLAG_TAG_CHECK)
+    assert np.array_equal(c.gpu.k_pool.view(torch.uint8).cpu().numpy(), c.ref.k_pool.view(np.uint8))
+    assert np.array_equal(c.gpu.v_pool.view(torch.uint8).cpu().numpy(), c.ref.v_pool.view(np.uint8))
+    if cache == FP8_TOKEN:
+        assert np.array_equal(c.gpu.k_scale.cpu().numpy(), c.ref.k_scale)
+        assert np.array_equal(c.gpu.v_scale.cpu().numpy(), c.ref.v_scale)
+    out, _, mag = c.want(abi.FLAG_TAG_CHECK)
+    c.assert_close(got, out, mag, torch.float32)
+    assert not got[4].any()
+    c.lens[4] = keep
+
+
+def test_slots_past_the_length_do_not_matter():
+    """Unwritten slots of a request's last page hold anything, NaN among it;
+    the plain decode reads the same pages."""
+    for cache in (FP8, FP8_TOKEN, BF16):
+        c = PrefixCase(15, [0, 0, -1, 0], [2], [1, 9, 21, 15], q_heads=8, kv_heads=2, dim=64, page=16, cache=cache)
+        ref = c.call()[0].clone()
+        for b in range(4):
+            n = int(c.lens[b])
+            p, s = int(c.table[b, (n - 1) // 16]), (n - 1) % 16 + 1
+            for x in (c.gpu.k_rows(), c.gpu.v_rows()):
+                if cache == BF16:
+                    x[p, :, s:] = float("nan")
+                else:
+                    x[p, :, s:] = 0x7F
+            if cache == FP8_TOKEN:
+                for x in (c.gpu.k_scale, c.gpu.v_scale):
+                    x.view(c.P, 2, 16)[p, :, s:] = float("inf")
+        assert torch.equal(c.call()[0], ref), cache
+        plain, _ = abi.paged_decode_attention(c.gpu, dev_bf16(c.q), dev_i32(c.lens), dev_i32(c.table), None, c.tau)
+        assert torch.isfinite(plain).all(), cache
+
+
+def test_captured_and_replayed_with_other_lengths():
+    c = PrefixCase(16, [0, 1, 0, -1, 1, 0], [8, 3], [1, 2, 3, 4, 5, 6], q_heads=8, kv_heads=2, dim=64, page=16, room=60)
+    c.device()
+    a = c.args()
+    ws = torch.empty(abi.prefix_workspace_bytes(c.gpu, 6, 8, 2), dtype=torch.uint8, device="cuda")
+    out = torch.empty(6, 8, 64, device="cuda")
+    st = torch.empty(6, dtype=torch.int32, device="cuda")
+    c.call(**a, workspace=ws, out=out, status=st)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        c.call(**a, workspace=ws, out=out, status=st)
+    for k in (0, 13, 50):
+        c.lens = (c.lens + k).astype(np.int32)
+        a["seq_lens"].copy_(dev_i32(c.lens))
+        ws.fill_(0xEE)  # scratch between calls
+        out.fill_(float("nan"))
+        g.replay()
+        torch.cuda.synchronize()
+        want, _, mag = c.want()
+        assert not st.any()
+        c.assert_close(out, want, mag, torch.float32, k)
+        c.lens = (c.lens - k).astype(np.int32)
+
+
+def test_on_a_side_stream_beside_another_call():
+    """Two calls on two streams with workspaces of their own."""
+    cs = [PrefixCase(17 + i, [0] * 12, [60 + 9 * i], [5 * j + 1 for j in range(12)], q_heads=16, kv_heads=4, dim=128,
+                     page=16) for i in range(2)]
+    want = [c.call()[0].clone() for c in cs]
+    args = [c.args() for c in cs]
+    streams = [torch.cuda.Stream() for _ in cs]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(5):
+        for i, (c, s) in enumerate(zip(cs, streams)):
+            with torch.cuda.stream(s):
+                got[i].append(c.call(**args[i])[0])
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(x, want[i]) for x in got[i])
+
+
+def test_fork_decode_release_together():
+    """One prompt forked into samples that decode a few steps each, reading the
+    prompt's pages once, and are given back: outputs against the oracle, and
+    the pool as it was."""
+    S, H, Hq, D, P, B, MP, n0 = 16, 2, 8, 64, 80, 7, 10, 100
+    rng = np.random.default_rng(30)
+    cache = abi.PagedCache(P, S, H, D)
+    cache.k_scale.fill_(0.01)
+    cache.v_scale.fill_(0.01)
+    alloc = abi.PageAllocator(P)
+    table = torch.full((B, MP), -1, dtype=torch.int32, device="cuda")
+    tags = torch.zeros((B, MP), dtype=torch.int32, device="cuda")
+    pages, ptags, _ = alloc.alloc(-(-n0 // S), cache.page_tags)
+    table[0, : pages.numel()], tags[0, : pages.numel()] = pages, ptags
+
+    def rows(n):
+        return synth.bf16_bits(rng.standard_normal((n, H, D), dtype=np.float32))
+
+    prompt = rows(n0), rows(n0)
+    st = abi.kv_append_quantize(cache, dev_bf16(prompt[0]), dev_bf16(prompt[1]), dev_i32(np.arange(n0)), table, tags,
+                                flags=abi.FLAG_TAG_CHECK, row_req=dev_i32(np.zeros(n0, np.int32)), batch=B)
+    assert not st.any()
+    kids = list(range(1, B))
+    st = alloc.fork(cache, dev_i32(np.zeros(B - 1, np.int32)), dev_i32(np.array(kids)),
+                    dev_i32(np.full(B - 1, n0, np.int32)), table, tags, flags=abi.FLAG_TAG_CHECK)
+    assert not st.any()
+    group, shared = torch.zeros(B, dtype=torch.int32, device="cuda"), dev_i32(np.array([n0 // S]))
+    import oracle
+    import prefix_helpers
+    c = PrefixCase(31, [0] * B, [n0 // S], [n0 % S] * B, q_heads=Hq, kv_heads=H, dim=D, page=S)
+    c.P, c.gpu = P, cache
+    for step in range(20):
+        lens = np.full(B, n0 + step + 1, np.int32)
+        if lens[0] % S == 1:  # a fresh page for each
+            pages, ptags, s1 = alloc.alloc(B, cache.page_tags)
+            assert not s1.any()
+            table[:, (lens[0] - 1) // S], tags[:, (lens[0] - 1) // S] = pages, ptags
+        q = synth.bf16_bits(rng.standard_normal((B, Hq, D), dtype=np.float32))
+        out, st = abi.paged_decode_attention_prefix(cache, dev_bf16(q), dev_i32(lens), table, tags, group, shared,
+                                                    0.125, flags=abi.FLAG_TAG_CHECK, k_new=dev_bf16(rows(B)),
+                                                    v_new=dev_bf16(rows(B)))
+        assert not st.any()
+        if step in (0, 11, 12, 19):
+            c.table, c.tags = table.cpu().numpy(), tags.cpu().numpy().view(np.uint32)
+            c.lens, c.q, c.tau = lens, q, 0.125
+            c.ref = oracle.Cache(P, S, H, D, page_tags=cache.page_tags.cpu().numpy().view(np.uint32),
+                                 k_scale=cache.k_scale.cpu().numpy(), v_scale=cache.v_scale.cpu().numpy())
+            c.ref.k_pool[:], c.ref.v_pool[:] = cache.k_pool.cpu().numpy(), cache.v_pool.cpu().numpy()
+            # the codec's NaN codes do not occur in written slots; unwritten ones are not read by the oracle
+            c.ref.k_pool[(c.ref.k_pool & 0x7F) == 0x7F] = 0
+            c.ref.v_pool[(c.ref.v_pool & 0x7F) == 0x7F] = 0
+            want, st_ref, mag = c.want(abi.FLAG_TAG_CHECK)
+            assert not st_ref.any()
+            c.assert_close(out, want, mag, torch.float32, step)
+    used = -(-(n0 + 20) // S)
+    assert not alloc.release(table[1:, :used].reshape(-1).contiguous()).any()
+    assert alloc.free_count() == P - used and not alloc.refs.any()
+    src, dst, n = alloc.compact(cache, table[:1].contiguous(), tags[:1].contiguous())
+    assert not alloc.release(table[0, :used].contiguous() if int(n.item()) == 0 else
+                             torch.arange(used, dtype=torch.int32, device="cuda")).any()
+    assert alloc.free_count() == P
+
+
+def test_wrong_arguments_are_refused():
+    c = PrefixCase(40, [0, 0], [2], [3, 4], q_heads=4, kv_heads=2, dim=64, page=16)
+    c.device()
+    with pytest.raises(ValueError):
+        c.call(prefix_group=dev_i32(np.array([0])))
+    with pytest.raises(ValueError):
+        c.call(out=torch.empty(2, 4, 64, dtype=torch.float16, device="cuda"))
+    with pytest.raises(ValueError):
+        c.call(q=dev_bf16(c.q).transpose(0, 1))
+    with pytest.raises(ValueError):
+        c.call(q=torch.zeros(2, 4, 32, dtype=torch.bfloat16, device="cuda"))
+    with pytest.raises(abi.PfkvError):
+        c.call(workspace=torch.empty(512, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(abi.PfkvError):
+        c.call(k_new=torch.zeros(2, 2, 64, dtype=torch.bfloat16, device="cuda"))
+    with pytest.raises(abi.PfkvError):
+        c.call(block_tags=None, flags=abi.FLAG_TAG_CHECK)

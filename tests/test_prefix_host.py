@@ -1,0 +1,113 @@
+"""CPU-only checks of the shared-prefix decode: refusals before any CUDA call,
+the workspace's size, and the work line restated."""
+import ctypes
+
+import numpy as np
+import pytest
+
+from paged_fp8_kv_quantize_gb300 import abi
+
+SIZE_MAX = ctypes.c_size_t(-1).value
+
+
+def desc(**kw):
+    d = abi.CacheDesc(100, 16, 8, 128, 128, 0, abi.DTYPE_FP8_E4M3, 0, 256, 256, 256, 256, 256)
+    for k, v in kw.items():
+        setattr(d, k, v)
+    return d
+
+
+def call(c=None, k=None, v=None, q=256, hq=32, lens=256, table=256, tags=256, batch=4, mp=8, group=256, pages=256,
+         n_groups=1, scale=1.0, flags=0, splits=64, ws=256, ws_bytes=0, out=256, out_dtype=0, st=256):
+    return abi.lib.pfkv_paged_decode_attention_prefix(
+        None if c is False else ctypes.byref(c or desc()), k, v, q, hq, lens, table, tags, batch, mp, group, pages,
+        n_groups, scale, flags, splits, ws, ws_bytes, out, out_dtype, st, None)
+
+
+def test_refusals():
+    assert call(False) == -1
+    for name in ("q", "lens", "table", "group", "pages", "ws", "out", "st"):
+        assert call(**{name: None}) == -1, name
+    assert call(k=256) == call(v=256) == -1  # both or neither
+    assert call(k=264, v=256) == call(q=8) == -6
+    assert call(tags=None, flags=abi.FLAG_TAG_CHECK) == -1
+    assert call(hq=30) == call(batch=-1) == call(mp=0) == call(splits=0) == call(splits=257) == -2
+    assert call(n_groups=-1) == call(scale=float("inf")) == call(scale=float("nan")) == -2
+    assert call(batch=1 << 20, mp=1 << 21) == -2
+    assert call(batch=1 << 27, hq=32) == -2  # a join block per (request, head)
+    assert call(n_groups=4097) == -3
+    assert call(out_dtype=2) == call(out_dtype=-1) == -4
+    assert call(desc(page_size=24)) == call(desc(page_size=272)) == -3
+    lat = desc(num_kv_heads=1, head_dim=576, v_head_dim=512, kv_shared=1, scale_mode=1, page_size=64)
+    assert call(lat, hq=64) == -3
+    assert call() == -5  # workspace too small
+    assert call(batch=0) == 0
+    big = abi.lib.pfkv_prefix_workspace_bytes(ctypes.byref(desc()), 4, 32, 1, 64)
+    assert call(ws_bytes=big - 1) == -5
+    assert call(ws=264, ws_bytes=big) == -6
+    assert call(desc(head_dim=96, v_head_dim=96), ws_bytes=1 << 40) == -3
+
+
+def test_workspace_bytes():
+    f = abi.lib.pfkv_prefix_workspace_bytes
+    d = desc()
+    plain = abi.lib.pfkv_decode_workspace_bytes(ctypes.byref(d), 64, 32, 64)
+    one = f(ctypes.byref(d), 64, 32, 1, 64)
+    # a slot per range (512 at most) and per row block of a KV head: 256 rows of 128 fp32 values and (m, l) at most
+    rows = one - plain
+    assert 512 * 128 * 520 <= rows <= (512 + 8 * (64 * 4 // 128 + 1)) * 256 * 520 + 64 * 1024
+    assert f(ctypes.byref(d), 64, 32, 5, 64) > one
+    assert plain < f(ctypes.byref(d), 64, 32, 0, 64) < plain + 64 * 1024
+    for bad in ((64, 33, 1, 64), (64, 32, 4097, 64), (64, 32, 1, 300)):
+        assert f(ctypes.byref(d), *bad) == SIZE_MAX, bad
+    assert f(None, 64, 32, 1, 64) == 0 and f(ctypes.byref(d), 64, 32, -1, 64) == 0
+
+
+def line(groups, H, G, rows, ctas, min_pages):
+    """The plan restated: [(members, pages)] -> (T, R, per group (pages, first item, first unit, row blocks))."""
+    unit = item = 0
+    out = []
+    for n, p in groups:
+        p = p if n else 0
+        blocks = -(-n * G // rows)
+        out.append((p, item, unit, blocks))
+        items = H * blocks if p else 0
+        item += items
+        unit += items * p
+    return unit, min(-(-unit // min_pages), ctas), out, item
+
+
+@pytest.mark.parametrize("seed", range(40))
+def test_work_line_covers_every_item_once(seed):
+    """Pieces of the ranges, as the prefix kernel walks them, against the
+    slots that the join looks for: every page of every item once, distinct
+    slots inside the workspace, and the join's range of pieces is the walk's."""
+    rng = np.random.default_rng(seed)
+    H, G, rows = int(rng.integers(1, 9)), int(rng.integers(1, 17)), int(rng.choice([128, 256]))
+    groups = [(int(rng.integers(0, 70)), int(rng.integers(0, 300))) for _ in range(int(rng.integers(1, 12)))]
+    T, R, g, items = line(groups, H, G, rows, int(rng.choice([1, 7, 152, 512])), int(rng.choice([1, 4, 16])))
+    if T == 0:
+        assert R == 0
+        return
+    seen, slots = {}, set()
+    for k in range(R):
+        u, u1 = k * T // R, (k + 1) * T // R
+        while u < u1:
+            lo = max(i for i, x in enumerate(g) if x[2] <= u)
+            p, item0, unit0, blocks = g[lo]
+            it, p0 = divmod(u - unit0, p)
+            p1 = min(p, p0 + u1 - u)
+            assert it < H * blocks
+            seen.setdefault((lo, it), []).append((p0, p1, k, k + item0 + it))
+            assert k + item0 + it not in slots
+            slots.add(k + item0 + it)
+            u += p1 - p0
+    for i, (p, item0, unit0, blocks) in enumerate(g):
+        for it in range(H * blocks if p else 0):
+            pieces = seen.pop((i, it))
+            assert [x[0] for x in pieces] == [0] + [x[1] for x in pieces[:-1]] and pieces[-1][1] == p
+            first = unit0 + it * p
+            k0, k1 = ((first + 1) * R - 1) // T, ((first + p) * R - 1) // T
+            assert [x[2] for x in pieces] == list(range(k0, k1 + 1))
+            assert [x[3] for x in pieces] == [k + item0 + it for k in range(k0, k1 + 1)]
+    assert not seen and max(slots) < R + items - 1 + 1
