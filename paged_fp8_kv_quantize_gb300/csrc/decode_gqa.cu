@@ -134,6 +134,20 @@ __device__ __forceinline__ void drain_wait_full(uint64_t *bar, uint32_t parity) 
     if (global_timer_ns() - t0 > kWaitLimitNs) return;
 }
 
+// Slots past a request's length hold anything, NaN among it, which a weight of
+// zero does not silence: zeros over rows first .. 15 of a 16-row V tile in
+// shared memory (and their scales, where scales is not 0).  Whole warp; once
+// per request and head, so kept out of the consumers' code and registers.
+__device__ __noinline__ void clear_dead_rows(uint32_t tile, int row_bytes, bool swz, int first, uint32_t scales) {
+  const int lane = threadIdx.x & 31;
+  for (int off = first * row_bytes + 16 * lane; off < 16 * row_bytes; off += 512)
+    sts128(tile + (swz ? swz128((uint32_t)off) : (uint32_t)off), make_uint4(0u, 0u, 0u, 0u));
+  if (scales && lane >= first && lane < 16)
+    asm volatile("st.shared.f32 [%0], %1;" ::"r"(scales + 4 * lane), "f"(0.f) : "memory");
+  fence_async_smem();  // the ring entry's next copy comes after these stores
+  __syncwarp();
+}
+
 template <bool kFp8, int kD, int kG, int kNCW>
 __global__ void __launch_bounds__(Cfg<kFp8, kD, kG, kNCW>::kThreads, Cfg<kFp8, kD, kG, kNCW>::kMinBlocks)
     gqa_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
@@ -467,6 +481,11 @@ __global__ void __launch_bounds__(Cfg<kFp8, kD, kG, kNCW>::kThreads, Cfg<kFp8, k
           tok_base[t] = (d.p0 + page_local) * S + mt_in_page * 16;
           live[t] = valid[t] && tok_base[t] < d.L;
           tbase[t] = smem_base + stg[t] * sp.stage_bytes + (uint32_t)(mt_in_page * 16 * C::kRowBytes);
+          if (live[t] && tok_base[t] + 16 > d.L && alive)
+            clear_dead_rows(tbase[t] + S * C::kRowBytes, C::kRowBytes, C::kSwz, d.L - tok_base[t],
+                            per_token ? smem_base + stg[t] * sp.stage_bytes + 2 * S * C::kRowBytes + 4 * S +
+                                            4 * (mt_in_page * 16)
+                                      : 0u);
         }
         alive = __all_sync(0xffffffffu, alive);  // the whole warp leaves together
         if (!alive) break;
@@ -563,8 +582,8 @@ __global__ void __launch_bounds__(Cfg<kFp8, kD, kG, kNCW>::kThreads, Cfg<kFp8, k
           if (per_token) {
             const uint32_t svs = smem_base + stg[t] * sp.stage_bytes + 2 * S * C::kRowBytes + 4 * S +
                                  4 * ((tok_base[t] - (tok_base[t] / S) * S) + gid);
-            vs0 = tok_base[t] + gid < d.L ? lds_f32(svs) : 0.f;
-            vs1 = tok_base[t] + gid + 8 < d.L ? lds_f32(svs + 32) : 0.f;
+            vs0 = lds_f32(svs);
+            vs1 = lds_f32(svs + 32);
           }
           uint32_t pb[C::kNP][2];
 #pragma unroll
@@ -596,15 +615,6 @@ __global__ void __launch_bounds__(Cfg<kFp8, kD, kG, kNCW>::kThreads, Cfg<kFp8, k
                 wv[r][4 * c] = v.x; wv[r][4 * c + 1] = v.y; wv[r][4 * c + 2] = v.z; wv[r][4 * c + 3] = v.w;
               }
             }
-          }
-          // slots past the length hold anything, NaN among it, and a weight of
-          // zero does not silence that
-          if (tok_base[t] + 16 > d.L) {
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-              if (tok_base[t] + 2 * tq + (r & 1) + 8 * (r >> 1) >= d.L)
-#pragma unroll
-                for (int c = 0; c < C::kSegV / 4; ++c) wv[r][c] = 0u;
           }
 #pragma unroll
           for (int mt = 0; mt < C::kKsteps; ++mt) {

@@ -19,7 +19,8 @@
 namespace pfkv {
 namespace {
 
-constexpr int kMaxRanges = 512;  // CTAs of the prefix kernel at most
+constexpr int kMaxRanges = 256;  // CTAs of the prefix kernel at most
+constexpr int kRows = 256;       // query rows of an item
 
 struct PrefixGroup {
   int first, n;      // its requests: members[first .. first + n)
@@ -56,9 +57,8 @@ __device__ __forceinline__ long long range_start(const PrefixHdr &h, long long k
 // The range that holds page u.
 __device__ __forceinline__ int range_of(const PrefixHdr &h, long long u) { return (int)(((u + 1) * h.R - 1) / h.T); }
 
-__device__ __forceinline__ int row_blocks(int n, int G, int rows) {
-  return (int)(((long long)n * G + rows - 1) / rows);
-}
+// Blocks of kRows rows that n requests' query rows of one KV head make.
+__device__ __forceinline__ int row_blocks(int n, int G) { return (int)(((long long)n * G + kRows - 1) / kRows); }
 
 }  // namespace
 }  // namespace pfkv

@@ -1,0 +1,684 @@
+// prefix_kernel.cuh -- the groups' query rows against their shared pages, on
+// the fifth-generation tensor cores (kernel 2 of prefix_attn.cu).
+//
+// One item is up to 256 query rows of one (group, KV head) over the group's
+// pages, a piece a range of those pages; per tile of kTok tokens
+//   S = Q K^T   (M = 128 rows, N = kTok, fp32 in tensor memory)
+//   P = 2^(tau log2(e) S - m)
+//   O += P V    (M = 128, N = head_dim; P from tensor memory)
+// with 16-bit operands (f16 for an FP8 cache, whose codes convert exactly,
+// bf16 for a BF16 one).  A probability is carried as kTerms 16-bit terms, each
+// the rounding of what the terms before it leave; see prefix_attn.cu for how
+// many a call takes.
+//
+// What bounds it: a KV byte of an FP8 cache meets 2 x rows products, so from
+// about 150 rows on the tensor cores, not HBM.  Per tile of 128 tokens and 256
+// rows (head_dim 128, one term) the products are 2048 cycles of one SM; the
+// exponentials 1024 to 2048 and the shared-memory traffic (operand reads 1536,
+// converted tiles 512) have to hide behind them.  Hence: one CTA per SM, and
+//   warps 0-3, 4-7  softmax of row half 0 and 1: a thread owns a row, so that
+//                   maxima and sums need no exchange; P overwrites S.
+//   warps 8-11      loaders.  FP8: 16-byte loads into registers one tile
+//                   ahead, e4m3 -> f16 once per CTA, stored in the operands'
+//                   128-byte-swizzled layout.  BF16: asynchronous copies two
+//                   tiles ahead.  Ring of four tiles (K, V, K, V).
+//   warp 12         issues the MMAs.  The two halves alternate, so that one
+//                   half's products run while the other's softmax does.
+// An item of more than 128 rows has 128 in each half, over the same tokens.
+// One of at most 128 rows gives both halves the same rows and alternate tiles
+// of the tokens; each half then leaves a partial result of its own.
+//
+// The running maximum m of a row moves only when a 64-token chunk exceeds it by
+// more than 2^8 (log2 units: 8), which after the first chunk is rare; O is then
+// rescaled in tensor memory by the row's own softmax warp, after the products
+// it has handed over and before the next.  Probabilities are carried with a
+// factor 2^kShift, so that those down to 2^-21 of the reference stay normal in
+// f16; l has the same factor, so the quotient does not see it.
+#pragma once
+
+#include "prefix.cuh"
+
+namespace pfkv {
+namespace {
+
+constexpr int kPThreads = 13 * 32;
+constexpr int kSlots = 4;        // tiles in the ring: K, V, K, V
+constexpr int kScaleSlots = 4;   // tiles whose per-token scales are kept
+constexpr float kGrow = 8.f;     // growth of a row's maximum that moves its reference
+
+template <bool kFp8, int kD, int kTerms>
+struct PCfg {
+  static constexpr int kTok = kTerms == 3 ? 64 : 128;  // tokens per tile (tensor memory bounds it)
+  static constexpr int kChunks = kTok / 64;
+  static constexpr uint32_t kBlkQ = 128 * 128;          // 64 dims of a query half
+  static constexpr uint32_t kQBytes = kBlkQ * (kD / 64);
+  static constexpr uint32_t kBlkT = kTok * 128;         // 64 dims of a tile
+  static constexpr uint32_t kTBytes = kBlkT * (kD / 64);
+  // tensor memory columns: S (and P over it), the third term, O
+  static constexpr uint32_t kColS = 0, kColX = 2 * kTok, kColO = 256;
+  // per-token mode: v scales relative to a running reference, at most twice it
+  static constexpr float kShift = kFp8 ? 6.f : 0.f;
+  static constexpr uint32_t kOffQ = 0, kOffT = 2 * kQBytes, kOffScale = kOffT + kSlots * kTBytes;
+  static constexpr uint32_t kOffBars = kOffScale + kScaleSlots * (2 * kTok * 4 + 16);
+  static constexpr uint32_t kTotal = kOffBars + 8 * 32 + 32 + 1024;
+  static constexpr uint32_t kIdQK = umma_idesc_f16(128, kTok, !kFp8, 0, 0);
+  static constexpr uint32_t kIdPV = umma_idesc_f16(128, kD, !kFp8, 0, 1);
+  static_assert(kTotal <= 232448, "shared memory plan exceeds one SM");
+};
+
+// One piece of work, as every role works it out.
+struct PItem {
+  int first, row0, n_rows, h, p0, p1;
+  long long slot;
+  bool split;  // at most 128 rows: the halves take alternate tiles
+};
+
+struct PWalk {
+  long long u, u1;
+  int k;
+};
+
+__device__ __forceinline__ bool walk_next(const PrefixArgs &a, PWalk &w, PItem &it) {
+  if (w.u >= w.u1) return false;
+  int lo = 0, hi = a.n_groups - 1;  // the last group that starts at or before u
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (a.groups[mid].unit0 <= w.u) lo = mid;
+    else hi = mid - 1;
+  }
+  const PrefixGroup g = a.groups[lo];
+  const int item = (int)((w.u - g.unit0) / g.pages);
+  const int mb = row_blocks(g.n, a.G);
+  it.first = g.first;
+  it.p0 = (int)(w.u - g.unit0 - (long long)item * g.pages);
+  it.p1 = (int)(w.u1 - w.u < g.pages - it.p0 ? it.p0 + (w.u1 - w.u) : g.pages);
+  it.h = item / mb;
+  it.row0 = (item - it.h * mb) * kRows;
+  it.n_rows = min(kRows, g.n * a.G - it.row0);
+  it.slot = (long long)w.k + g.item0 + item;
+  it.split = it.n_rows <= kRows / 2;
+  w.u += it.p1 - it.p0;
+  return true;
+}
+
+struct PBars {
+  uint64_t *full, *empty;              // ring
+  uint64_t *s_full, *q_ready;          // per half
+  uint64_t *p_full, *pv_done;          // per half and chunk
+  uint64_t *sc_full;                   // per-token scales
+  uint64_t *drain;
+};
+
+__device__ __forceinline__ PBars pbars_at(uint8_t *base) {
+  uint64_t *b = reinterpret_cast<uint64_t *>(base);
+  PBars r;
+  r.full = b; b += kSlots;
+  r.empty = b; b += kSlots;
+  r.s_full = b; b += 2;
+  r.p_full = b; b += 4;
+  r.pv_done = b; b += 4;
+  r.q_ready = b; b += 2;
+  r.sc_full = b; b += kScaleSlots;
+  r.drain = b;
+  return r;
+}
+
+__device__ __forceinline__ bool mbar_wait_warp(uint64_t *bar, uint32_t parity, volatile int *abort) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort));
+}
+
+// ---------------------------------------------------------------- loaders (warps 8-11)
+
+// Per-token scales of tile n: K scales as they are, V scales relative to a
+// running reference vref, which moves when a tile's largest scale exceeds
+// twice it.  Every loader warp reads all of the tile's V scales for their
+// maximum, so that the warps need not meet, and writes its own 32 tokens'.
+template <typename C>
+__device__ __forceinline__ void hand_scales(uint8_t *smem, const PBars &B, uint32_t n, float ks,
+                                            const float (&vs)[C::kTok / 32], float &vref, int t) {
+  float *dst = reinterpret_cast<float *>(smem + C::kOffScale) + (n % kScaleSlots) * (2 * C::kTok + 4);
+  const int lane = t & 31, warp = t >> 5;
+  float mx = vs[0], mine = vs[0];
+#pragma unroll
+  for (int i = 1; i < C::kTok / 32; ++i) {
+    mx = fmaxf(mx, vs[i]);
+    if (i == warp) mine = vs[i];
+  }
+  mx = warp_max_f32(mx);
+  if (mx > 2.f * vref) vref = mx;
+  if (t < C::kTok) {
+    dst[t] = ks;
+    dst[C::kTok + t] = vref > 0.f ? mine / vref : 0.f;
+  }
+  if (t == 0) dst[2 * C::kTok] = vref;
+  __syncwarp();
+  if (lane == 0) mbar_arrive(&B.sc_full[n % kScaleSlots]);
+}
+
+// FP8.  A warp's load covers 16 codes x (8 lanes a row of 128, 4 of 64);
+// iteration i covers tokens 16 i .. 16 i + 15 (D 128) or 32 i .. 32 i + 31.
+template <bool kFp8, int kD, int kTerms>
+__device__ __forceinline__ void loader_fp8(const PrefixArgs &a, uint8_t *smem, const PBars &B, const PrefixHdr &hdr,
+                                           volatile int *abort) {
+  using C = PCfg<kFp8, kD, kTerms>;
+  constexpr int kLanes = kD / 16;                  // lanes a row
+  constexpr int kRowsIt = 128 / kLanes;            // tokens per iteration
+  constexpr int kIt = C::kTok / kRowsIt;
+  const int t = threadIdx.x - 8 * 32, lane = t & 31;
+  const int S = a.d.S, H = a.d.cache.num_kv_heads, c = t % kLanes, r_it = t / kLanes;
+  const bool per_token = a.d.scale_mode == PFKV_SCALE_PER_TOKEN;
+  const uint32_t s_ring = smem_addr(smem + C::kOffT);
+  // Where this thread's 16 values of its row go: two 16-byte chunks, 2c and
+  // 2c + 1.  D 128: lanes 4-7 of a row write them in the other order, so that
+  // eight lanes' stores meet different banks.
+  const bool swap = kD == 128 && (c & 4);
+  const int j0 = 2 * c + (swap ? 1 : 0), j1 = 2 * c + (swap ? 0 : 1);
+  PWalk w{range_start(hdr, blockIdx.x), range_start(hdr, blockIdx.x + 1), (int)blockIdx.x};
+  PItem it;
+  const bool withhold = (a.d.flags & PFKV_FLAG_TEST_WITHHOLD) && blockIdx.x == 0;
+  uint32_t n = 0;  // tiles handed over
+  bool have = walk_next(a, w, it);
+  uint4 kr[kIt], vr[kIt];
+  float ks = 0.f, vs[C::kTok / 32] = {}, vref = 0.f;
+  // loads of the tile at token t0 of item q: which pages (one lane each), then rows
+  int pids = -1;
+  auto look_up = [&](const PItem &q, int t0) {
+    const int tok = t0 + 16 * lane;
+    pids = -1;
+    if (lane < C::kTok / 16 && tok < (q.p1 - q.p0) * S) {
+      const int p = __ldg(a.d.block_table + (size_t)a.members[q.first] * a.d.MP + q.p0 + tok / S);
+      if (p >= 0 && p < a.d.P) pids = p;
+    }
+  };
+  auto load = [&](const PItem &q, int t0, uint4 (&x)[kIt], const void *pool) {
+#pragma unroll
+    for (int i = 0; i < kIt; ++i) {
+      const int r = i * kRowsIt + r_it;
+      const int p = __shfl_sync(0xffffffffu, pids, r >> 4);
+      x[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (p >= 0)
+        x[i] = *(reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(pool) +
+                                                 (((size_t)p * H + q.h) * S + (t0 + r) % S) * kD) + c);
+    }
+  };
+  auto load_scale = [&](const PItem &q, int t0) {
+    ks = 0.f;
+#pragma unroll
+    for (int i = 0; i < C::kTok / 32; ++i) {
+      const int r = 32 * i + lane, p = __shfl_sync(0xffffffffu, pids, r >> 4);
+      vs[i] = 0.f;
+      if (p >= 0) {
+        const size_t row = ((size_t)p * H + q.h) * S + (t0 + r) % S;
+        vs[i] = a.d.v_scale[row];
+        if (i == t >> 5) ks = a.d.k_scale[row];
+      }
+    }
+  };
+  auto store = [&](uint32_t slot, const uint4 (&x)[kIt]) {
+    const uint32_t base = s_ring + slot * C::kTBytes;
+#pragma unroll
+    for (int i = 0; i < kIt; ++i) {
+      const int r = i * kRowsIt + r_it;
+      uint4 lo, hi;
+      e4m3x4_to_f16x4(x[i].x, lo.x, lo.y);
+      e4m3x4_to_f16x4(x[i].y, lo.z, lo.w);
+      e4m3x4_to_f16x4(x[i].z, hi.x, hi.y);
+      e4m3x4_to_f16x4(x[i].w, hi.z, hi.w);
+      const uint32_t row = base + r * 128;
+      sts128(row + (j0 >> 3) * C::kBlkT + (((j0 & 7) ^ (r & 7)) << 4), swap ? hi : lo);
+      sts128(row + (j1 >> 3) * C::kBlkT + (((j1 & 7) ^ (r & 7)) << 4), swap ? lo : hi);
+    }
+    fence_async_smem();
+    __syncwarp();
+  };
+  if (have) {
+    look_up(it, 0);
+    load(it, 0, kr, a.d.k_pool);
+    load(it, 0, vr, a.d.v_pool);
+    if (per_token) load_scale(it, 0);
+  }
+  while (have) {
+    const int n_tok = (it.p1 - it.p0) * S;
+    vref = 0.f;
+    for (int t0 = 0; t0 < n_tok; t0 += C::kTok, ++n) {
+      // the tile after this one, of this item or the next
+      PItem nx = it;
+      int nt = t0 + C::kTok;
+      bool more = true;
+      if (nt >= n_tok) {
+        more = walk_next(a, w, nx);
+        nt = 0;
+      }
+      const uint32_t ik = 2 * n, sk = ik % kSlots, sv = (ik + 1) % kSlots, ph = ((ik / kSlots) & 1u) ^ 1u;
+      if (!mbar_wait_warp(&B.empty[sk], ph, abort)) return;
+      if (per_token) hand_scales<C>(smem, B, n, ks, vs, vref, t);
+      store(sk, kr);
+      // test hook: the first CTA never hands its first tile over, and the other warps' bounded waits give up
+      if (withhold && n == 0) return;
+      if (lane == 0) mbar_arrive(&B.full[sk]);
+      if (more) {
+        look_up(nx, nt);
+        load(nx, nt, kr, a.d.k_pool);
+        if (per_token) load_scale(nx, nt);
+      }
+      if (!mbar_wait_warp(&B.empty[sv], ph, abort)) return;
+      store(sv, vr);
+      if (lane == 0) mbar_arrive(&B.full[sv]);
+      if (more) load(nx, nt, vr, a.d.v_pool);
+      if (nt == 0) {
+        it = nx;
+        have = more;
+      }
+    }
+  }
+}
+
+// BF16: copies straight into the operand layout, two tiles in flight.
+template <bool kFp8, int kD, int kTerms>
+__device__ __forceinline__ void loader_bf16(const PrefixArgs &a, uint8_t *smem, const PBars &B, const PrefixHdr &hdr,
+                                            volatile int *abort) {
+  using C = PCfg<kFp8, kD, kTerms>;
+  constexpr int kLanes = kD / 8, kRowsIt = 128 / kLanes, kIt = C::kTok / kRowsIt;
+  const int t = threadIdx.x - 8 * 32, lane = t & 31;
+  const int S = a.d.S, H = a.d.cache.num_kv_heads, c = t % kLanes, r_it = t / kLanes;
+  const uint32_t s_ring = smem_addr(smem + C::kOffT);
+  PWalk w{range_start(hdr, blockIdx.x), range_start(hdr, blockIdx.x + 1), (int)blockIdx.x};
+  PItem it;
+  const bool withhold = (a.d.flags & PFKV_FLAG_TEST_WITHHOLD) && blockIdx.x == 0;
+  uint32_t n = 0;  // tiles issued (K and V counted apart); tile n - 2 is handed over when tile n is issued
+  auto hand_over = [&](uint32_t i) {
+    fence_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&B.full[i % kSlots]);
+  };
+  while (walk_next(a, w, it)) {
+    const int n_tok = (it.p1 - it.p0) * S;
+    for (int t0 = 0; t0 < n_tok; t0 += C::kTok) {
+      int pids = -1;
+      const int tok = t0 + 16 * lane;
+      if (lane < C::kTok / 16 && tok < n_tok) {
+        const int p = __ldg(a.d.block_table + (size_t)a.members[it.first] * a.d.MP + it.p0 + tok / S);
+        if (p >= 0 && p < a.d.P) pids = p;
+      }
+#pragma unroll
+      for (int part = 0; part < 2; ++part, ++n) {
+        if (!mbar_wait_warp(&B.empty[n % kSlots], ((n / kSlots) & 1u) ^ 1u, abort)) {
+          cp_async_wait<0>();
+          return;
+        }
+        const uint32_t base = s_ring + (n % kSlots) * C::kTBytes;
+        const uint8_t *pool = static_cast<const uint8_t *>(part ? a.d.v_pool : a.d.k_pool);
+#pragma unroll
+        for (int i = 0; i < kIt; ++i) {
+          const int r = i * kRowsIt + r_it;
+          const int p = __shfl_sync(0xffffffffu, pids, r >> 4);
+          cp_async16(base + (c >> 3) * C::kBlkT + r * 128 + (((c & 7) ^ (r & 7)) << 4),
+                     pool + (((size_t)max(p, 0) * H + it.h) * S + (t0 + r) % S) * (2 * kD) + 16 * c, p >= 0);
+        }
+        cp_async_commit();
+        if (n >= 2) {
+          cp_async_wait<2>();
+          if (withhold && n == 2) {  // test hook, as in the FP8 loader
+            cp_async_wait<0>();
+            return;
+          }
+          hand_over(n - 2);
+        }
+      }
+    }
+  }
+  cp_async_wait<0>();
+  if (n >= 2) {
+    if (withhold && n == 2) return;
+    hand_over(n - 2);
+    hand_over(n - 1);
+  }
+}
+
+// ---------------------------------------------------------------- MMA issuer (warp 12, one thread)
+
+// Unit u of an item is one half's tile: half u & 1, tile u / 2 (both halves
+// over the same tokens) or u (split).  Order QK(0) QK(1), then PV(u) QK(u + 2):
+// a half's S is overwritten only after its P, which lies over it, was read by
+// the PV issued before.
+template <bool kFp8, int kD, int kTerms>
+__device__ __forceinline__ void issue_mmas(const PrefixArgs &a, uint8_t *smem, const PBars &B, const PrefixHdr &hdr,
+                                           uint32_t tmem, volatile int *abort) {
+  using C = PCfg<kFp8, kD, kTerms>;
+  const int S = a.d.S;
+  const uint64_t dq = umma_sdesc(smem_addr(smem + C::kOffQ), 16, 1024, 2);
+  const uint64_t dk = umma_sdesc(smem_addr(smem + C::kOffT), 16, 1024, 2);
+  const uint64_t dv = umma_sdesc(smem_addr(smem + C::kOffT), C::kBlkT, 1024, 2);
+  PWalk w{range_start(hdr, blockIdx.x), range_start(hdr, blockIdx.x + 1), (int)blockIdx.x};
+  PItem it;
+  uint32_t base = 0, items = 0;  // tiles before this item
+  uint32_t pc[2][C::kChunks] = {};
+  bool ok = true;
+  for (; ok && walk_next(a, w, it); ++items) {
+    const int n_tok = (it.p1 - it.p0) * S;
+    const int tiles = (n_tok + C::kTok - 1) / C::kTok, units = it.split ? tiles : 2 * tiles;
+    for (int t = 0; t < 2 && ok; ++t) ok = mbar_wait(&B.q_ready[t], items & 1u, abort);
+    auto qk = [&](int u) {
+      const int t = u & 1;
+      const uint32_t ik = 2 * (base + (uint32_t)(it.split ? u : u >> 1)), slot = ik % kSlots;
+      ok = mbar_wait(&B.full[slot], (ik / kSlots) & 1u, abort);
+      if (!ok) return;
+      tc_fence_after();
+#pragma unroll
+      for (int s = 0; s < kD / 16; ++s) {
+        const uint32_t oq = t * C::kQBytes + (s >> 2) * C::kBlkQ + (s & 3) * 32;
+        const uint32_t ok_ = slot * C::kTBytes + (s >> 2) * C::kBlkT + (s & 3) * 32;
+        umma_f16(tmem + C::kColS + t * C::kTok, dq + (uint64_t)(oq >> 4), dk + (uint64_t)(ok_ >> 4), C::kIdQK,
+                 s ? 1u : 0u);
+      }
+      umma_commit(&B.s_full[t]);
+      if (it.split || t == 1) umma_commit(&B.empty[slot]);
+    };
+    for (int u = 0; u < 2 && u < units && ok; ++u) qk(u);
+    if (units == 1 && ok) umma_commit(&B.s_full[1]);  // half 1 has no tile; see its wait
+    for (int u = 0; u < units && ok; ++u) {
+      const int t = u & 1, tile = it.split ? u : u >> 1;
+      const uint32_t iv = 2 * (base + (uint32_t)tile) + 1, slot = iv % kSlots;
+      const int chunks = (min(C::kTok, n_tok - tile * C::kTok) + 63) / 64;
+      ok = mbar_wait(&B.full[slot], (iv / kSlots) & 1u, abort);
+#pragma unroll
+      for (int c = 0; c < C::kChunks; ++c) {
+        if (c >= chunks || !ok) break;
+        ok = mbar_wait(&B.p_full[2 * t + c], pc[t][c]++ & 1u, abort);
+        if (!ok) break;
+        tc_fence_after();
+#pragma unroll
+        for (int k = 0; k < kTerms; ++k) {
+          const uint32_t p = tmem + (k < 2 ? C::kColS + t * C::kTok + 64 * c + 32 * k : C::kColX + 32 * t);
+#pragma unroll
+          for (int s = 0; s < 4; ++s)
+            umma_f16_ts(tmem + C::kColO + 128 * t, p + 8 * s,
+                        dv + (uint64_t)((slot * C::kTBytes + (4 * c + s) * 2048) >> 4), C::kIdPV,
+                        (u < 2 && c == 0 && k == 0 && s == 0) ? 0u : 1u);
+        }
+        umma_commit(&B.pv_done[2 * t + c]);
+      }
+      if (!ok) break;
+      if (it.split || t == 1) umma_commit(&B.empty[slot]);
+      if (u + 2 < units) qk(u + 2);
+    }
+    base += (uint32_t)tiles;
+  }
+  // every MMA issued here has completed before tensor memory is released
+  umma_commit(B.drain);
+  const uint64_t t0 = global_timer_ns();
+  while (!mbar_try_wait(B.drain, 0))
+    if (global_timer_ns() - t0 > kWaitLimitNs) break;
+}
+
+// ---------------------------------------------------------------- softmax (warps 0-7)
+
+template <bool kFp8, int kD, int kTerms>
+__device__ __forceinline__ void softmax_rows(const PrefixArgs &a, uint8_t *smem, const PBars &B, const PrefixHdr &hdr,
+                                             uint32_t tmem, volatile int *abort) {
+  using C = PCfg<kFp8, kD, kTerms>;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int t = warp >> 2, r = (warp & 3) * 32 + lane;  // half, row of it
+  const bool per_token = kFp8 && a.d.scale_mode == PFKV_SCALE_PER_TOKEN;
+  const uint32_t tq = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+  const uint32_t col_s = tq + C::kColS + t * C::kTok, col_o = tq + C::kColO + 128 * t;
+  const int S = a.d.S;
+  PWalk w{range_start(hdr, blockIdx.x), range_start(hdr, blockIdx.x + 1), (int)blockIdx.x};
+  PItem it;
+  uint32_t base = 0, n_s = 0, n_pv[2] = {0, 0};  // tiles, units, and units' first and second chunks before
+  while (walk_next(a, w, it)) {
+    const int n_tok = (it.p1 - it.p0) * S;
+    const int tiles = (n_tok + C::kTok - 1) / C::kTok, units = it.split ? tiles : 2 * tiles;
+    const int row = it.split ? r : t * (kRows / 2) + r;  // row of the item's block
+    const bool mine = row < it.n_rows;
+    // this thread's query row into the operand; f16: scaled by 2^e into [2^14, 2^15), exact; the sign of the
+    // factor that turns products into scores goes with it, so that the largest product is the largest score
+    float mult = a.d.sm_scale_log2;
+    if (kFp8 && !per_token) mult *= a.d.k_scale[it.h];
+    {
+      uint4 x[kD / 8];
+      const uint4 *src = nullptr;
+      if (mine) {
+        const int gr = it.row0 + row, b = a.members[it.first + gr / a.G];
+        src = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.d.q) +
+                                              ((size_t)b * a.d.Hq + it.h * a.G + gr % a.G) * kD);
+      }
+#pragma unroll
+      for (int j = 0; j < kD / 8; ++j) x[j] = mine ? src[j] : make_uint4(0u, 0u, 0u, 0u);
+      float mx = 0.f;
+#pragma unroll
+      for (int j = 0; j < kD / 8; ++j) mx = amax8(x[j], mx);
+      int e = 0;
+      if (kFp8 && mx > 0.f) {
+        frexpf(mx, &e);
+        e = 15 - e;
+      }
+      // 2^e as two factors, either of which is a normal number
+      float f1 = ldexpf(mult < 0.f ? -1.f : 1.f, e / 2);
+      const float f2 = ldexpf(1.f, e - e / 2);
+      mult = ldexpf(fabsf(mult), -e);
+      if (mult == 0.f) {  // all scores are zero; a factor of zero would meet the masked tokens' -inf
+        f1 = 0.f;
+        mult = 1.f;
+      }
+      const uint32_t dst = smem_addr(smem + C::kOffQ) + t * C::kQBytes + r * 128;
+#pragma unroll
+      for (int j = 0; j < kD / 8; ++j) {
+        uint32_t v[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const float lo = __uint_as_float(v[q] << 16) * f1 * f2, hi = __uint_as_float(v[q] & 0xffff0000u) * f1 * f2;
+          v[q] = kFp8 ? pack_f16x2(lo, hi) : pack_bf16x2(lo, hi);
+        }
+        sts128(dst + (j >> 3) * C::kBlkQ + (((j & 7) ^ (r & 7)) << 4), make_uint4(v[0], v[1], v[2], v[3]));
+      }
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&B.q_ready[t]);
+    }
+    float m = kNegInf, l = 0.f, vref = 1.f;
+    bool first = true;
+    int last = 0;  // the chunk handed over last; its products are the last to finish
+    for (int u = t; u < units; u += 2) {
+      const int tile = it.split ? u : u >> 1;
+      const int valid = n_tok - tile * C::kTok;
+      const uint32_t n = base + (uint32_t)tile;
+      const float *sc = reinterpret_cast<const float *>(smem + C::kOffScale) + (n % kScaleSlots) * (2 * C::kTok + 4);
+      if (!mbar_wait_warp(&B.s_full[t], n_s++ & 1u, abort)) return;
+      float moved = 1.f;
+      if (per_token) {
+        if (!mbar_wait_warp(&B.sc_full[n % kScaleSlots], (n / kScaleSlots) & 1u, abort)) return;
+        const float now = sc[2 * C::kTok];  // against the reference this half last used (split: not every tile's)
+        if (!first && now != vref) moved = vref / now;
+        vref = now;
+      }
+      tc_fence_after();
+#pragma unroll 1
+      for (int c = 0; c < C::kChunks && 64 * c < valid; ++c) {
+        uint32_t z[64];
+        tmem_ld64(col_s + 64 * c, z);
+        float mx = kNegInf;
+        if (per_token) {
+#pragma unroll
+          for (int j = 0; j < 64; j += 4) {
+            const float4 k4 = *reinterpret_cast<const float4 *>(sc + 64 * c + j);
+            z[j] = __float_as_uint(__uint_as_float(z[j]) * k4.x);
+            z[j + 1] = __float_as_uint(__uint_as_float(z[j + 1]) * k4.y);
+            z[j + 2] = __float_as_uint(__uint_as_float(z[j + 2]) * k4.z);
+            z[j + 3] = __float_as_uint(__uint_as_float(z[j + 3]) * k4.w);
+          }
+        }
+        if (64 * c + 64 > valid) {
+#pragma unroll
+          for (int j = 0; j < 64; ++j)
+            if (64 * c + j >= valid) z[j] = 0xff800000u;
+        }
+#pragma unroll
+        for (int j = 0; j < 64; ++j) mx = fmaxf(mx, __uint_as_float(z[j]));
+        mx = mx == kNegInf ? kNegInf : mx * mult;
+        // move the reference
+        const bool grow = mx > m + kGrow || first;
+        if (__any_sync(0xffffffffu, grow || moved != 1.f)) {
+          const float mn = grow ? fmaxf(m, mx) : m;
+          const float al = first ? 0.f : fast_exp2(m - mn);
+          l *= al;
+          if (!first) {
+            // the products handed over before: those of earlier tiles are done, as S could not be here otherwise
+            if (c > 0 && !mbar_wait_warp(&B.pv_done[2 * t], (n_pv[0] - 1) & 1u, abort)) return;
+            tc_fence_after();
+            const float f = al * moved;
+#pragma unroll 1
+            for (int i = 0; i < kD / 32; ++i) {
+              uint32_t o[32];
+              tmem_ld32(col_o + 32 * i, o);
+#pragma unroll
+              for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+              tmem_st32(col_o + 32 * i, o);
+            }
+            tmem_wait_st();
+          }
+          m = mn;
+          moved = 1.f;
+        }
+        first = false;
+        const float off = C::kShift - m;
+        float sum0 = 0.f, sum1 = 0.f;
+        uint32_t pk[32];
+#pragma unroll
+        for (int k = 0; k < kTerms; ++k) {
+#pragma unroll
+          for (int j = 0; j < 64; j += 2) {
+            float p0, p1;
+            if (k == 0) {
+              p0 = fast_exp2(fmaf(__uint_as_float(z[j]), mult, off));
+              p1 = fast_exp2(fmaf(__uint_as_float(z[j + 1]), mult, off));
+              sum0 += p0;
+              sum1 += p1;
+              if (per_token) {
+                const float2 v2 = *reinterpret_cast<const float2 *>(sc + C::kTok + 64 * c + j);
+                p0 *= v2.x;
+                p1 *= v2.y;
+              }
+            } else {
+              p0 = __uint_as_float(z[j]);
+              p1 = __uint_as_float(z[j + 1]);
+            }
+            if constexpr (kFp8) {
+              pk[j / 2] = pack_f16x2(p0, p1);
+              if (k + 1 < kTerms) {
+                const float2 back = __half22float2(*reinterpret_cast<const __half2 *>(&pk[j / 2]));
+                z[j] = __float_as_uint(p0 - back.x);
+                z[j + 1] = __float_as_uint(p1 - back.y);
+              }
+            } else {
+              pk[j / 2] = pack_bf16x2(p0, p1);
+              if (k + 1 < kTerms) {
+                z[j] = __float_as_uint(p0 - __uint_as_float(pk[j / 2] << 16));
+                z[j + 1] = __float_as_uint(p1 - __uint_as_float(pk[j / 2] & 0xffff0000u));
+              }
+            }
+          }
+          tmem_st32(k < 2 ? col_s + 64 * c + 32 * k : tq + C::kColX + 32 * t, pk);
+        }
+        l += sum0 + sum1;
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&B.p_full[2 * t + c]);
+        if (c == 0) ++n_pv[0];
+        else ++n_pv[1];
+        last = c;
+      }
+    }
+    // the half's partial result; a half without a tile (split, a single one) waits for the issuer all the same,
+    // so that it does not run ahead of it
+    if (first) {
+      if (!mbar_wait_warp(&B.s_full[t], n_s++ & 1u, abort)) return;
+    } else {
+      if (!mbar_wait_warp(&B.pv_done[2 * t + last], ((last ? n_pv[1] : n_pv[0]) - 1) & 1u, abort)) return;
+      tc_fence_after();
+    }
+    const float fac = !kFp8 ? 1.f : per_token ? vref : a.d.v_scale[it.h];
+    const size_t at = (size_t)it.slot * kRows + t * (kRows / 2) + r;
+#pragma unroll 1
+    for (int i = 0; i < kD / 32; ++i) {
+      uint32_t o[32];
+      if (!first) {
+        tmem_ld32(col_o + 32 * i, o);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 32; ++j) o[j] = 0u;
+      }
+      if (mine)
+#pragma unroll
+        for (int j = 0; j < 32; j += 8) {
+          float v[8];
+#pragma unroll
+          for (int q = 0; q < 8; ++q) v[q] = __uint_as_float(o[j + q]) * fac;
+          stg256(a.o + at * kD + 32 * i + j, v);
+        }
+    }
+    if (mine) a.ml[at] = make_float2(first ? kNegInf : m - C::kShift, l);
+    tc_fence_before();
+    base += (uint32_t)tiles;
+  }
+}
+
+template <bool kFp8, int kD, int kTerms>
+__global__ void __launch_bounds__(kPThreads, 1) prefix_kernel(const PrefixArgs a) {
+  using C = PCfg<kFp8, kD, kTerms>;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_abort;
+  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const PBars B = pbars_at(smem + C::kOffBars);
+  const int warp = threadIdx.x >> 5;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kSlots; ++i) {
+      mbar_init(&B.full[i], 4);
+      mbar_init(&B.empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&B.s_full[i], 1);
+      mbar_init(&B.q_ready[i], 4);
+    }
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&B.p_full[i], 4);
+      mbar_init(&B.pv_done[i], 1);
+    }
+    for (int i = 0; i < kScaleSlots; ++i) mbar_init(&B.sc_full[i], 4);
+    mbar_init(B.drain, 1);
+    s_abort = 0;
+    mbar_init_fence();
+  }
+  if (warp == 12) tmem_alloc(&s_tmem, 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = s_tmem;
+  volatile int *abort = &s_abort;
+  pdl_wait();
+  pdl_launch_dependents();
+  const PrefixHdr hdr = *a.hdr;
+  if ((int)blockIdx.x < hdr.R) {
+    if (warp < 8) {
+      softmax_rows<kFp8, kD, kTerms>(a, smem, B, hdr, tmem, abort);
+    } else if (warp < 12) {
+      if constexpr (kFp8) loader_fp8<kFp8, kD, kTerms>(a, smem, B, hdr, abort);
+      else loader_bf16<kFp8, kD, kTerms>(a, smem, B, hdr, abort);
+    } else if ((threadIdx.x & 31) == 0) {
+      issue_mmas<kFp8, kD, kTerms>(a, smem, B, hdr, tmem, abort);
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 12) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+  if (threadIdx.x == 0) a.aborts[blockIdx.x] = s_abort;
+}
+
+}  // namespace
+}  // namespace pfkv
