@@ -18,12 +18,16 @@
 // converted tiles 512) have to hide behind them.  Hence: one CTA per SM, and
 //   warps 0-3, 4-7  softmax of row half 0 and 1: a thread owns a row, so that
 //                   maxima and sums need no exchange; P overwrites S.
-//   warps 8-11      loaders.  FP8: 16-byte loads into registers one tile
-//                   ahead, e4m3 -> f16 once per CTA, stored in the operands'
-//                   128-byte-swizzled layout.  BF16: asynchronous copies two
-//                   tiles ahead.  Ring of four tiles (K, V, K, V).
+//   warps 8-11      operands, in a ring of K and V tiles in the 128-byte-
+//                   swizzled layout.  FP8: e4m3 -> f16 from staged codes,
+//                   once per CTA.  BF16: asynchronous copies from the pool,
+//                   two tiles ahead.
 //   warp 12         issues the MMAs.  The two halves alternate, so that one
 //                   half's products run while the other's softmax does.
+//   warp 13         planner: works out the CTA's items and where each tile's
+//                   rows lie (bounds-checked page ids), so that nobody else
+//                   waits for a table entry; FP8: bulk-copies the codes into
+//                   a staging ring of three tiles (48 KB in flight).
 // An item of more than 128 rows has 128 in each half, over the same tokens.
 // One of at most 128 rows gives both halves the same rows and alternate tiles
 // of the tokens; each half then leaves a partial result of its own.
@@ -41,15 +45,44 @@
 namespace pfkv {
 namespace {
 
-constexpr int kPThreads = 13 * 32;
-constexpr int kSlots = 4;        // tiles in the ring: K, V, K, V
+constexpr int kPThreads = 16 * 32;  // four warpgroups; warps 14 and 15 only lend their registers
 constexpr int kScaleSlots = 4;   // tiles whose per-token scales are kept
+constexpr int kItemSlots = 4;    // items announced ahead
+constexpr int kTileSlots = 8;    // tiles announced ahead
+// Registers a thread after the launch's 128: two softmax warpgroups, the
+// operand warps, and the rest; 2 x 176 + 88 + 72 = 4 x 128.
+constexpr int kRegsSoftmax = 176, kRegsLoader = 88, kRegsRest = 72;
+static_assert(kRegsSoftmax >= 128 && kRegsLoader <= 128 && kRegsRest <= 128 &&
+                  2 * kRegsSoftmax + kRegsLoader + kRegsRest <= 4 * 128,
+              "an increase goes up and a decrease down, and all of them fit what the block was launched with");
 constexpr float kGrow = 8.f;     // growth of a row's maximum that moves its reference
+
+// One piece of work, announced by the planner; n_rows 0 ends the work.
+struct PItem {
+  int first, row0, n_rows, h, p0, p1;
+  long long slot;
+  int split;  // at most 128 rows: the halves take alternate tiles
+  int pad;
+};
+static_assert(sizeof(PItem) == 40, "item slot");
+
+// One tile, announced by the planner: the pool row of each 16 tokens' first
+// one (they lie in one page), or -1 for tokens past the end or a page id
+// outside the pool.
+struct PTile {
+  long long row[8];
+  int kind;      // 0: ends the work, 1: a tile, 2: an item's first tile
+  uint32_t rows; // bit g: row[g] is one
+};
+static_assert(sizeof(PTile) == 72, "tile slot");
 
 template <bool kFp8, int kD, int kTerms>
 struct PCfg {
   static constexpr int kTok = kTerms == 3 ? 64 : 128;  // tokens per tile (tensor memory bounds it)
   static constexpr int kChunks = kTok / 64;
+  static constexpr int kSlots = kFp8 && kD == 128 ? 3 : 4;  // operand ring: K, V, K, V, ...
+  static constexpr int kStage = kFp8 ? 3 : 0;               // staged code tiles
+  static constexpr uint32_t kCodeBytes = kTok * kD;
   static constexpr uint32_t kBlkQ = 128 * 128;          // 64 dims of a query half
   static constexpr uint32_t kQBytes = kBlkQ * (kD / 64);
   static constexpr uint32_t kBlkT = kTok * 128;         // 64 dims of a tile
@@ -58,19 +91,15 @@ struct PCfg {
   static constexpr uint32_t kColS = 0, kColX = 2 * kTok, kColO = 256;
   // per-token mode: v scales relative to a running reference, at most twice it
   static constexpr float kShift = kFp8 ? 6.f : 0.f;
-  static constexpr uint32_t kOffQ = 0, kOffT = 2 * kQBytes, kOffScale = kOffT + kSlots * kTBytes;
+  static constexpr uint32_t kOffQ = 0, kOffT = 2 * kQBytes, kOffCode = kOffT + kSlots * kTBytes;
+  static constexpr uint32_t kOffCodeScale = kOffCode + kStage * kCodeBytes;  // K and V scales beside the codes of K
+  static constexpr uint32_t kOffScale = kOffCodeScale + kStage * 2 * kTok * 4;
   static constexpr uint32_t kOffBars = kOffScale + kScaleSlots * (2 * kTok * 4 + 16);
-  static constexpr uint32_t kTotal = kOffBars + 8 * 32 + 32 + 1024;
+  static constexpr uint32_t kOffItems = kOffBars + 8 * 64;
+  static constexpr uint32_t kTotal = kOffItems + kItemSlots * sizeof(PItem) + kTileSlots * sizeof(PTile) + 1024;
   static constexpr uint32_t kIdQK = umma_idesc_f16(128, kTok, !kFp8, 0, 0);
   static constexpr uint32_t kIdPV = umma_idesc_f16(128, kD, !kFp8, 0, 1);
   static_assert(kTotal <= 232448, "shared memory plan exceeds one SM");
-};
-
-// One piece of work, as every role works it out.
-struct PItem {
-  int first, row0, n_rows, h, p0, p1;
-  long long slot;
-  bool split;  // at most 128 rows: the halves take alternate tiles
 };
 
 struct PWalk {
@@ -101,24 +130,33 @@ __device__ __forceinline__ bool walk_next(const PrefixArgs &a, PWalk &w, PItem &
   return true;
 }
 
+constexpr int kMaxSlots = 4;
 struct PBars {
-  uint64_t *full, *empty;              // ring
+  uint64_t *full, *empty;              // operand ring
+  uint64_t *code_full, *code_empty;    // staging ring
   uint64_t *s_full, *q_ready;          // per half
   uint64_t *p_full, *pv_done;          // per half and chunk
   uint64_t *sc_full;                   // per-token scales
+  uint64_t *item_full, *item_empty, *tile_full, *tile_empty;
   uint64_t *drain;
 };
 
 __device__ __forceinline__ PBars pbars_at(uint8_t *base) {
   uint64_t *b = reinterpret_cast<uint64_t *>(base);
   PBars r;
-  r.full = b; b += kSlots;
-  r.empty = b; b += kSlots;
+  r.full = b; b += kMaxSlots;
+  r.empty = b; b += kMaxSlots;
+  r.code_full = b; b += kMaxSlots;
+  r.code_empty = b; b += kMaxSlots;
   r.s_full = b; b += 2;
   r.p_full = b; b += 4;
   r.pv_done = b; b += 4;
   r.q_ready = b; b += 2;
   r.sc_full = b; b += kScaleSlots;
+  r.item_full = b; b += kItemSlots;
+  r.item_empty = b; b += kItemSlots;
+  r.tile_full = b; b += kTileSlots;
+  r.tile_empty = b; b += kTileSlots;
   r.drain = b;
   return r;
 }
@@ -127,212 +165,255 @@ __device__ __forceinline__ bool mbar_wait_warp(uint64_t *bar, uint32_t parity, v
   return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort));
 }
 
+// The new count must not be below (inc) or above (dec) the current one.
+template <int kRegs>
+__device__ __forceinline__ void regs_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+template <int kRegs>
+__device__ __forceinline__ void regs_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+
+// ---------------------------------------------------------------- planner (warp 13)
+
+// Bulk copies of one staged tile (part 0: K, with the per-token scales of K
+// and V; 1: V): lane g takes 16 tokens' codes, which are contiguous.
+template <typename C, int kD>
+__device__ __forceinline__ bool stage_codes(const PrefixArgs &a, uint8_t *smem, const PBars &B, const PTile &d,
+                                            uint32_t i, int part, bool per_token, volatile int *abort) {
+  const int lane = threadIdx.x & 31;
+  const uint32_t s = i % C::kStage;
+  if (!mbar_wait_warp(&B.code_empty[s], ((i / C::kStage) & 1u) ^ 1u, abort)) return false;
+  const uint32_t each = 16 * kD + (per_token && part == 0 ? 128 : 0);
+  if (lane == 0) mbar_arrive_expect_tx(&B.code_full[s], each * (uint32_t)__popc(d.rows));
+  __syncwarp();
+  if (lane < 8 && (d.rows >> lane & 1u)) {
+    const long long row = d.row[lane];
+    const uint8_t *pool = static_cast<const uint8_t *>(part ? a.d.v_pool : a.d.k_pool);
+    bulk_load(smem + C::kOffCode + s * C::kCodeBytes + lane * 16 * kD, pool + row * kD, 16 * kD, &B.code_full[s]);
+    if (per_token && part == 0) {
+      float *dst = reinterpret_cast<float *>(smem + C::kOffCodeScale) + s * 2 * C::kTok + 16 * lane;
+      bulk_load(dst, a.d.k_scale + row, 64, &B.code_full[s]);
+      bulk_load(dst + C::kTok, a.d.v_scale + row, 64, &B.code_full[s]);
+    }
+  }
+  return true;
+}
+
+template <bool kFp8, int kD, int kTerms>
+__device__ __forceinline__ void plan_tiles(const PrefixArgs &a, uint8_t *smem, const PBars &B, const PrefixHdr &hdr,
+                                           volatile int *abort) {
+  using C = PCfg<kFp8, kD, kTerms>;
+  PItem *items = reinterpret_cast<PItem *>(smem + C::kOffItems);
+  PTile *tiles = reinterpret_cast<PTile *>(smem + C::kOffItems + kItemSlots * sizeof(PItem));
+  const int lane = threadIdx.x & 31, S = a.d.S, H = a.d.cache.num_kv_heads;
+  const bool per_token = kFp8 && a.d.scale_mode == PFKV_SCALE_PER_TOKEN;
+  constexpr int kGroups = C::kTok / 16, kAtOnce = 32 / kGroups;  // 16-token groups of a tile; tiles per look-up
+  PWalk w{range_start(hdr, blockIdx.x), range_start(hdr, blockIdx.x + 1), (int)blockIdx.x};
+  uint32_t n = 0;
+  bool ok = true;
+  for (uint32_t i = 0; ok; ++i) {
+    PItem it{};
+    const bool have = walk_next(a, w, it);
+    if (!mbar_wait_warp(&B.item_empty[i % kItemSlots], ((i / kItemSlots) & 1u) ^ 1u, abort)) break;
+    if (lane == 0) {
+      items[i % kItemSlots] = it;
+      mbar_arrive(&B.item_full[i % kItemSlots]);
+    }
+    const int n_tok = have ? (it.p1 - it.p0) * S : 1;
+    const int *trow = have ? a.d.block_table + (size_t)a.members[it.first] * a.d.MP + it.p0 : nullptr;
+    auto look_up = [&](int t0) -> int {
+      const int tok = t0 + 16 * lane;
+      return have && tok < n_tok ? __ldg(trow + tok / S) : -1;
+    };
+    int next = look_up(0);
+    for (int t0 = 0; t0 < n_tok && ok; t0 += kAtOnce * C::kTok) {
+      const int p = next;
+      next = look_up(t0 + kAtOnce * C::kTok);  // on its way while this batch goes out
+      const bool fine = p >= 0 && p < a.d.P;
+      const uint32_t rows = __ballot_sync(0xffffffffu, fine);
+      for (int k = 0; k < kAtOnce && t0 + k * C::kTok < n_tok; ++k, ++n) {
+        PTile &d = tiles[n % kTileSlots];
+        ok = mbar_wait_warp(&B.tile_empty[n % kTileSlots], ((n / kTileSlots) & 1u) ^ 1u, abort);
+        if (!ok) break;
+        if (lane / kGroups == k)
+          d.row[lane % kGroups] = fine ? ((long long)p * H + it.h) * S + (t0 + 16 * lane) % S : -1;
+        if (lane == 0) {
+          d.kind = !have ? 0 : t0 + k == 0 ? 2 : 1;
+          d.rows = rows >> (kGroups * k) & ((1u << kGroups) - 1u);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&B.tile_full[n % kTileSlots]);
+        if constexpr (kFp8) {
+          for (int part = 0; part < 2 && have && ok; ++part)
+            ok = stage_codes<C, kD>(a, smem, B, d, 2 * n + part, part, per_token, abort);
+        }
+        if (!ok) break;
+      }
+    }
+    if (!have) return;
+  }
+  // a wait gave up: copies in flight land before the block may exit
+  if constexpr (kFp8) {
+    const uint32_t issued = 2 * n + 2;  // at most
+    for (uint32_t i = issued > C::kStage + 2 ? issued - C::kStage - 2 : 0; i < issued; ++i) {
+      const uint64_t t0 = global_timer_ns();
+      while (!mbar_try_wait(&B.code_full[i % C::kStage], (i / C::kStage) & 1u))
+        if (global_timer_ns() - t0 > kWaitLimitNs / 8) break;
+    }
+  }
+}
+
 // ---------------------------------------------------------------- loaders (warps 8-11)
 
-// Per-token scales of tile n: K scales as they are, V scales relative to a
-// running reference vref, which moves when a tile's largest scale exceeds
-// twice it.  Every loader warp reads all of the tile's V scales for their
-// maximum, so that the warps need not meet, and writes its own 32 tokens'.
+// Per-token scales of tile n, from beside its staged K codes: K scales as they
+// are, V scales relative to a running reference vref, which moves when a
+// tile's largest scale exceeds twice it.  Every operand warp reads all of the
+// tile's V scales for their maximum, so that the warps need not meet, and
+// writes its own 32 tokens'.
 template <typename C>
-__device__ __forceinline__ void hand_scales(uint8_t *smem, const PBars &B, uint32_t n, float ks,
-                                            const float (&vs)[C::kTok / 32], float &vref, int t) {
+__device__ __forceinline__ void hand_scales(uint8_t *smem, const PBars &B, uint32_t n, uint32_t stage, uint32_t rows,
+                                            float &vref, int t) {
   float *dst = reinterpret_cast<float *>(smem + C::kOffScale) + (n % kScaleSlots) * (2 * C::kTok + 4);
+  const float *src = reinterpret_cast<const float *>(smem + C::kOffCodeScale) + stage * 2 * C::kTok;
   const int lane = t & 31, warp = t >> 5;
-  float mx = vs[0], mine = vs[0];
+  float mx = 0.f, mine = 0.f;
 #pragma unroll
-  for (int i = 1; i < C::kTok / 32; ++i) {
-    mx = fmaxf(mx, vs[i]);
-    if (i == warp) mine = vs[i];
+  for (int i = 0; i < C::kTok / 32; ++i) {
+    const int r = 32 * i + lane;
+    const float v = rows >> (r >> 4) & 1u ? src[C::kTok + r] : 0.f;
+    mx = fmaxf(mx, v);
+    if (i == warp) mine = v;
   }
   mx = warp_max_f32(mx);
   if (mx > 2.f * vref) vref = mx;
-  if (t < C::kTok) {
-    dst[t] = ks;
-    dst[C::kTok + t] = vref > 0.f ? mine / vref : 0.f;
-  }
+  dst[t] = rows >> (t >> 4) & 1u ? src[t] : 0.f;
+  dst[C::kTok + t] = vref > 0.f ? mine / vref : 0.f;
   if (t == 0) dst[2 * C::kTok] = vref;
   __syncwarp();
   if (lane == 0) mbar_arrive(&B.sc_full[n % kScaleSlots]);
 }
 
-// FP8.  A warp's load covers 16 codes x (8 lanes a row of 128, 4 of 64);
-// iteration i covers tokens 16 i .. 16 i + 15 (D 128) or 32 i .. 32 i + 31.
+// FP8: staged codes to f16 operands.  A thread takes 16 codes of a row at a
+// time (8 lanes a row of 128, 4 of 64).
 template <bool kFp8, int kD, int kTerms>
-__device__ __forceinline__ void loader_fp8(const PrefixArgs &a, uint8_t *smem, const PBars &B, const PrefixHdr &hdr,
-                                           volatile int *abort) {
+__device__ __forceinline__ void loader_fp8(const PrefixArgs &a, uint8_t *smem, const PBars &B, volatile int *abort) {
   using C = PCfg<kFp8, kD, kTerms>;
   constexpr int kLanes = kD / 16;                  // lanes a row
   constexpr int kRowsIt = 128 / kLanes;            // tokens per iteration
   constexpr int kIt = C::kTok / kRowsIt;
-  const int t = threadIdx.x - 8 * 32, lane = t & 31;
-  const int S = a.d.S, H = a.d.cache.num_kv_heads, c = t % kLanes, r_it = t / kLanes;
+  static_assert(C::kTok == 128, "one token per operand thread for the scales");
+  const PTile *tiles = reinterpret_cast<const PTile *>(smem + C::kOffItems + kItemSlots * sizeof(PItem));
+  const int t = threadIdx.x - 8 * 32, lane = t & 31, c = t % kLanes, r_it = t / kLanes;
   const bool per_token = a.d.scale_mode == PFKV_SCALE_PER_TOKEN;
-  const uint32_t s_ring = smem_addr(smem + C::kOffT);
+  const uint32_t s_ring = smem_addr(smem + C::kOffT), s_code = smem_addr(smem + C::kOffCode) + r_it * kD + 16 * c;
   // Where this thread's 16 values of its row go: two 16-byte chunks, 2c and
   // 2c + 1.  D 128: lanes 4-7 of a row write them in the other order, so that
   // eight lanes' stores meet different banks.
   const bool swap = kD == 128 && (c & 4);
   const int j0 = 2 * c + (swap ? 1 : 0), j1 = 2 * c + (swap ? 0 : 1);
-  PWalk w{range_start(hdr, blockIdx.x), range_start(hdr, blockIdx.x + 1), (int)blockIdx.x};
-  PItem it;
   const bool withhold = (a.d.flags & PFKV_FLAG_TEST_WITHHOLD) && blockIdx.x == 0;
-  uint32_t n = 0;  // tiles handed over
-  bool have = walk_next(a, w, it);
-  uint4 kr[kIt], vr[kIt];
-  float ks = 0.f, vs[C::kTok / 32] = {}, vref = 0.f;
-  // loads of the tile at token t0 of item q: which pages (one lane each), then rows
-  int pids = -1;
-  auto look_up = [&](const PItem &q, int t0) {
-    const int tok = t0 + 16 * lane;
-    pids = -1;
-    if (lane < C::kTok / 16 && tok < (q.p1 - q.p0) * S) {
-      const int p = __ldg(a.d.block_table + (size_t)a.members[q.first] * a.d.MP + q.p0 + tok / S);
-      if (p >= 0 && p < a.d.P) pids = p;
-    }
-  };
-  auto load = [&](const PItem &q, int t0, uint4 (&x)[kIt], const void *pool) {
+  float vref = 0.f;
+  for (uint32_t n = 0;; ++n) {
+    if (!mbar_wait_warp(&B.tile_full[n % kTileSlots], (n / kTileSlots) & 1u, abort)) return;
+    const int kind = tiles[n % kTileSlots].kind;
+    const uint32_t rows = tiles[n % kTileSlots].rows;
+    if (kind == 0) return;
+    if (kind == 2) vref = 0.f;
+#pragma unroll 1
+    for (int part = 0; part < 2; ++part) {
+      const uint32_t i = 2 * n + part, st = i % C::kStage, slot = i % C::kSlots;
+      if (!mbar_wait_warp(&B.code_full[st], (i / C::kStage) & 1u, abort)) return;
+      uint4 x[kIt];
 #pragma unroll
-    for (int i = 0; i < kIt; ++i) {
-      const int r = i * kRowsIt + r_it;
-      const int p = __shfl_sync(0xffffffffu, pids, r >> 4);
-      x[i] = make_uint4(0u, 0u, 0u, 0u);
-      if (p >= 0)
-        x[i] = *(reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(pool) +
-                                                 (((size_t)p * H + q.h) * S + (t0 + r) % S) * kD) + c);
-    }
-  };
-  auto load_scale = [&](const PItem &q, int t0) {
-    ks = 0.f;
-#pragma unroll
-    for (int i = 0; i < C::kTok / 32; ++i) {
-      const int r = 32 * i + lane, p = __shfl_sync(0xffffffffu, pids, r >> 4);
-      vs[i] = 0.f;
-      if (p >= 0) {
-        const size_t row = ((size_t)p * H + q.h) * S + (t0 + r) % S;
-        vs[i] = a.d.v_scale[row];
-        if (i == t >> 5) ks = a.d.k_scale[row];
+      for (int k = 0; k < kIt; ++k) {
+        const int r = k * kRowsIt + r_it;
+        x[k] = lds128(s_code + st * C::kCodeBytes + k * kRowsIt * kD);
+        if (!(rows >> (r >> 4) & 1u)) x[k] = make_uint4(0u, 0u, 0u, 0u);  // never copied: no NaN among what stands there
       }
-    }
-  };
-  auto store = [&](uint32_t slot, const uint4 (&x)[kIt]) {
-    const uint32_t base = s_ring + slot * C::kTBytes;
+      if (!mbar_wait_warp(&B.empty[slot], ((i / C::kSlots) & 1u) ^ 1u, abort)) return;
+      if (per_token && part == 0) hand_scales<C>(smem, B, n, st, rows, vref, t);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&B.code_empty[st]);
+      const uint32_t base = s_ring + slot * C::kTBytes;
 #pragma unroll
-    for (int i = 0; i < kIt; ++i) {
-      const int r = i * kRowsIt + r_it;
-      uint4 lo, hi;
-      e4m3x4_to_f16x4(x[i].x, lo.x, lo.y);
-      e4m3x4_to_f16x4(x[i].y, lo.z, lo.w);
-      e4m3x4_to_f16x4(x[i].z, hi.x, hi.y);
-      e4m3x4_to_f16x4(x[i].w, hi.z, hi.w);
-      const uint32_t row = base + r * 128;
-      sts128(row + (j0 >> 3) * C::kBlkT + (((j0 & 7) ^ (r & 7)) << 4), swap ? hi : lo);
-      sts128(row + (j1 >> 3) * C::kBlkT + (((j1 & 7) ^ (r & 7)) << 4), swap ? lo : hi);
-    }
-    fence_async_smem();
-    __syncwarp();
-  };
-  if (have) {
-    look_up(it, 0);
-    load(it, 0, kr, a.d.k_pool);
-    load(it, 0, vr, a.d.v_pool);
-    if (per_token) load_scale(it, 0);
-  }
-  while (have) {
-    const int n_tok = (it.p1 - it.p0) * S;
-    vref = 0.f;
-    for (int t0 = 0; t0 < n_tok; t0 += C::kTok, ++n) {
-      // the tile after this one, of this item or the next
-      PItem nx = it;
-      int nt = t0 + C::kTok;
-      bool more = true;
-      if (nt >= n_tok) {
-        more = walk_next(a, w, nx);
-        nt = 0;
+      for (int k = 0; k < kIt; ++k) {
+        const int r = k * kRowsIt + r_it;
+        uint4 lo, hi;
+        e4m3x4_to_f16x4(x[k].x, lo.x, lo.y);
+        e4m3x4_to_f16x4(x[k].y, lo.z, lo.w);
+        e4m3x4_to_f16x4(x[k].z, hi.x, hi.y);
+        e4m3x4_to_f16x4(x[k].w, hi.z, hi.w);
+        const uint32_t row = base + r * 128;
+        sts128(row + (j0 >> 3) * C::kBlkT + (((j0 & 7) ^ (r & 7)) << 4), swap ? hi : lo);
+        sts128(row + (j1 >> 3) * C::kBlkT + (((j1 & 7) ^ (r & 7)) << 4), swap ? lo : hi);
       }
-      const uint32_t ik = 2 * n, sk = ik % kSlots, sv = (ik + 1) % kSlots, ph = ((ik / kSlots) & 1u) ^ 1u;
-      if (!mbar_wait_warp(&B.empty[sk], ph, abort)) return;
-      if (per_token) hand_scales<C>(smem, B, n, ks, vs, vref, t);
-      store(sk, kr);
+      fence_async_smem();
+      __syncwarp();
       // test hook: the first CTA never hands its first tile over, and the other warps' bounded waits give up
-      if (withhold && n == 0) return;
-      if (lane == 0) mbar_arrive(&B.full[sk]);
-      if (more) {
-        look_up(nx, nt);
-        load(nx, nt, kr, a.d.k_pool);
-        if (per_token) load_scale(nx, nt);
-      }
-      if (!mbar_wait_warp(&B.empty[sv], ph, abort)) return;
-      store(sv, vr);
-      if (lane == 0) mbar_arrive(&B.full[sv]);
-      if (more) load(nx, nt, vr, a.d.v_pool);
-      if (nt == 0) {
-        it = nx;
-        have = more;
-      }
+      if (withhold && i == 0) return;
+      if (lane == 0) mbar_arrive(&B.full[slot]);
     }
+    if (lane == 0) mbar_arrive(&B.tile_empty[n % kTileSlots]);
   }
 }
 
 // BF16: copies straight into the operand layout, two tiles in flight.
 template <bool kFp8, int kD, int kTerms>
-__device__ __forceinline__ void loader_bf16(const PrefixArgs &a, uint8_t *smem, const PBars &B, const PrefixHdr &hdr,
-                                            volatile int *abort) {
+__device__ __forceinline__ void loader_bf16(const PrefixArgs &a, uint8_t *smem, const PBars &B, volatile int *abort) {
   using C = PCfg<kFp8, kD, kTerms>;
   constexpr int kLanes = kD / 8, kRowsIt = 128 / kLanes, kIt = C::kTok / kRowsIt;
-  const int t = threadIdx.x - 8 * 32, lane = t & 31;
-  const int S = a.d.S, H = a.d.cache.num_kv_heads, c = t % kLanes, r_it = t / kLanes;
+  const PTile *tiles = reinterpret_cast<const PTile *>(smem + C::kOffItems + kItemSlots * sizeof(PItem));
+  const int t = threadIdx.x - 8 * 32, lane = t & 31, c = t % kLanes, r_it = t / kLanes;
   const uint32_t s_ring = smem_addr(smem + C::kOffT);
-  PWalk w{range_start(hdr, blockIdx.x), range_start(hdr, blockIdx.x + 1), (int)blockIdx.x};
-  PItem it;
   const bool withhold = (a.d.flags & PFKV_FLAG_TEST_WITHHOLD) && blockIdx.x == 0;
-  uint32_t n = 0;  // tiles issued (K and V counted apart); tile n - 2 is handed over when tile n is issued
+  uint32_t n = 0;  // copies issued (K and V counted apart); copy n - 2 is handed over when copy n is issued
   auto hand_over = [&](uint32_t i) {
     fence_async_smem();
     __syncwarp();
-    if (lane == 0) mbar_arrive(&B.full[i % kSlots]);
+    if (lane == 0) mbar_arrive(&B.full[i % C::kSlots]);
   };
-  while (walk_next(a, w, it)) {
-    const int n_tok = (it.p1 - it.p0) * S;
-    for (int t0 = 0; t0 < n_tok; t0 += C::kTok) {
-      int pids = -1;
-      const int tok = t0 + 16 * lane;
-      if (lane < C::kTok / 16 && tok < n_tok) {
-        const int p = __ldg(a.d.block_table + (size_t)a.members[it.first] * a.d.MP + it.p0 + tok / S);
-        if (p >= 0 && p < a.d.P) pids = p;
+  for (uint32_t m = 0;; ++m) {
+    if (!mbar_wait_warp(&B.tile_full[m % kTileSlots], (m / kTileSlots) & 1u, abort)) break;
+    const PTile &d = tiles[m % kTileSlots];
+    if (d.kind == 0) {
+      cp_async_wait<0>();
+      if (n >= 2 && !(withhold && n == 2)) {
+        hand_over(n - 2);
+        hand_over(n - 1);
       }
+      return;
+    }
 #pragma unroll
-      for (int part = 0; part < 2; ++part, ++n) {
-        if (!mbar_wait_warp(&B.empty[n % kSlots], ((n / kSlots) & 1u) ^ 1u, abort)) {
+    for (int part = 0; part < 2; ++part, ++n) {
+      if (!mbar_wait_warp(&B.empty[n % C::kSlots], ((n / C::kSlots) & 1u) ^ 1u, abort)) {
+        cp_async_wait<0>();
+        return;
+      }
+      const uint32_t base = s_ring + (n % C::kSlots) * C::kTBytes;
+      const uint8_t *pool = static_cast<const uint8_t *>(part ? a.d.v_pool : a.d.k_pool);
+#pragma unroll
+      for (int i = 0; i < kIt; ++i) {
+        const int r = i * kRowsIt + r_it;
+        const long long row = d.row[r >> 4];
+        cp_async16(base + (c >> 3) * C::kBlkT + r * 128 + (((c & 7) ^ (r & 7)) << 4),
+                   pool + (row >= 0 ? row + (r & 15) : 0) * (2 * kD) + 16 * c, row >= 0);
+      }
+      cp_async_commit();
+      if (n >= 2) {
+        cp_async_wait<2>();
+        if (withhold && n == 2) {  // test hook, as in the FP8 loader
           cp_async_wait<0>();
           return;
         }
-        const uint32_t base = s_ring + (n % kSlots) * C::kTBytes;
-        const uint8_t *pool = static_cast<const uint8_t *>(part ? a.d.v_pool : a.d.k_pool);
-#pragma unroll
-        for (int i = 0; i < kIt; ++i) {
-          const int r = i * kRowsIt + r_it;
-          const int p = __shfl_sync(0xffffffffu, pids, r >> 4);
-          cp_async16(base + (c >> 3) * C::kBlkT + r * 128 + (((c & 7) ^ (r & 7)) << 4),
-                     pool + (((size_t)max(p, 0) * H + it.h) * S + (t0 + r) % S) * (2 * kD) + 16 * c, p >= 0);
-        }
-        cp_async_commit();
-        if (n >= 2) {
-          cp_async_wait<2>();
-          if (withhold && n == 2) {  // test hook, as in the FP8 loader
-            cp_async_wait<0>();
-            return;
-          }
-          hand_over(n - 2);
-        }
+        hand_over(n - 2);
       }
     }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&B.tile_empty[m % kTileSlots]);
   }
   cp_async_wait<0>();
-  if (n >= 2) {
-    if (withhold && n == 2) return;
-    hand_over(n - 2);
-    hand_over(n - 1);
-  }
 }
 
 // ---------------------------------------------------------------- MMA issuer (warp 12, one thread)
@@ -342,26 +423,29 @@ __device__ __forceinline__ void loader_bf16(const PrefixArgs &a, uint8_t *smem, 
 // a half's S is overwritten only after its P, which lies over it, was read by
 // the PV issued before.
 template <bool kFp8, int kD, int kTerms>
-__device__ __forceinline__ void issue_mmas(const PrefixArgs &a, uint8_t *smem, const PBars &B, const PrefixHdr &hdr,
-                                           uint32_t tmem, volatile int *abort) {
+__device__ __forceinline__ void issue_mmas(const PrefixArgs &a, uint8_t *smem, const PBars &B, uint32_t tmem,
+                                           volatile int *abort) {
   using C = PCfg<kFp8, kD, kTerms>;
   const int S = a.d.S;
   const uint64_t dq = umma_sdesc(smem_addr(smem + C::kOffQ), 16, 1024, 2);
   const uint64_t dk = umma_sdesc(smem_addr(smem + C::kOffT), 16, 1024, 2);
   const uint64_t dv = umma_sdesc(smem_addr(smem + C::kOffT), C::kBlkT, 1024, 2);
-  PWalk w{range_start(hdr, blockIdx.x), range_start(hdr, blockIdx.x + 1), (int)blockIdx.x};
-  PItem it;
-  uint32_t base = 0, items = 0;  // tiles before this item
+  uint32_t base = 0;  // tiles before this item
   uint32_t pc[2][C::kChunks] = {};
   bool ok = true;
-  for (; ok && walk_next(a, w, it); ++items) {
+  for (uint32_t items = 0; ok; ++items) {
+    ok = mbar_wait(&B.item_full[items % kItemSlots], (items / kItemSlots) & 1u, abort);
+    if (!ok) break;
+    const PItem it = reinterpret_cast<const PItem *>(smem + C::kOffItems)[items % kItemSlots];
+    mbar_arrive(&B.item_empty[items % kItemSlots]);
+    if (it.n_rows == 0) break;
     const int n_tok = (it.p1 - it.p0) * S;
     const int tiles = (n_tok + C::kTok - 1) / C::kTok, units = it.split ? tiles : 2 * tiles;
     for (int t = 0; t < 2 && ok; ++t) ok = mbar_wait(&B.q_ready[t], items & 1u, abort);
     auto qk = [&](int u) {
       const int t = u & 1;
-      const uint32_t ik = 2 * (base + (uint32_t)(it.split ? u : u >> 1)), slot = ik % kSlots;
-      ok = mbar_wait(&B.full[slot], (ik / kSlots) & 1u, abort);
+      const uint32_t ik = 2 * (base + (uint32_t)(it.split ? u : u >> 1)), slot = ik % C::kSlots;
+      ok = mbar_wait(&B.full[slot], (ik / C::kSlots) & 1u, abort);
       if (!ok) return;
       tc_fence_after();
 #pragma unroll
@@ -378,9 +462,9 @@ __device__ __forceinline__ void issue_mmas(const PrefixArgs &a, uint8_t *smem, c
     if (units == 1 && ok) umma_commit(&B.s_full[1]);  // half 1 has no tile; see its wait
     for (int u = 0; u < units && ok; ++u) {
       const int t = u & 1, tile = it.split ? u : u >> 1;
-      const uint32_t iv = 2 * (base + (uint32_t)tile) + 1, slot = iv % kSlots;
+      const uint32_t iv = 2 * (base + (uint32_t)tile) + 1, slot = iv % C::kSlots;
       const int chunks = (min(C::kTok, n_tok - tile * C::kTok) + 63) / 64;
-      ok = mbar_wait(&B.full[slot], (iv / kSlots) & 1u, abort);
+      ok = mbar_wait(&B.full[slot], (iv / C::kSlots) & 1u, abort);
 #pragma unroll
       for (int c = 0; c < C::kChunks; ++c) {
         if (c >= chunks || !ok) break;
@@ -414,8 +498,8 @@ __device__ __forceinline__ void issue_mmas(const PrefixArgs &a, uint8_t *smem, c
 // ---------------------------------------------------------------- softmax (warps 0-7)
 
 template <bool kFp8, int kD, int kTerms>
-__device__ __forceinline__ void softmax_rows(const PrefixArgs &a, uint8_t *smem, const PBars &B, const PrefixHdr &hdr,
-                                             uint32_t tmem, volatile int *abort) {
+__device__ __forceinline__ void softmax_rows(const PrefixArgs &a, uint8_t *smem, const PBars &B, uint32_t tmem,
+                                             volatile int *abort) {
   using C = PCfg<kFp8, kD, kTerms>;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int t = warp >> 2, r = (warp & 3) * 32 + lane;  // half, row of it
@@ -423,10 +507,13 @@ __device__ __forceinline__ void softmax_rows(const PrefixArgs &a, uint8_t *smem,
   const uint32_t tq = tmem + ((uint32_t)((warp & 3) * 32) << 16);
   const uint32_t col_s = tq + C::kColS + t * C::kTok, col_o = tq + C::kColO + 128 * t;
   const int S = a.d.S;
-  PWalk w{range_start(hdr, blockIdx.x), range_start(hdr, blockIdx.x + 1), (int)blockIdx.x};
-  PItem it;
   uint32_t base = 0, n_s = 0, n_pv[2] = {0, 0};  // tiles, units, and units' first and second chunks before
-  while (walk_next(a, w, it)) {
+  for (uint32_t items = 0;; ++items) {
+    if (!mbar_wait_warp(&B.item_full[items % kItemSlots], (items / kItemSlots) & 1u, abort)) return;
+    const PItem it = reinterpret_cast<const PItem *>(smem + C::kOffItems)[items % kItemSlots];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&B.item_empty[items % kItemSlots]);
+    if (it.n_rows == 0) return;
     const int n_tok = (it.p1 - it.p0) * S;
     const int tiles = (n_tok + C::kTok - 1) / C::kTok, units = it.split ? tiles : 2 * tiles;
     const int row = it.split ? r : t * (kRows / 2) + r;  // row of the item's block
@@ -634,9 +721,11 @@ __global__ void __launch_bounds__(kPThreads, 1) prefix_kernel(const PrefixArgs a
   const PBars B = pbars_at(smem + C::kOffBars);
   const int warp = threadIdx.x >> 5;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kSlots; ++i) {
+    for (int i = 0; i < kMaxSlots; ++i) {
       mbar_init(&B.full[i], 4);
       mbar_init(&B.empty[i], 1);
+      mbar_init(&B.code_full[i], 1);
+      mbar_init(&B.code_empty[i], 4);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&B.s_full[i], 1);
@@ -647,6 +736,14 @@ __global__ void __launch_bounds__(kPThreads, 1) prefix_kernel(const PrefixArgs a
       mbar_init(&B.pv_done[i], 1);
     }
     for (int i = 0; i < kScaleSlots; ++i) mbar_init(&B.sc_full[i], 4);
+    for (int i = 0; i < kItemSlots; ++i) {
+      mbar_init(&B.item_full[i], 1);
+      mbar_init(&B.item_empty[i], 9);  // eight softmax warps and the issuer
+    }
+    for (int i = 0; i < kTileSlots; ++i) {
+      mbar_init(&B.tile_full[i], 1);
+      mbar_init(&B.tile_empty[i], 4);
+    }
     mbar_init(B.drain, 1);
     s_abort = 0;
     mbar_init_fence();
@@ -662,12 +759,19 @@ __global__ void __launch_bounds__(kPThreads, 1) prefix_kernel(const PrefixArgs a
   const PrefixHdr hdr = *a.hdr;
   if ((int)blockIdx.x < hdr.R) {
     if (warp < 8) {
-      softmax_rows<kFp8, kD, kTerms>(a, smem, B, hdr, tmem, abort);
+      regs_inc<kRegsSoftmax>();
+      softmax_rows<kFp8, kD, kTerms>(a, smem, B, tmem, abort);
     } else if (warp < 12) {
-      if constexpr (kFp8) loader_fp8<kFp8, kD, kTerms>(a, smem, B, hdr, abort);
-      else loader_bf16<kFp8, kD, kTerms>(a, smem, B, hdr, abort);
-    } else if ((threadIdx.x & 31) == 0) {
-      issue_mmas<kFp8, kD, kTerms>(a, smem, B, hdr, tmem, abort);
+      regs_dec<kRegsLoader>();
+      if constexpr (kFp8) loader_fp8<kFp8, kD, kTerms>(a, smem, B, abort);
+      else loader_bf16<kFp8, kD, kTerms>(a, smem, B, abort);
+    } else {
+      regs_dec<kRegsRest>();
+      if (warp == 12) {
+        if ((threadIdx.x & 31) == 0) issue_mmas<kFp8, kD, kTerms>(a, smem, B, tmem, abort);
+      } else if (warp == 13) {
+        plan_tiles<kFp8, kD, kTerms>(a, smem, B, hdr, abort);
+      }
     }
   }
   __syncwarp();
