@@ -2,8 +2,8 @@
 // the fifth-generation tensor cores (kernel 2 of prefix_attn.cu).
 //
 // One item is up to 256 query rows of one (group, KV head) over the group's
-// pages, a piece a range of those pages; per tile of kTok tokens
-//   S = Q K^T   (M = 128 rows, N = kTok, fp32 in tensor memory)
+// pages, a piece a range of those pages; per unit of 128 rows and 64 tokens
+//   S = Q K^T   (M = 128, N = 64, fp32 in tensor memory)
 //   P = 2^(tau log2(e) S - m)
 //   O += P V    (M = 128, N = head_dim; P from tensor memory)
 // with 16-bit operands (f16 for an FP8 cache, whose codes convert exactly,
@@ -12,31 +12,32 @@
 // many a call takes.
 //
 // What bounds it: a KV byte of an FP8 cache meets 2 x rows products, so from
-// about 150 rows on the tensor cores, not HBM.  Per tile of 128 tokens and 256
-// rows (head_dim 128, one term) the products are 2048 cycles of one SM; the
-// exponentials 1024 to 2048 and the shared-memory traffic (operand reads 1536,
-// converted tiles 512) have to hide behind them.  Hence: one CTA per SM, and
+// about 150 rows on the tensor cores, not HBM.  Between a unit's products lies
+// its softmax, whose latency (hand-over, tensor-memory reads and writes,
+// exponentials) is longer than the products; so each row half keeps two score
+// buffers, the next unit's QK^T runs while this one's softmax does, and PV
+// follows when it can.  One CTA per SM:
 //   warps 0-3, 4-7  softmax of row half 0 and 1: a thread owns a row, so that
 //                   maxima and sums need no exchange; P overwrites S.
-//   warps 8-11      operands, in a ring of K and V tiles in the 128-byte-
-//                   swizzled layout.  FP8: e4m3 -> f16 from staged codes,
-//                   once per CTA.  BF16: asynchronous copies from the pool,
-//                   two tiles ahead.
-//   warp 12         issues the MMAs.  The two halves alternate, so that one
-//                   half's products run while the other's softmax does.
+//   warps 8-11      operands, in a ring of K and V tiles of 128 tokens in the
+//                   128-byte-swizzled layout.  FP8: e4m3 -> f16 from staged
+//                   codes, once per CTA.  BF16: asynchronous copies from the
+//                   pool, two tiles ahead.
+//   warps 12, 14    issue the MMAs of QK^T and of PV, a thread each.
 //   warp 13         planner: works out the CTA's items and where each tile's
 //                   rows lie (bounds-checked page ids), so that nobody else
 //                   waits for a table entry; FP8: bulk-copies the codes into
 //                   a staging ring of three tiles (48 KB in flight).
 // An item of more than 128 rows has 128 in each half, over the same tokens.
-// One of at most 128 rows gives both halves the same rows and alternate tiles
-// of the tokens; each half then leaves a partial result of its own.
+// One of at most 128 rows gives both halves the same rows, half 0 the first 64
+// tokens of each tile and half 1 the others; each half then leaves a partial
+// result of its own.
 //
-// The running maximum m of a row moves only when a 64-token chunk exceeds it by
-// more than 2^8 (log2 units: 8), which after the first chunk is rare; O is then
+// The running maximum m of a row moves only when a unit exceeds it by more
+// than 2^8 (log2 units: 8), which after the first unit is rare; O is then
 // rescaled in tensor memory by the row's own softmax warp, after the products
 // it has handed over and before the next.  Probabilities are carried with a
-// factor 2^kShift, so that those down to 2^-21 of the reference stay normal in
+// factor 2^kShift, so that those down to 2^-20 of the reference stay normal in
 // f16; l has the same factor, so the quotient does not see it.
 #pragma once
 
@@ -45,7 +46,7 @@
 namespace pfkv {
 namespace {
 
-constexpr int kPThreads = 16 * 32;  // four warpgroups; warps 14 and 15 only lend their registers
+constexpr int kPThreads = 16 * 32;  // four warpgroups; warp 15 only lends its registers
 constexpr int kScaleSlots = 4;   // tiles whose per-token scales are kept
 constexpr int kItemSlots = 4;    // items announced ahead
 constexpr int kTileSlots = 8;    // tiles announced ahead
@@ -61,7 +62,7 @@ constexpr float kGrow = 8.f;     // growth of a row's maximum that moves its ref
 struct PItem {
   int first, row0, n_rows, h, p0, p1;
   long long slot;
-  int split;  // at most 128 rows: the halves take alternate tiles
+  int split;  // at most 128 rows: each half takes 64 tokens of a tile
   int pad;
 };
 static_assert(sizeof(PItem) == 40, "item slot");
@@ -76,20 +77,22 @@ struct PTile {
 };
 static_assert(sizeof(PTile) == 72, "tile slot");
 
+constexpr int kTok = 128;  // tokens per tile
+
 template <bool kFp8, int kD, int kTerms>
 struct PCfg {
-  static constexpr int kTok = kTerms == 3 ? 64 : 128;  // tokens per tile (tensor memory bounds it)
-  static constexpr int kChunks = kTok / 64;
-  static constexpr int kSlots = kFp8 && kD == 128 ? 3 : 4;  // operand ring: K, V, K, V, ...
-  static constexpr int kStage = kFp8 ? 3 : 0;               // staged code tiles
+  static constexpr int kBufs = kTerms == 3 && kD == 128 ? 1 : 2;  // score buffers per half (tensor memory bounds it)
+  static constexpr int kSlots = kFp8 && kD == 128 ? 3 : 4;        // operand ring: K, V, K, V, ...
+  static constexpr int kStage = kFp8 ? 3 : 0;                     // staged code tiles
+  static constexpr uint32_t kBlk = 128 * 128;                     // 64 dims of a query half or of a tile
+  static constexpr uint32_t kQBytes = kBlk * (kD / 64), kTBytes = kQBytes;
   static constexpr uint32_t kCodeBytes = kTok * kD;
-  static constexpr uint32_t kBlkQ = 128 * 128;          // 64 dims of a query half
-  static constexpr uint32_t kQBytes = kBlkQ * (kD / 64);
-  static constexpr uint32_t kBlkT = kTok * 128;         // 64 dims of a tile
-  static constexpr uint32_t kTBytes = kBlkT * (kD / 64);
-  // tensor memory columns: S (and P over it), the third term, O
-  static constexpr uint32_t kColS = 0, kColX = 2 * kTok, kColO = 256;
-  // per-token mode: v scales relative to a running reference, at most twice it
+  // tensor memory: score buffers (P lies over its scores), third terms, O
+  __host__ __device__ static constexpr uint32_t col_s(int t, int b) { return (uint32_t)(t * kBufs + b) * 64; }
+  __host__ __device__ static constexpr uint32_t col_x(int t, int b) { return 128 * kBufs + (uint32_t)(t * kBufs + b) * 32; }
+  __host__ __device__ static constexpr uint32_t col_o(int t) { return 512 - (uint32_t)(2 - t) * kD; }
+  static_assert((kTerms == 3 ? 192 : 128) * kBufs + 2 * kD <= 512, "tensor memory plan");
+  // per-token mode: V scales relative to a running reference, at most twice it
   static constexpr float kShift = kFp8 ? 6.f : 0.f;
   static constexpr uint32_t kOffQ = 0, kOffT = 2 * kQBytes, kOffCode = kOffT + kSlots * kTBytes;
   static constexpr uint32_t kOffCodeScale = kOffCode + kStage * kCodeBytes;  // K and V scales beside the codes of K
@@ -97,7 +100,7 @@ struct PCfg {
   static constexpr uint32_t kOffBars = kOffScale + kScaleSlots * (2 * kTok * 4 + 16);
   static constexpr uint32_t kOffItems = kOffBars + 8 * 64;
   static constexpr uint32_t kTotal = kOffItems + kItemSlots * sizeof(PItem) + kTileSlots * sizeof(PTile) + 1024;
-  static constexpr uint32_t kIdQK = umma_idesc_f16(128, kTok, !kFp8, 0, 0);
+  static constexpr uint32_t kIdQK = umma_idesc_f16(128, 64, !kFp8, 0, 0);
   static constexpr uint32_t kIdPV = umma_idesc_f16(128, kD, !kFp8, 0, 1);
   static_assert(kTotal <= 232448, "shared memory plan exceeds one SM");
 };
@@ -134,11 +137,11 @@ constexpr int kMaxSlots = 4;
 struct PBars {
   uint64_t *full, *empty;              // operand ring
   uint64_t *code_full, *code_empty;    // staging ring
-  uint64_t *s_full, *q_ready;          // per half
-  uint64_t *p_full, *pv_done;          // per half and chunk
+  uint64_t *q_ready, *q_read;             // per half
+  uint64_t *s_full, *p_full, *pv_done;    // per half and score buffer
   uint64_t *sc_full;                   // per-token scales
   uint64_t *item_full, *item_empty, *tile_full, *tile_empty;
-  uint64_t *drain;
+  uint64_t *drain;  // one per issuing thread
 };
 
 __device__ __forceinline__ PBars pbars_at(uint8_t *base) {
@@ -148,10 +151,11 @@ __device__ __forceinline__ PBars pbars_at(uint8_t *base) {
   r.empty = b; b += kMaxSlots;
   r.code_full = b; b += kMaxSlots;
   r.code_empty = b; b += kMaxSlots;
-  r.s_full = b; b += 2;
+  r.q_ready = b; b += 2;
+  r.q_read = b; b += 2;
+  r.s_full = b; b += 4;
   r.p_full = b; b += 4;
   r.pv_done = b; b += 4;
-  r.q_ready = b; b += 2;
   r.sc_full = b; b += kScaleSlots;
   r.item_full = b; b += kItemSlots;
   r.item_empty = b; b += kItemSlots;
@@ -193,9 +197,9 @@ __device__ __forceinline__ bool stage_codes(const PrefixArgs &a, uint8_t *smem, 
     const uint8_t *pool = static_cast<const uint8_t *>(part ? a.d.v_pool : a.d.k_pool);
     bulk_load(smem + C::kOffCode + s * C::kCodeBytes + lane * 16 * kD, pool + row * kD, 16 * kD, &B.code_full[s]);
     if (per_token && part == 0) {
-      float *dst = reinterpret_cast<float *>(smem + C::kOffCodeScale) + s * 2 * C::kTok + 16 * lane;
+      float *dst = reinterpret_cast<float *>(smem + C::kOffCodeScale) + s * 2 * kTok + 16 * lane;
       bulk_load(dst, a.d.k_scale + row, 64, &B.code_full[s]);
-      bulk_load(dst + C::kTok, a.d.v_scale + row, 64, &B.code_full[s]);
+      bulk_load(dst + kTok, a.d.v_scale + row, 64, &B.code_full[s]);
     }
   }
   return true;
@@ -209,7 +213,7 @@ __device__ __forceinline__ void plan_tiles(const PrefixArgs &a, uint8_t *smem, c
   PTile *tiles = reinterpret_cast<PTile *>(smem + C::kOffItems + kItemSlots * sizeof(PItem));
   const int lane = threadIdx.x & 31, S = a.d.S, H = a.d.cache.num_kv_heads;
   const bool per_token = kFp8 && a.d.scale_mode == PFKV_SCALE_PER_TOKEN;
-  constexpr int kGroups = C::kTok / 16, kAtOnce = 32 / kGroups;  // 16-token groups of a tile; tiles per look-up
+  constexpr int kGroups = kTok / 16, kAtOnce = 32 / kGroups;  // 16-token groups of a tile; tiles per look-up
   PWalk w{range_start(hdr, blockIdx.x), range_start(hdr, blockIdx.x + 1), (int)blockIdx.x};
   uint32_t n = 0;
   bool ok = true;
@@ -228,12 +232,12 @@ __device__ __forceinline__ void plan_tiles(const PrefixArgs &a, uint8_t *smem, c
       return have && tok < n_tok ? __ldg(trow + tok / S) : -1;
     };
     int next = look_up(0);
-    for (int t0 = 0; t0 < n_tok && ok; t0 += kAtOnce * C::kTok) {
+    for (int t0 = 0; t0 < n_tok && ok; t0 += kAtOnce * kTok) {
       const int p = next;
-      next = look_up(t0 + kAtOnce * C::kTok);  // on its way while this batch goes out
+      next = look_up(t0 + kAtOnce * kTok);  // on its way while this batch goes out
       const bool fine = p >= 0 && p < a.d.P;
       const uint32_t rows = __ballot_sync(0xffffffffu, fine);
-      for (int k = 0; k < kAtOnce && t0 + k * C::kTok < n_tok; ++k, ++n) {
+      for (int k = 0; k < kAtOnce && t0 + k * kTok < n_tok; ++k, ++n) {
         PTile &d = tiles[n % kTileSlots];
         ok = mbar_wait_warp(&B.tile_empty[n % kTileSlots], ((n / kTileSlots) & 1u) ^ 1u, abort);
         if (!ok) break;
@@ -275,22 +279,22 @@ __device__ __forceinline__ void plan_tiles(const PrefixArgs &a, uint8_t *smem, c
 template <typename C>
 __device__ __forceinline__ void hand_scales(uint8_t *smem, const PBars &B, uint32_t n, uint32_t stage, uint32_t rows,
                                             float &vref, int t) {
-  float *dst = reinterpret_cast<float *>(smem + C::kOffScale) + (n % kScaleSlots) * (2 * C::kTok + 4);
-  const float *src = reinterpret_cast<const float *>(smem + C::kOffCodeScale) + stage * 2 * C::kTok;
+  float *dst = reinterpret_cast<float *>(smem + C::kOffScale) + (n % kScaleSlots) * (2 * kTok + 4);
+  const float *src = reinterpret_cast<const float *>(smem + C::kOffCodeScale) + stage * 2 * kTok;
   const int lane = t & 31, warp = t >> 5;
   float mx = 0.f, mine = 0.f;
 #pragma unroll
-  for (int i = 0; i < C::kTok / 32; ++i) {
+  for (int i = 0; i < kTok / 32; ++i) {
     const int r = 32 * i + lane;
-    const float v = rows >> (r >> 4) & 1u ? src[C::kTok + r] : 0.f;
+    const float v = rows >> (r >> 4) & 1u ? src[kTok + r] : 0.f;
     mx = fmaxf(mx, v);
     if (i == warp) mine = v;
   }
   mx = warp_max_f32(mx);
   if (mx > 2.f * vref) vref = mx;
   dst[t] = rows >> (t >> 4) & 1u ? src[t] : 0.f;
-  dst[C::kTok + t] = vref > 0.f ? mine / vref : 0.f;
-  if (t == 0) dst[2 * C::kTok] = vref;
+  dst[kTok + t] = vref > 0.f ? mine / vref : 0.f;
+  if (t == 0) dst[2 * kTok] = vref;
   __syncwarp();
   if (lane == 0) mbar_arrive(&B.sc_full[n % kScaleSlots]);
 }
@@ -302,8 +306,8 @@ __device__ __forceinline__ void loader_fp8(const PrefixArgs &a, uint8_t *smem, c
   using C = PCfg<kFp8, kD, kTerms>;
   constexpr int kLanes = kD / 16;                  // lanes a row
   constexpr int kRowsIt = 128 / kLanes;            // tokens per iteration
-  constexpr int kIt = C::kTok / kRowsIt;
-  static_assert(C::kTok == 128, "one token per operand thread for the scales");
+  constexpr int kIt = kTok / kRowsIt;
+  static_assert(kTok == 128, "one token per operand thread for the scales");
   const PTile *tiles = reinterpret_cast<const PTile *>(smem + C::kOffItems + kItemSlots * sizeof(PItem));
   const int t = threadIdx.x - 8 * 32, lane = t & 31, c = t % kLanes, r_it = t / kLanes;
   const bool per_token = a.d.scale_mode == PFKV_SCALE_PER_TOKEN;
@@ -346,8 +350,8 @@ __device__ __forceinline__ void loader_fp8(const PrefixArgs &a, uint8_t *smem, c
         e4m3x4_to_f16x4(x[k].z, hi.x, hi.y);
         e4m3x4_to_f16x4(x[k].w, hi.z, hi.w);
         const uint32_t row = base + r * 128;
-        sts128(row + (j0 >> 3) * C::kBlkT + (((j0 & 7) ^ (r & 7)) << 4), swap ? hi : lo);
-        sts128(row + (j1 >> 3) * C::kBlkT + (((j1 & 7) ^ (r & 7)) << 4), swap ? lo : hi);
+        sts128(row + (j0 >> 3) * C::kBlk + (((j0 & 7) ^ (r & 7)) << 4), swap ? hi : lo);
+        sts128(row + (j1 >> 3) * C::kBlk + (((j1 & 7) ^ (r & 7)) << 4), swap ? lo : hi);
       }
       fence_async_smem();
       __syncwarp();
@@ -363,7 +367,7 @@ __device__ __forceinline__ void loader_fp8(const PrefixArgs &a, uint8_t *smem, c
 template <bool kFp8, int kD, int kTerms>
 __device__ __forceinline__ void loader_bf16(const PrefixArgs &a, uint8_t *smem, const PBars &B, volatile int *abort) {
   using C = PCfg<kFp8, kD, kTerms>;
-  constexpr int kLanes = kD / 8, kRowsIt = 128 / kLanes, kIt = C::kTok / kRowsIt;
+  constexpr int kLanes = kD / 8, kRowsIt = 128 / kLanes, kIt = kTok / kRowsIt;
   const PTile *tiles = reinterpret_cast<const PTile *>(smem + C::kOffItems + kItemSlots * sizeof(PItem));
   const int t = threadIdx.x - 8 * 32, lane = t & 31, c = t % kLanes, r_it = t / kLanes;
   const uint32_t s_ring = smem_addr(smem + C::kOffT);
@@ -397,7 +401,7 @@ __device__ __forceinline__ void loader_bf16(const PrefixArgs &a, uint8_t *smem, 
       for (int i = 0; i < kIt; ++i) {
         const int r = i * kRowsIt + r_it;
         const long long row = d.row[r >> 4];
-        cp_async16(base + (c >> 3) * C::kBlkT + r * 128 + (((c & 7) ^ (r & 7)) << 4),
+        cp_async16(base + (c >> 3) * C::kBlk + r * 128 + (((c & 7) ^ (r & 7)) << 4),
                    pool + (row >= 0 ? row + (r & 15) : 0) * (2 * kD) + 16 * c, row >= 0);
       }
       cp_async_commit();
@@ -416,83 +420,114 @@ __device__ __forceinline__ void loader_bf16(const PrefixArgs &a, uint8_t *smem, 
   cp_async_wait<0>();
 }
 
-// ---------------------------------------------------------------- MMA issuer (warp 12, one thread)
+// ---------------------------------------------------------------- MMA issuers (warps 12 and 14, one thread each)
 
-// Unit u of an item is one half's tile: half u & 1, tile u / 2 (both halves
-// over the same tokens) or u (split).  Order QK(0) QK(1), then PV(u) QK(u + 2):
-// a half's S is overwritten only after its P, which lies over it, was read by
-// the PV issued before.
+// A half's unit is 64 tokens of a tile; the units of a tile in the order
+// (64 tokens, half), in split mode half t takes the t-th 64 tokens.  Unit u of
+// a half has score buffer u % kBufs.
+
+// Waits, bounded, until every MMA this thread issued has completed (before
+// tensor memory is released).
+__device__ __forceinline__ void drain_mmas(uint64_t *bar) {
+  umma_commit(bar);
+  const uint64_t t0 = global_timer_ns();
+  while (!mbar_try_wait(bar, 0))
+    if (global_timer_ns() - t0 > kWaitLimitNs) break;
+}
+
+// Item of a ring slot; the caller has released it afterwards.  False: no more
+// work, or a wait gave up.
+template <typename C>
+__device__ __forceinline__ bool next_item(uint8_t *smem, const PBars &B, uint32_t i, PItem &it, volatile int *abort) {
+  if (!mbar_wait(&B.item_full[i % kItemSlots], (i / kItemSlots) & 1u, abort)) return false;
+  it = reinterpret_cast<const PItem *>(smem + C::kOffItems)[i % kItemSlots];
+  mbar_arrive(&B.item_empty[i % kItemSlots]);
+  return it.n_rows != 0;
+}
+
+// S[t][b] = Q_t K^T, once the PV that last read P from the buffer is done.
 template <bool kFp8, int kD, int kTerms>
-__device__ __forceinline__ void issue_mmas(const PrefixArgs &a, uint8_t *smem, const PBars &B, uint32_t tmem,
-                                           volatile int *abort) {
+__device__ __forceinline__ void issue_qk(const PrefixArgs &a, uint8_t *smem, const PBars &B, uint32_t tmem,
+                                         volatile int *abort) {
   using C = PCfg<kFp8, kD, kTerms>;
-  const int S = a.d.S;
   const uint64_t dq = umma_sdesc(smem_addr(smem + C::kOffQ), 16, 1024, 2);
   const uint64_t dk = umma_sdesc(smem_addr(smem + C::kOffT), 16, 1024, 2);
-  const uint64_t dv = umma_sdesc(smem_addr(smem + C::kOffT), C::kBlkT, 1024, 2);
-  uint32_t base = 0;  // tiles before this item
-  uint32_t pc[2][C::kChunks] = {};
+  uint32_t tile = 0, u[2] = {0, 0};
+  PItem it;
   bool ok = true;
-  for (uint32_t items = 0; ok; ++items) {
-    ok = mbar_wait(&B.item_full[items % kItemSlots], (items / kItemSlots) & 1u, abort);
-    if (!ok) break;
-    const PItem it = reinterpret_cast<const PItem *>(smem + C::kOffItems)[items % kItemSlots];
-    mbar_arrive(&B.item_empty[items % kItemSlots]);
-    if (it.n_rows == 0) break;
-    const int n_tok = (it.p1 - it.p0) * S;
-    const int tiles = (n_tok + C::kTok - 1) / C::kTok, units = it.split ? tiles : 2 * tiles;
-    for (int t = 0; t < 2 && ok; ++t) ok = mbar_wait(&B.q_ready[t], items & 1u, abort);
-    auto qk = [&](int u) {
-      const int t = u & 1;
-      const uint32_t ik = 2 * (base + (uint32_t)(it.split ? u : u >> 1)), slot = ik % C::kSlots;
+  for (uint32_t i = 0; ok && next_item<C>(smem, B, i, it, abort); ++i) {
+    const int n_tok = (it.p1 - it.p0) * a.d.S;
+    ok = mbar_wait(&B.q_ready[0], i & 1u, abort) && mbar_wait(&B.q_ready[1], i & 1u, abort);
+    for (int t0 = 0; ok && t0 < n_tok; t0 += kTok, ++tile) {
+      const uint32_t ik = 2 * tile, slot = ik % C::kSlots;
       ok = mbar_wait(&B.full[slot], (ik / C::kSlots) & 1u, abort);
-      if (!ok) return;
-      tc_fence_after();
+      const uint64_t dks = dk + (uint64_t)((slot * C::kTBytes) >> 4);
 #pragma unroll
-      for (int s = 0; s < kD / 16; ++s) {
-        const uint32_t oq = t * C::kQBytes + (s >> 2) * C::kBlkQ + (s & 3) * 32;
-        const uint32_t ok_ = slot * C::kTBytes + (s >> 2) * C::kBlkT + (s & 3) * 32;
-        umma_f16(tmem + C::kColS + t * C::kTok, dq + (uint64_t)(oq >> 4), dk + (uint64_t)(ok_ >> 4), C::kIdQK,
-                 s ? 1u : 0u);
-      }
-      umma_commit(&B.s_full[t]);
-      if (it.split || t == 1) umma_commit(&B.empty[slot]);
-    };
-    for (int u = 0; u < 2 && u < units && ok; ++u) qk(u);
-    if (units == 1 && ok) umma_commit(&B.s_full[1]);  // half 1 has no tile; see its wait
-    for (int u = 0; u < units && ok; ++u) {
-      const int t = u & 1, tile = it.split ? u : u >> 1;
-      const uint32_t iv = 2 * (base + (uint32_t)tile) + 1, slot = iv % C::kSlots;
-      const int chunks = (min(C::kTok, n_tok - tile * C::kTok) + 63) / 64;
-      ok = mbar_wait(&B.full[slot], (iv / C::kSlots) & 1u, abort);
+      for (int c = 0; c < 2; ++c)
 #pragma unroll
-      for (int c = 0; c < C::kChunks; ++c) {
-        if (c >= chunks || !ok) break;
-        ok = mbar_wait(&B.p_full[2 * t + c], pc[t][c]++ & 1u, abort);
-        if (!ok) break;
-        tc_fence_after();
+        for (int t = 0; t < 2; ++t) {
+          if (!ok || t0 + 64 * c >= n_tok || (it.split && c != t)) continue;
+          const uint32_t b = u[t] % C::kBufs;
+          ok = mbar_wait(&B.pv_done[2 * t + b], ((u[t] / C::kBufs) & 1u) ^ 1u, abort);
+          if (!ok) continue;
+          ++u[t];
+          tc_fence_after();
+          const uint32_t d = tmem + C::col_s(t, 0) + 64 * b;
 #pragma unroll
-        for (int k = 0; k < kTerms; ++k) {
-          const uint32_t p = tmem + (k < 2 ? C::kColS + t * C::kTok + 64 * c + 32 * k : C::kColX + 32 * t);
-#pragma unroll
-          for (int s = 0; s < 4; ++s)
-            umma_f16_ts(tmem + C::kColO + 128 * t, p + 8 * s,
-                        dv + (uint64_t)((slot * C::kTBytes + (4 * c + s) * 2048) >> 4), C::kIdPV,
-                        (u < 2 && c == 0 && k == 0 && s == 0) ? 0u : 1u);
+          for (int s = 0; s < kD / 16; ++s)
+            umma_f16(d, dq + (uint64_t)((t * C::kQBytes + (s >> 2) * C::kBlk + (s & 3) * 32) >> 4),
+                     dks + (uint64_t)(((s >> 2) * C::kBlk + c * 64 * 128 + (s & 3) * 32) >> 4), C::kIdQK, s ? 1u : 0u);
+          umma_commit(&B.s_full[2 * t + b]);
         }
-        umma_commit(&B.pv_done[2 * t + c]);
-      }
-      if (!ok) break;
-      if (it.split || t == 1) umma_commit(&B.empty[slot]);
-      if (u + 2 < units) qk(u + 2);
+      if (ok) umma_commit(&B.empty[slot]);
     }
-    base += (uint32_t)tiles;
+    // the query operands may be replaced
+    umma_commit(&B.q_read[0]);
+    umma_commit(&B.q_read[1]);
   }
-  // every MMA issued here has completed before tensor memory is released
-  umma_commit(B.drain);
-  const uint64_t t0 = global_timer_ns();
-  while (!mbar_try_wait(B.drain, 0))
-    if (global_timer_ns() - t0 > kWaitLimitNs) break;
+  drain_mmas(&B.drain[0]);
+}
+
+// O[t] += P V, once P is in place.
+template <bool kFp8, int kD, int kTerms>
+__device__ __forceinline__ void issue_pv(const PrefixArgs &a, uint8_t *smem, const PBars &B, uint32_t tmem,
+                                         volatile int *abort) {
+  using C = PCfg<kFp8, kD, kTerms>;
+  const uint64_t dv = umma_sdesc(smem_addr(smem + C::kOffT), C::kBlk, 1024, 2);
+  uint32_t tile = 0, u[2] = {0, 0};
+  PItem it;
+  bool ok = true;
+  for (uint32_t i = 0; ok && next_item<C>(smem, B, i, it, abort); ++i) {
+    const int n_tok = (it.p1 - it.p0) * a.d.S;
+    uint32_t acc[2] = {0u, 0u};
+    for (int t0 = 0; ok && t0 < n_tok; t0 += kTok, ++tile) {
+      const uint32_t iv = 2 * tile + 1, slot = iv % C::kSlots;
+      ok = mbar_wait(&B.full[slot], (iv / C::kSlots) & 1u, abort);
+      const uint64_t dvs = dv + (uint64_t)((slot * C::kTBytes) >> 4);
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          if (!ok || t0 + 64 * c >= n_tok || (it.split && c != t)) continue;
+          const uint32_t b = u[t] % C::kBufs;
+          ok = mbar_wait(&B.p_full[2 * t + b], (u[t] / C::kBufs) & 1u, abort);
+          if (!ok) continue;
+          ++u[t];
+          tc_fence_after();
+          const uint32_t s0 = tmem + C::col_s(t, 0) + 64 * b, x0 = tmem + C::col_x(t, 0) + 32 * b;
+#pragma unroll
+          for (int k = 0; k < kTerms; ++k)
+#pragma unroll
+            for (int s = 0; s < 4; ++s)
+              umma_f16_ts(tmem + C::col_o(t), (k < 2 ? s0 + 32 * k : x0) + 8 * s,
+                          dvs + (uint64_t)((c * 64 * 128 + s * 2048) >> 4), C::kIdPV, k + s ? 1u : acc[t]);
+          acc[t] = 1u;
+          umma_commit(&B.pv_done[2 * t + b]);
+        }
+      if (ok) umma_commit(&B.empty[slot]);
+    }
+  }
+  drain_mmas(&B.drain[1]);
 }
 
 // ---------------------------------------------------------------- softmax (warps 0-7)
@@ -504,10 +539,9 @@ __device__ __forceinline__ void softmax_rows(const PrefixArgs &a, uint8_t *smem,
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int t = warp >> 2, r = (warp & 3) * 32 + lane;  // half, row of it
   const bool per_token = kFp8 && a.d.scale_mode == PFKV_SCALE_PER_TOKEN;
-  const uint32_t tq = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-  const uint32_t col_s = tq + C::kColS + t * C::kTok, col_o = tq + C::kColO + 128 * t;
+  const uint32_t tq = tmem + ((uint32_t)((warp & 3) * 32) << 16), col_o = tq + C::col_o(t);
   const int S = a.d.S;
-  uint32_t base = 0, n_s = 0, n_pv[2] = {0, 0};  // tiles, units, and units' first and second chunks before
+  uint32_t tile0 = 0, u = 0;  // tiles before this item, this half's units so far
   for (uint32_t items = 0;; ++items) {
     if (!mbar_wait_warp(&B.item_full[items % kItemSlots], (items / kItemSlots) & 1u, abort)) return;
     const PItem it = reinterpret_cast<const PItem *>(smem + C::kOffItems)[items % kItemSlots];
@@ -515,13 +549,14 @@ __device__ __forceinline__ void softmax_rows(const PrefixArgs &a, uint8_t *smem,
     if (lane == 0) mbar_arrive(&B.item_empty[items % kItemSlots]);
     if (it.n_rows == 0) return;
     const int n_tok = (it.p1 - it.p0) * S;
-    const int tiles = (n_tok + C::kTok - 1) / C::kTok, units = it.split ? tiles : 2 * tiles;
     const int row = it.split ? r : t * (kRows / 2) + r;  // row of the item's block
     const bool mine = row < it.n_rows;
     // this thread's query row into the operand; f16: scaled by 2^e into [2^14, 2^15), exact; the sign of the
     // factor that turns products into scores goes with it, so that the largest product is the largest score
     float mult = a.d.sm_scale_log2;
     if (kFp8 && !per_token) mult *= a.d.k_scale[it.h];
+    // (the half's last QK^T of the item before has read the operand)
+    if (items > 0 && !mbar_wait_warp(&B.q_read[t], (items - 1) & 1u, abort)) return;
     {
       uint4 x[kD / 8];
       const uint4 *src = nullptr;
@@ -557,7 +592,7 @@ __device__ __forceinline__ void softmax_rows(const PrefixArgs &a, uint8_t *smem,
           const float lo = __uint_as_float(v[q] << 16) * f1 * f2, hi = __uint_as_float(v[q] & 0xffff0000u) * f1 * f2;
           v[q] = kFp8 ? pack_f16x2(lo, hi) : pack_bf16x2(lo, hi);
         }
-        sts128(dst + (j >> 3) * C::kBlkQ + (((j & 7) ^ (r & 7)) << 4), make_uint4(v[0], v[1], v[2], v[3]));
+        sts128(dst + (j >> 3) * C::kBlk + (((j & 7) ^ (r & 7)) << 4), make_uint4(v[0], v[1], v[2], v[3]));
       }
       fence_async_smem();
       __syncwarp();
@@ -565,124 +600,116 @@ __device__ __forceinline__ void softmax_rows(const PrefixArgs &a, uint8_t *smem,
     }
     float m = kNegInf, l = 0.f, vref = 1.f;
     bool first = true;
-    int last = 0;  // the chunk handed over last; its products are the last to finish
-    for (int u = t; u < units; u += 2) {
-      const int tile = it.split ? u : u >> 1;
-      const int valid = n_tok - tile * C::kTok;
-      const uint32_t n = base + (uint32_t)tile;
-      const float *sc = reinterpret_cast<const float *>(smem + C::kOffScale) + (n % kScaleSlots) * (2 * C::kTok + 4);
-      if (!mbar_wait_warp(&B.s_full[t], n_s++ & 1u, abort)) return;
+    // 64 tokens of a tile at a time: both halves of it, or in split mode this half's
+#pragma unroll 1
+    for (int tok = it.split ? 64 * t : 0; tok < n_tok; tok += it.split ? kTok : 64) {
+      const int valid = n_tok - tok;
+      const uint32_t buf = u % C::kBufs, col = tq + C::col_s(t, 0) + 64 * buf, n = tile0 + (uint32_t)tok / kTok;
+      const float *sc = reinterpret_cast<const float *>(smem + C::kOffScale) +
+                        (n % kScaleSlots) * (2 * kTok + 4) + (tok & 64);
+      if (!mbar_wait_warp(&B.s_full[2 * t + buf], (u / C::kBufs) & 1u, abort)) return;
       float moved = 1.f;
       if (per_token) {
         if (!mbar_wait_warp(&B.sc_full[n % kScaleSlots], (n / kScaleSlots) & 1u, abort)) return;
-        const float now = sc[2 * C::kTok];  // against the reference this half last used (split: not every tile's)
+        const float now = sc[2 * kTok - (tok & 64)];  // against the reference this half last used
         if (!first && now != vref) moved = vref / now;
         vref = now;
       }
       tc_fence_after();
-#pragma unroll 1
-      for (int c = 0; c < C::kChunks && 64 * c < valid; ++c) {
-        uint32_t z[64];
-        tmem_ld64(col_s + 64 * c, z);
-        float mx = kNegInf;
-        if (per_token) {
+      uint32_t z[64];
+      tmem_ld64(col, z);
+      float mx = kNegInf;
+      if (per_token) {
 #pragma unroll
-          for (int j = 0; j < 64; j += 4) {
-            const float4 k4 = *reinterpret_cast<const float4 *>(sc + 64 * c + j);
-            z[j] = __float_as_uint(__uint_as_float(z[j]) * k4.x);
-            z[j + 1] = __float_as_uint(__uint_as_float(z[j + 1]) * k4.y);
-            z[j + 2] = __float_as_uint(__uint_as_float(z[j + 2]) * k4.z);
-            z[j + 3] = __float_as_uint(__uint_as_float(z[j + 3]) * k4.w);
-          }
+        for (int j = 0; j < 64; j += 4) {
+          const float4 k4 = *reinterpret_cast<const float4 *>(sc + j);
+          z[j] = __float_as_uint(__uint_as_float(z[j]) * k4.x);
+          z[j + 1] = __float_as_uint(__uint_as_float(z[j + 1]) * k4.y);
+          z[j + 2] = __float_as_uint(__uint_as_float(z[j + 2]) * k4.z);
+          z[j + 3] = __float_as_uint(__uint_as_float(z[j + 3]) * k4.w);
         }
-        if (64 * c + 64 > valid) {
-#pragma unroll
-          for (int j = 0; j < 64; ++j)
-            if (64 * c + j >= valid) z[j] = 0xff800000u;
-        }
-#pragma unroll
-        for (int j = 0; j < 64; ++j) mx = fmaxf(mx, __uint_as_float(z[j]));
-        mx = mx == kNegInf ? kNegInf : mx * mult;
-        // move the reference
-        const bool grow = mx > m + kGrow || first;
-        if (__any_sync(0xffffffffu, grow || moved != 1.f)) {
-          const float mn = grow ? fmaxf(m, mx) : m;
-          const float al = first ? 0.f : fast_exp2(m - mn);
-          l *= al;
-          if (!first) {
-            // the products handed over before: those of earlier tiles are done, as S could not be here otherwise
-            if (c > 0 && !mbar_wait_warp(&B.pv_done[2 * t], (n_pv[0] - 1) & 1u, abort)) return;
-            tc_fence_after();
-            const float f = al * moved;
-#pragma unroll 1
-            for (int i = 0; i < kD / 32; ++i) {
-              uint32_t o[32];
-              tmem_ld32(col_o + 32 * i, o);
-#pragma unroll
-              for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
-              tmem_st32(col_o + 32 * i, o);
-            }
-            tmem_wait_st();
-          }
-          m = mn;
-          moved = 1.f;
-        }
-        first = false;
-        const float off = C::kShift - m;
-        float sum0 = 0.f, sum1 = 0.f;
-        uint32_t pk[32];
-#pragma unroll
-        for (int k = 0; k < kTerms; ++k) {
-#pragma unroll
-          for (int j = 0; j < 64; j += 2) {
-            float p0, p1;
-            if (k == 0) {
-              p0 = fast_exp2(fmaf(__uint_as_float(z[j]), mult, off));
-              p1 = fast_exp2(fmaf(__uint_as_float(z[j + 1]), mult, off));
-              sum0 += p0;
-              sum1 += p1;
-              if (per_token) {
-                const float2 v2 = *reinterpret_cast<const float2 *>(sc + C::kTok + 64 * c + j);
-                p0 *= v2.x;
-                p1 *= v2.y;
-              }
-            } else {
-              p0 = __uint_as_float(z[j]);
-              p1 = __uint_as_float(z[j + 1]);
-            }
-            if constexpr (kFp8) {
-              pk[j / 2] = pack_f16x2(p0, p1);
-              if (k + 1 < kTerms) {
-                const float2 back = __half22float2(*reinterpret_cast<const __half2 *>(&pk[j / 2]));
-                z[j] = __float_as_uint(p0 - back.x);
-                z[j + 1] = __float_as_uint(p1 - back.y);
-              }
-            } else {
-              pk[j / 2] = pack_bf16x2(p0, p1);
-              if (k + 1 < kTerms) {
-                z[j] = __float_as_uint(p0 - __uint_as_float(pk[j / 2] << 16));
-                z[j + 1] = __float_as_uint(p1 - __uint_as_float(pk[j / 2] & 0xffff0000u));
-              }
-            }
-          }
-          tmem_st32(k < 2 ? col_s + 64 * c + 32 * k : tq + C::kColX + 32 * t, pk);
-        }
-        l += sum0 + sum1;
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&B.p_full[2 * t + c]);
-        if (c == 0) ++n_pv[0];
-        else ++n_pv[1];
-        last = c;
       }
+      if (valid < 64) {
+#pragma unroll
+        for (int j = 0; j < 64; ++j)
+          if (j >= valid) z[j] = 0xff800000u;
+      }
+#pragma unroll
+      for (int j = 0; j < 64; ++j) mx = fmaxf(mx, __uint_as_float(z[j]));
+      mx = mx == kNegInf ? kNegInf : mx * mult;
+      // move the reference
+      const bool grow = mx > m + kGrow || first;
+      if (__any_sync(0xffffffffu, grow || moved != 1.f)) {
+        const float mn = grow ? fmaxf(m, mx) : m;
+        const float al = first ? 0.f : fast_exp2(m - mn);
+        l *= al;
+        if (!first) {
+          // after the products handed over last
+          if (!mbar_wait_warp(&B.pv_done[2 * t + (u - 1) % C::kBufs], ((u - 1) / C::kBufs) & 1u, abort)) return;
+          tc_fence_after();
+          const float f = al * moved;
+#pragma unroll 1
+          for (int i = 0; i < kD / 32; ++i) {
+            uint32_t o[32];
+            tmem_ld32(col_o + 32 * i, o);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+            tmem_st32(col_o + 32 * i, o);
+          }
+          tmem_wait_st();
+        }
+        m = mn;
+      }
+      first = false;
+      const float off = C::kShift - m;
+      float sum0 = 0.f, sum1 = 0.f;
+      uint32_t pk[32];
+#pragma unroll
+      for (int k = 0; k < kTerms; ++k) {
+#pragma unroll
+        for (int j = 0; j < 64; j += 2) {
+          float p0, p1;
+          if (k == 0) {
+            p0 = fast_exp2(fmaf(__uint_as_float(z[j]), mult, off));
+            p1 = fast_exp2(fmaf(__uint_as_float(z[j + 1]), mult, off));
+            sum0 += p0;
+            sum1 += p1;
+            if (per_token) {
+              const float2 v2 = *reinterpret_cast<const float2 *>(sc + kTok + j);
+              p0 *= v2.x;
+              p1 *= v2.y;
+            }
+          } else {
+            p0 = __uint_as_float(z[j]);
+            p1 = __uint_as_float(z[j + 1]);
+          }
+          if constexpr (kFp8) {
+            pk[j / 2] = pack_f16x2(p0, p1);
+            if (k + 1 < kTerms) {
+              const float2 back = __half22float2(*reinterpret_cast<const __half2 *>(&pk[j / 2]));
+              z[j] = __float_as_uint(p0 - back.x);
+              z[j + 1] = __float_as_uint(p1 - back.y);
+            }
+          } else {
+            pk[j / 2] = pack_bf16x2(p0, p1);
+            if (k + 1 < kTerms) {
+              z[j] = __float_as_uint(p0 - __uint_as_float(pk[j / 2] << 16));
+              z[j + 1] = __float_as_uint(p1 - __uint_as_float(pk[j / 2] & 0xffff0000u));
+            }
+          }
+        }
+        tmem_st32(k < 2 ? col + 32 * k : tq + C::col_x(t, 0) + 32 * buf, pk);
+      }
+      l += sum0 + sum1;
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&B.p_full[2 * t + buf]);
+      ++u;
     }
-    // the half's partial result; a half without a tile (split, a single one) waits for the issuer all the same,
-    // so that it does not run ahead of it
-    if (first) {
-      if (!mbar_wait_warp(&B.s_full[t], n_s++ & 1u, abort)) return;
-    } else {
-      if (!mbar_wait_warp(&B.pv_done[2 * t + last], ((last ? n_pv[1] : n_pv[0]) - 1) & 1u, abort)) return;
+    // the half's partial result
+    if (!first) {
+      if (!mbar_wait_warp(&B.pv_done[2 * t + (u - 1) % C::kBufs], ((u - 1) / C::kBufs) & 1u, abort)) return;
       tc_fence_after();
     }
     const float fac = !kFp8 ? 1.f : per_token ? vref : a.d.v_scale[it.h];
@@ -692,7 +719,7 @@ __device__ __forceinline__ void softmax_rows(const PrefixArgs &a, uint8_t *smem,
       uint32_t o[32];
       if (!first) {
         tmem_ld32(col_o + 32 * i, o);
-      } else {
+      } else {  // split, and at most 64 tokens: half 1 has none
 #pragma unroll
         for (int j = 0; j < 32; ++j) o[j] = 0u;
       }
@@ -707,7 +734,7 @@ __device__ __forceinline__ void softmax_rows(const PrefixArgs &a, uint8_t *smem,
     }
     if (mine) a.ml[at] = make_float2(first ? kNegInf : m - C::kShift, l);
     tc_fence_before();
-    base += (uint32_t)tiles;
+    tile0 += (uint32_t)(n_tok + kTok - 1) / kTok;
   }
 }
 
@@ -728,23 +755,24 @@ __global__ void __launch_bounds__(kPThreads, 1) prefix_kernel(const PrefixArgs a
       mbar_init(&B.code_empty[i], 4);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&B.s_full[i], 1);
       mbar_init(&B.q_ready[i], 4);
+      mbar_init(&B.q_read[i], 1);
+      mbar_init(&B.drain[i], 1);
     }
     for (int i = 0; i < 4; ++i) {
+      mbar_init(&B.s_full[i], 1);
       mbar_init(&B.p_full[i], 4);
       mbar_init(&B.pv_done[i], 1);
     }
     for (int i = 0; i < kScaleSlots; ++i) mbar_init(&B.sc_full[i], 4);
     for (int i = 0; i < kItemSlots; ++i) {
       mbar_init(&B.item_full[i], 1);
-      mbar_init(&B.item_empty[i], 9);  // eight softmax warps and the issuer
+      mbar_init(&B.item_empty[i], 10);  // eight softmax warps and the issuers
     }
     for (int i = 0; i < kTileSlots; ++i) {
       mbar_init(&B.tile_full[i], 1);
       mbar_init(&B.tile_empty[i], 4);
     }
-    mbar_init(B.drain, 1);
     s_abort = 0;
     mbar_init_fence();
   }
@@ -768,7 +796,9 @@ __global__ void __launch_bounds__(kPThreads, 1) prefix_kernel(const PrefixArgs a
     } else {
       regs_dec<kRegsRest>();
       if (warp == 12) {
-        if ((threadIdx.x & 31) == 0) issue_mmas<kFp8, kD, kTerms>(a, smem, B, tmem, abort);
+        if ((threadIdx.x & 31) == 0) issue_qk<kFp8, kD, kTerms>(a, smem, B, tmem, abort);
+      } else if (warp == 14) {
+        if ((threadIdx.x & 31) == 0) issue_pv<kFp8, kD, kTerms>(a, smem, B, tmem, abort);
       } else if (warp == 13) {
         plan_tiles<kFp8, kD, kTerms>(a, smem, B, hdr, abort);
       }
