@@ -23,7 +23,7 @@
 //                   128-byte-swizzled layout.  FP8: e4m3 -> f16 from staged
 //                   codes, once per CTA.  BF16: asynchronous copies from the
 //                   pool, two tiles ahead.
-//   warps 12, 14    issue the MMAs of QK^T and of PV, a thread each.
+//   warps 12, 14    issue the MMAs of QK^T and of PV.
 //   warp 13         planner: works out the CTA's items and where each tile's
 //                   rows lie (bounds-checked page ids), so that nobody else
 //                   waits for a table entry; FP8: bulk-copies the codes into
@@ -33,12 +33,14 @@
 // tokens of each tile and half 1 the others; each half then leaves a partial
 // result of its own.
 //
-// The running maximum m of a row moves only when a unit exceeds it by more
-// than 2^8 (log2 units: 8), which after the first unit is rare; O is then
-// rescaled in tensor memory by the row's own softmax warp, after the products
-// it has handed over and before the next.  Probabilities are carried with a
-// factor 2^kShift, so that those down to 2^-20 of the reference stay normal in
-// f16; l has the same factor, so the quotient does not see it.
+// The running maximum m of a row is a reference that moves only when a unit
+// exceeds it by far (2^14 for f16 weights, which then still fit; 2^60 for
+// bf16), which after the first unit hardly happens; O is then rescaled in
+// tensor memory by the row's own softmax warp, after the products it has handed
+// over and before the next.  (With 2^8 a third of the units of heavy-tailed
+// scores, one key element in a hundred 20 times as large, moved some row.)
+// f16 weights below 2^-14 of the reference are subnormal: off by at most 2^-25
+// of it, alone or (second term) together.
 #pragma once
 
 #include "prefix.cuh"
@@ -56,7 +58,6 @@ constexpr int kRegsSoftmax = 176, kRegsLoader = 88, kRegsRest = 72;
 static_assert(kRegsSoftmax >= 128 && kRegsLoader <= 128 && kRegsRest <= 128 &&
                   2 * kRegsSoftmax + kRegsLoader + kRegsRest <= 4 * 128,
               "an increase goes up and a decrease down, and all of them fit what the block was launched with");
-constexpr float kGrow = 8.f;     // growth of a row's maximum that moves its reference
 
 // One piece of work, announced by the planner; n_rows 0 ends the work.
 struct PItem {
@@ -92,8 +93,10 @@ struct PCfg {
   __host__ __device__ static constexpr uint32_t col_x(int t, int b) { return 128 * kBufs + (uint32_t)(t * kBufs + b) * 32; }
   __host__ __device__ static constexpr uint32_t col_o(int t) { return 512 - (uint32_t)(2 - t) * kD; }
   static_assert((kTerms == 3 ? 192 : 128) * kBufs + 2 * kD <= 512, "tensor memory plan");
-  // per-token mode: V scales relative to a running reference, at most twice it
-  static constexpr float kShift = kFp8 ? 6.f : 0.f;
+  // Growth of a row's maximum (log2) that moves its reference.  f16: weights up
+  // to 2^14, times V scales of at most twice their reference, stay below 65504;
+  // bf16 has the range of fp32.
+  static constexpr float kGrow = kFp8 ? 14.f : 60.f;
   static constexpr uint32_t kOffQ = 0, kOffT = 2 * kQBytes, kOffCode = kOffT + kSlots * kTBytes;
   static constexpr uint32_t kOffCodeScale = kOffCode + kStage * kCodeBytes;  // K and V scales beside the codes of K
   static constexpr uint32_t kOffScale = kOffCodeScale + kStage * 2 * kTok * 4;
@@ -141,7 +144,7 @@ struct PBars {
   uint64_t *s_full, *p_full, *pv_done;    // per half and score buffer
   uint64_t *sc_full;                   // per-token scales
   uint64_t *item_full, *item_empty, *tile_full, *tile_empty;
-  uint64_t *drain;  // one per issuing thread
+  uint64_t *drain;  // one per issuing warp
 };
 
 __device__ __forceinline__ PBars pbars_at(uint8_t *base) {
@@ -420,29 +423,44 @@ __device__ __forceinline__ void loader_bf16(const PrefixArgs &a, uint8_t *smem, 
   cp_async_wait<0>();
 }
 
-// ---------------------------------------------------------------- MMA issuers (warps 12 and 14, one thread each)
+// ---------------------------------------------------------------- MMA issuers (warps 12 and 14)
 
 // A half's unit is 64 tokens of a tile; the units of a tile in the order
 // (64 tokens, half), in split mode half t takes the t-th 64 tokens.  Unit u of
 // a half has score buffer u % kBufs.
 
+//
+// The whole warp runs the loops and one elected lane issues: everything that an
+// MMA takes is then the same in all lanes and lives in uniform registers.
+// (With one thread running the loops, each MMA paid for moving its
+// descriptors there: the document step took 117 us in this kernel.)
+__device__ __forceinline__ bool elect_one() {
+  uint32_t e;
+  asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}\n" : "=r"(e));
+  return e != 0;
+}
+__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
+
 // Waits, bounded, until every MMA this thread issued has completed (before
 // tensor memory is released).
 __device__ __forceinline__ void drain_mmas(uint64_t *bar) {
-  umma_commit(bar);
+  if (elect_one()) umma_commit(bar);
   const uint64_t t0 = global_timer_ns();
   while (!mbar_try_wait(bar, 0))
     if (global_timer_ns() - t0 > kWaitLimitNs) break;
 }
 
-// Item of a ring slot; the caller has released it afterwards.  False: no more
-// work, or a wait gave up.
+// Tokens of item i and whether it is split; 0: no more work, or a wait gave up.
 template <typename C>
-__device__ __forceinline__ bool next_item(uint8_t *smem, const PBars &B, uint32_t i, PItem &it, volatile int *abort) {
-  if (!mbar_wait(&B.item_full[i % kItemSlots], (i / kItemSlots) & 1u, abort)) return false;
-  it = reinterpret_cast<const PItem *>(smem + C::kOffItems)[i % kItemSlots];
-  mbar_arrive(&B.item_empty[i % kItemSlots]);
-  return it.n_rows != 0;
+__device__ __forceinline__ int next_item(uint8_t *smem, const PBars &B, uint32_t i, int S, bool &split,
+                                         volatile int *abort) {
+  if (!mbar_wait_warp(&B.item_full[i % kItemSlots], (i / kItemSlots) & 1u, abort)) return 0;
+  const PItem &it = reinterpret_cast<const PItem *>(smem + C::kOffItems)[i % kItemSlots];
+  const int n_tok = uniform(it.n_rows ? (it.p1 - it.p0) * S : 0);
+  split = uniform(it.split) != 0;
+  __syncwarp();
+  if (elect_one()) mbar_arrive(&B.item_empty[i % kItemSlots]);
+  return n_tok;
 }
 
 // S[t][b] = Q_t K^T, once the PV that last read P from the buffer is done.
@@ -453,37 +471,42 @@ __device__ __forceinline__ void issue_qk(const PrefixArgs &a, uint8_t *smem, con
   const uint64_t dq = umma_sdesc(smem_addr(smem + C::kOffQ), 16, 1024, 2);
   const uint64_t dk = umma_sdesc(smem_addr(smem + C::kOffT), 16, 1024, 2);
   uint32_t tile = 0, u[2] = {0, 0};
-  PItem it;
-  bool ok = true;
-  for (uint32_t i = 0; ok && next_item<C>(smem, B, i, it, abort); ++i) {
-    const int n_tok = (it.p1 - it.p0) * a.d.S;
-    ok = mbar_wait(&B.q_ready[0], i & 1u, abort) && mbar_wait(&B.q_ready[1], i & 1u, abort);
+  bool ok = true, split = false;
+  for (uint32_t i = 0; ok; ++i) {
+    const int n_tok = next_item<C>(smem, B, i, a.d.S, split, abort);
+    if (n_tok == 0) break;
+    ok = mbar_wait_warp(&B.q_ready[0], i & 1u, abort) && mbar_wait_warp(&B.q_ready[1], i & 1u, abort);
     for (int t0 = 0; ok && t0 < n_tok; t0 += kTok, ++tile) {
       const uint32_t ik = 2 * tile, slot = ik % C::kSlots;
-      ok = mbar_wait(&B.full[slot], (ik / C::kSlots) & 1u, abort);
+      ok = mbar_wait_warp(&B.full[slot], (ik / C::kSlots) & 1u, abort);
       const uint64_t dks = dk + (uint64_t)((slot * C::kTBytes) >> 4);
 #pragma unroll
       for (int c = 0; c < 2; ++c)
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-          if (!ok || t0 + 64 * c >= n_tok || (it.split && c != t)) continue;
+          if (!ok || t0 + 64 * c >= n_tok || (split && c != t)) continue;
           const uint32_t b = u[t] % C::kBufs;
-          ok = mbar_wait(&B.pv_done[2 * t + b], ((u[t] / C::kBufs) & 1u) ^ 1u, abort);
+          ok = mbar_wait_warp(&B.pv_done[2 * t + b], ((u[t] / C::kBufs) & 1u) ^ 1u, abort);
           if (!ok) continue;
           ++u[t];
           tc_fence_after();
           const uint32_t d = tmem + C::col_s(t, 0) + 64 * b;
+          if (elect_one()) {
 #pragma unroll
-          for (int s = 0; s < kD / 16; ++s)
-            umma_f16(d, dq + (uint64_t)((t * C::kQBytes + (s >> 2) * C::kBlk + (s & 3) * 32) >> 4),
-                     dks + (uint64_t)(((s >> 2) * C::kBlk + c * 64 * 128 + (s & 3) * 32) >> 4), C::kIdQK, s ? 1u : 0u);
-          umma_commit(&B.s_full[2 * t + b]);
+            for (int s = 0; s < kD / 16; ++s)
+              umma_f16(d, dq + (uint64_t)((t * C::kQBytes + (s >> 2) * C::kBlk + (s & 3) * 32) >> 4),
+                       dks + (uint64_t)(((s >> 2) * C::kBlk + c * 64 * 128 + (s & 3) * 32) >> 4), C::kIdQK, s ? 1u : 0u);
+            umma_commit(&B.s_full[2 * t + b]);
+          }
+          __syncwarp();
         }
-      if (ok) umma_commit(&B.empty[slot]);
+      if (ok && elect_one()) umma_commit(&B.empty[slot]);
     }
     // the query operands may be replaced
-    umma_commit(&B.q_read[0]);
-    umma_commit(&B.q_read[1]);
+    if (elect_one()) {
+      umma_commit(&B.q_read[0]);
+      umma_commit(&B.q_read[1]);
+    }
   }
   drain_mmas(&B.drain[0]);
 }
@@ -495,36 +518,39 @@ __device__ __forceinline__ void issue_pv(const PrefixArgs &a, uint8_t *smem, con
   using C = PCfg<kFp8, kD, kTerms>;
   const uint64_t dv = umma_sdesc(smem_addr(smem + C::kOffT), C::kBlk, 1024, 2);
   uint32_t tile = 0, u[2] = {0, 0};
-  PItem it;
-  bool ok = true;
-  for (uint32_t i = 0; ok && next_item<C>(smem, B, i, it, abort); ++i) {
-    const int n_tok = (it.p1 - it.p0) * a.d.S;
+  bool ok = true, split = false;
+  for (uint32_t i = 0; ok; ++i) {
+    const int n_tok = next_item<C>(smem, B, i, a.d.S, split, abort);
+    if (n_tok == 0) break;
     uint32_t acc[2] = {0u, 0u};
     for (int t0 = 0; ok && t0 < n_tok; t0 += kTok, ++tile) {
       const uint32_t iv = 2 * tile + 1, slot = iv % C::kSlots;
-      ok = mbar_wait(&B.full[slot], (iv / C::kSlots) & 1u, abort);
+      ok = mbar_wait_warp(&B.full[slot], (iv / C::kSlots) & 1u, abort);
       const uint64_t dvs = dv + (uint64_t)((slot * C::kTBytes) >> 4);
 #pragma unroll
       for (int c = 0; c < 2; ++c)
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-          if (!ok || t0 + 64 * c >= n_tok || (it.split && c != t)) continue;
+          if (!ok || t0 + 64 * c >= n_tok || (split && c != t)) continue;
           const uint32_t b = u[t] % C::kBufs;
-          ok = mbar_wait(&B.p_full[2 * t + b], (u[t] / C::kBufs) & 1u, abort);
+          ok = mbar_wait_warp(&B.p_full[2 * t + b], (u[t] / C::kBufs) & 1u, abort);
           if (!ok) continue;
           ++u[t];
           tc_fence_after();
           const uint32_t s0 = tmem + C::col_s(t, 0) + 64 * b, x0 = tmem + C::col_x(t, 0) + 32 * b;
+          if (elect_one()) {
 #pragma unroll
-          for (int k = 0; k < kTerms; ++k)
+            for (int k = 0; k < kTerms; ++k)
 #pragma unroll
-            for (int s = 0; s < 4; ++s)
-              umma_f16_ts(tmem + C::col_o(t), (k < 2 ? s0 + 32 * k : x0) + 8 * s,
-                          dvs + (uint64_t)((c * 64 * 128 + s * 2048) >> 4), C::kIdPV, k + s ? 1u : acc[t]);
+              for (int s = 0; s < 4; ++s)
+                umma_f16_ts(tmem + C::col_o(t), (k < 2 ? s0 + 32 * k : x0) + 8 * s,
+                            dvs + (uint64_t)((c * 64 * 128 + s * 2048) >> 4), C::kIdPV, k + s ? 1u : acc[t]);
+            umma_commit(&B.pv_done[2 * t + b]);
+          }
+          __syncwarp();
           acc[t] = 1u;
-          umma_commit(&B.pv_done[2 * t + b]);
         }
-      if (ok) umma_commit(&B.empty[slot]);
+      if (ok && elect_one()) umma_commit(&B.empty[slot]);
     }
   }
   drain_mmas(&B.drain[1]);
@@ -638,7 +664,7 @@ __device__ __forceinline__ void softmax_rows(const PrefixArgs &a, uint8_t *smem,
       for (int j = 0; j < 64; ++j) mx = fmaxf(mx, __uint_as_float(z[j]));
       mx = mx == kNegInf ? kNegInf : mx * mult;
       // move the reference
-      const bool grow = mx > m + kGrow || first;
+      const bool grow = mx > m + C::kGrow || first;
       if (__any_sync(0xffffffffu, grow || moved != 1.f)) {
         const float mn = grow ? fmaxf(m, mx) : m;
         const float al = first ? 0.f : fast_exp2(m - mn);
@@ -661,7 +687,7 @@ __device__ __forceinline__ void softmax_rows(const PrefixArgs &a, uint8_t *smem,
         m = mn;
       }
       first = false;
-      const float off = C::kShift - m;
+      const float off = -m;
       float sum0 = 0.f, sum1 = 0.f;
       uint32_t pk[32];
 #pragma unroll
@@ -732,7 +758,7 @@ __device__ __forceinline__ void softmax_rows(const PrefixArgs &a, uint8_t *smem,
           stg256(a.o + at * kD + 32 * i + j, v);
         }
     }
-    if (mine) a.ml[at] = make_float2(first ? kNegInf : m - C::kShift, l);
+    if (mine) a.ml[at] = make_float2(first ? kNegInf : m, l);
     tc_fence_before();
     tile0 += (uint32_t)(n_tok + kTok - 1) / kTok;
   }
@@ -780,7 +806,7 @@ __global__ void __launch_bounds__(kPThreads, 1) prefix_kernel(const PrefixArgs a
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = s_tmem;
+  const uint32_t tmem = (uint32_t)uniform((int)s_tmem);
   volatile int *abort = &s_abort;
   pdl_wait();
   pdl_launch_dependents();
@@ -796,9 +822,9 @@ __global__ void __launch_bounds__(kPThreads, 1) prefix_kernel(const PrefixArgs a
     } else {
       regs_dec<kRegsRest>();
       if (warp == 12) {
-        if ((threadIdx.x & 31) == 0) issue_qk<kFp8, kD, kTerms>(a, smem, B, tmem, abort);
+        issue_qk<kFp8, kD, kTerms>(a, smem, B, tmem, abort);
       } else if (warp == 14) {
-        if ((threadIdx.x & 31) == 0) issue_pv<kFp8, kD, kTerms>(a, smem, B, tmem, abort);
+        issue_pv<kFp8, kD, kTerms>(a, smem, B, tmem, abort);
       } else if (warp == 13) {
         plan_tiles<kFp8, kD, kTerms>(a, smem, B, hdr, abort);
       }
