@@ -312,14 +312,12 @@ __device__ __forceinline__ void loader_fp8(const PrefixArgs &a, uint8_t *smem, c
   constexpr int kIt = kTok / kRowsIt;
   static_assert(kTok == 128, "one token per operand thread for the scales");
   const PTile *tiles = reinterpret_cast<const PTile *>(smem + C::kOffItems + kItemSlots * sizeof(PItem));
-  const int t = threadIdx.x - 8 * 32, lane = t & 31, c = t % kLanes, r_it = t / kLanes;
+  const int t = threadIdx.x - 8 * 32, lane = t & 31, c = t % kLanes;
+  // D 128: the second half of a row goes with the first half of its neighbour, so that eight lanes' stores, which
+  // the swizzle places by row and 16-byte chunk, meet different banks
+  const int r_it = (t / kLanes) ^ (kD == 128 ? c >> 2 : 0);
   const bool per_token = a.d.scale_mode == PFKV_SCALE_PER_TOKEN;
   const uint32_t s_ring = smem_addr(smem + C::kOffT), s_code = smem_addr(smem + C::kOffCode) + r_it * kD + 16 * c;
-  // Where this thread's 16 values of its row go: two 16-byte chunks, 2c and
-  // 2c + 1.  D 128: lanes 4-7 of a row write them in the other order, so that
-  // eight lanes' stores meet different banks.
-  const bool swap = kD == 128 && (c & 4);
-  const int j0 = 2 * c + (swap ? 1 : 0), j1 = 2 * c + (swap ? 0 : 1);
   const bool withhold = (a.d.flags & PFKV_FLAG_TEST_WITHHOLD) && blockIdx.x == 0;
   float vref = 0.f;
   for (uint32_t n = 0;; ++n) {
@@ -337,7 +335,8 @@ __device__ __forceinline__ void loader_fp8(const PrefixArgs &a, uint8_t *smem, c
       for (int k = 0; k < kIt; ++k) {
         const int r = k * kRowsIt + r_it;
         x[k] = lds128(s_code + st * C::kCodeBytes + k * kRowsIt * kD);
-        if (!(rows >> (r >> 4) & 1u)) x[k] = make_uint4(0u, 0u, 0u, 0u);  // never copied: no NaN among what stands there
+        // never copied: what stands there may be NaN
+        if (rows != 0xffu && !(rows >> (r >> 4) & 1u)) x[k] = make_uint4(0u, 0u, 0u, 0u);
       }
       if (!mbar_wait_warp(&B.empty[slot], ((i / C::kSlots) & 1u) ^ 1u, abort)) return;
       if (per_token && part == 0) hand_scales<C>(smem, B, n, st, rows, vref, t);
@@ -352,9 +351,9 @@ __device__ __forceinline__ void loader_fp8(const PrefixArgs &a, uint8_t *smem, c
         e4m3x4_to_f16x4(x[k].y, lo.z, lo.w);
         e4m3x4_to_f16x4(x[k].z, hi.x, hi.y);
         e4m3x4_to_f16x4(x[k].w, hi.z, hi.w);
-        const uint32_t row = base + r * 128;
-        sts128(row + (j0 >> 3) * C::kBlk + (((j0 & 7) ^ (r & 7)) << 4), swap ? hi : lo);
-        sts128(row + (j1 >> 3) * C::kBlk + (((j1 & 7) ^ (r & 7)) << 4), swap ? lo : hi);
+        const uint32_t row = base + (c >> 2) * C::kBlk + r * 128;  // 16-byte chunks 2c and 2c + 1 of the row
+        sts128(row + ((((2 * c) & 7) ^ (r & 7)) << 4), lo);
+        sts128(row + ((((2 * c + 1) & 7) ^ (r & 7)) << 4), hi);
       }
       fence_async_smem();
       __syncwarp();
@@ -661,7 +660,8 @@ __device__ __forceinline__ void softmax_rows(const PrefixArgs &a, uint8_t *smem,
           if (j >= valid) z[j] = 0xff800000u;
       }
 #pragma unroll
-      for (int j = 0; j < 64; ++j) mx = fmaxf(mx, __uint_as_float(z[j]));
+      for (int j = 0; j < 64; j += 2)  // three at a time
+        mx = fmaxf(fmaxf(mx, __uint_as_float(z[j])), __uint_as_float(z[j + 1]));
       mx = mx == kNegInf ? kNegInf : mx * mult;
       // move the reference
       const bool grow = mx > m + C::kGrow || first;
@@ -687,45 +687,44 @@ __device__ __forceinline__ void softmax_rows(const PrefixArgs &a, uint8_t *smem,
         m = mn;
       }
       first = false;
-      const float off = -m;
-      float sum0 = 0.f, sum1 = 0.f;
+      const uint64_t mult2 = f32x2(mult, mult), off2 = f32x2(-m, -m);
+      uint64_t sum = f32x2(0.f, 0.f);
       uint32_t pk[32];
 #pragma unroll
       for (int k = 0; k < kTerms; ++k) {
 #pragma unroll
         for (int j = 0; j < 64; j += 2) {
+          uint64_t p = f32x2(__uint_as_float(z[j]), __uint_as_float(z[j + 1]));
           float p0, p1;
           if (k == 0) {
-            p0 = fast_exp2(fmaf(__uint_as_float(z[j]), mult, off));
-            p1 = fast_exp2(fmaf(__uint_as_float(z[j + 1]), mult, off));
-            sum0 += p0;
-            sum1 += p1;
-            if (per_token) {
-              const float2 v2 = *reinterpret_cast<const float2 *>(sc + kTok + j);
-              p0 *= v2.x;
-              p1 *= v2.y;
-            }
-          } else {
-            p0 = __uint_as_float(z[j]);
-            p1 = __uint_as_float(z[j + 1]);
+            f32x2_split(fma_f32x2(p, mult2, off2), p0, p1);
+            p0 = fast_exp2(p0);
+            p1 = fast_exp2(p1);
+            p = f32x2(p0, p1);
+            sum = add_f32x2(sum, p);
+            if (per_token) p = mul_f32x2(p, *reinterpret_cast<const uint64_t *>(sc + kTok + j));
           }
-          if constexpr (kFp8) {
-            pk[j / 2] = pack_f16x2(p0, p1);
-            if (k + 1 < kTerms) {
+          f32x2_split(p, p0, p1);
+          pk[j / 2] = kFp8 ? pack_f16x2(p0, p1) : pack_bf16x2(p0, p1);
+          if (k + 1 < kTerms) {  // what the next term carries
+            float b0, b1;
+            if constexpr (kFp8) {
               const float2 back = __half22float2(*reinterpret_cast<const __half2 *>(&pk[j / 2]));
-              z[j] = __float_as_uint(p0 - back.x);
-              z[j + 1] = __float_as_uint(p1 - back.y);
+              b0 = back.x;
+              b1 = back.y;
+            } else {
+              b0 = __uint_as_float(pk[j / 2] << 16);
+              b1 = __uint_as_float(pk[j / 2] & 0xffff0000u);
             }
-          } else {
-            pk[j / 2] = pack_bf16x2(p0, p1);
-            if (k + 1 < kTerms) {
-              z[j] = __float_as_uint(p0 - __uint_as_float(pk[j / 2] << 16));
-              z[j + 1] = __float_as_uint(p1 - __uint_as_float(pk[j / 2] & 0xffff0000u));
-            }
+            f32x2_split(fma_f32x2(f32x2(b0, b1), f32x2(-1.f, -1.f), p), p0, p1);
+            z[j] = __float_as_uint(p0);
+            z[j + 1] = __float_as_uint(p1);
           }
         }
         tmem_st32(k < 2 ? col + 32 * k : tq + C::col_x(t, 0) + 32 * buf, pk);
       }
+      float sum0, sum1;
+      f32x2_split(sum, sum0, sum1);
       l += sum0 + sum1;
       tmem_wait_st();
       tc_fence_before();
