@@ -8,10 +8,11 @@
 // with m_i the maximum of the scaled scores of part i, l_i the sum of
 // e^{z - m_i} and o_i the sum of e^{z - m_i} v.  Kernels, in one stream:
 //   1. plan    one block per request: members of each group, lengths past
-//              the prefix, and the check that every member's first pages are
-//              the same pages (and, under the tag check, are still its own).
+//              the prefix, the work line.
 //   2. prefix  the groups' query rows as one matrix per KV head against the
-//              prefix pages (matrix instructions; see prefix_kernel).
+//              prefix pages (prefix_kernel.cuh); beside it, on a spare warp,
+//              the check that every member's first pages are the same pages
+//              (and, under the tag check, are still its own).
 //   3. split   each request's own pages: the grouped-query decode's split
 //              kernel (decode_gqa.cu) on lengths and tables past the prefix.
 //   4. join    partial results of 2 and 3 to out; status.
@@ -44,8 +45,6 @@ __device__ __forceinline__ int block_sum(int v, int *s_sum) {
 __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const PrefixArgs a) {
   extern __shared__ int s_count[];  // block B: requests of each group
   __shared__ int s_sum[kPlanThreads / 32];
-  __shared__ int s_lead;
-  __shared__ uint32_t s_bits;
   pdl_wait();
   const int t = threadIdx.x, B = a.d.B, MP = a.d.MP, S = a.d.S;
   if ((int)blockIdx.x == B) {
@@ -64,8 +63,9 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const PrefixA
         const int n = g < a.n_groups ? s_count[g] : 0;
         int pages = g < a.n_groups ? a.group_pages[g] : 0;
         if (pages < 0 || pages > MP || n == 0) pages = 0;  // a bad one is reported by its requests
-        const int items = pages ? a.d.cache.num_kv_heads * row_blocks(n, a.G) : 0;
-        const long long units = (long long)items * pages;
+        const HeadLine line = head_line(n, a.G, pages, a.c0);
+        const int items = pages ? a.d.cache.num_kv_heads * line.blocks : 0;
+        const long long units = pages ? a.d.cache.num_kv_heads * line.head : 0;
         int xn = n, xi = items;
         long long xu = units;
 #pragma unroll
@@ -84,9 +84,9 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const PrefixA
         unit += __shfl_sync(0xffffffffu, xu, 31);
       }
       if (t == 0) {
-        const long long r = (unit + a.min_pages - 1) / a.min_pages;
+        const long long r = unit / a.min_units;
         a.hdr->T = unit;
-        a.hdr->R = (int)(r < a.ctas ? r : a.ctas);
+        a.hdr->R = unit == 0 ? 0 : r < 1 ? 1 : (int)(r < a.ctas ? r : a.ctas);
       }
     }
     return;
@@ -96,88 +96,72 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const PrefixA
   uint32_t bits = 0u;
   if (L < 1 || (long long)L > (long long)MP * S) bits |= PFKV_ST_BAD_LEN;
   if (g < -1 || g >= a.n_groups) bits |= PFKV_ST_BAD_GROUP;
-  int pages = 0;
-  const bool member = g >= 0 && g < a.n_groups;
-  if (member) {
+  int pages = 0, rank = 0;
+  if (g >= 0 && g < a.n_groups) {
     pages = a.group_pages[g];
     if (pages < 0 || pages > MP) {
       bits |= PFKV_ST_BAD_GROUP;
       pages = 0;
     }
-    // place among all members, place in the group, the group's first request
-    if (t == 0) {
-      s_lead = b;
-      s_bits = 0u;
-    }
-    __syncthreads();
+    // its place among all members, and in its group
     int before = 0, mine = 0;
     for (int k = t; k < B; k += kPlanThreads) {
       const int gk = a.group_of[k];
       before += gk >= 0 && gk < g;
-      if (gk == g && k < b) {
-        ++mine;
-        atomicMin(&s_lead, k);
-      }
+      mine += gk == g && k < b;
     }
-    const int rank = block_sum(mine, s_sum);
+    rank = block_sum(mine, s_sum);
     const int at = block_sum(before, s_sum) + rank;
-    const int lead = s_lead;
-    if (t == 0) {
-      a.rank[b] = rank;
-      a.members[at] = b;
-    }
+    if (t == 0) a.members[at] = b;
     if (!bits && (long long)L < (long long)pages * S) bits |= PFKV_ST_BAD_LEN;
-    uint32_t mb = 0u;
-    if (!bits) {
-      const int *row = a.d.block_table + (size_t)b * MP, *first = a.d.block_table + (size_t)lead * MP;
-      const uint32_t *want = a.d.block_tags + (size_t)b * MP;  // read under the tag check only
-#pragma unroll 4
-      for (int i = t; i < pages; i += kPlanThreads) {
-        const int p = row[i];
-        if (p < 0 || p >= a.d.P)
-          mb |= PFKV_ST_PAGE_OOB;
-        else if ((a.d.flags & PFKV_FLAG_TAG_CHECK) && a.d.page_tags[p] != want[i])
-          mb |= PFKV_ST_STALE_TAG;
-        if (p != first[i]) mb |= PFKV_ST_PREFIX_DIFFERS;
-      }
-    }
-    if (mb) atomicOr(&s_bits, mb);
-    __syncthreads();
-    bits |= s_bits;
   }
   if (t == 0) {
     const long long own = (long long)L - (long long)pages * S;
     // a request that is already refused takes no further part
     a.own_len[b] = bits ? 0 : (int)own;
     a.skip[b] = pages;
+    a.rank[b] = rank;
     // a new token belongs in a page of the request's own
     if (!bits && a.d.append && own == 0) bits |= PFKV_ST_BAD_LEN;
     a.pre_st[b] = bits;
+    a.check_st[b] = 0u;
   }
 }
 
 // ---------------------------------------------------------------- join
 
-// One block per (request, query head): the pieces of the request's own pages
-// (split kernel) and of its group's prefix, joined by the log-sum-exp rule.
-// Reads every partial once; 4 (D 128) or 8 (D 64) pieces at a time.
-constexpr int kJoinThreads = 128;
+// Per (request, query head): the pieces of the request's own pages (split
+// kernel) and of its group's prefix, joined by the log-sum-exp rule.  Reads
+// every partial once, a row of a piece per warp and load.  Bound by latency:
+// a few dependent look-ups, then rows in flight.  kWarps warps share a row: one
+// where there are rows enough to fill the SMs, eight (a block) for few rows
+// of many pieces each.
+constexpr int kJoinThreads = 256;
 constexpr int kMaxJoin = 256 + 2 * kMaxRanges;
 
-template <int kD>
+template <int kD, int kWarps>
 __global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(const PrefixArgs a) {
-  constexpr int kCols = kD / 4, kPar = kJoinThreads / kCols;
-  __shared__ float s_w[kMaxJoin], s_l[kMaxJoin];
-  __shared__ float4 s_acc[kJoinThreads];
-  __shared__ float s_red[2][kJoinThreads / 32];
+  constexpr int kCols = kD / 4, kPar = 32 / kCols;  // float4 columns; pieces a warp reads at once
+  __shared__ float s_w[kWarps == 1 ? kJoinThreads / 32 : 1][kMaxJoin];
+  __shared__ float4 s_acc[kWarps == 1 ? 1 : kWarps][32];
   pdl_wait();
-  const int b = blockIdx.x / a.d.Hq, hq = blockIdx.x - b * a.d.Hq, t = threadIdx.x, lane = t & 31, warp = t >> 5;
-  uint32_t st = a.pre_st[b];
+  const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+  const long long id = kWarps == 1 ? (long long)blockIdx.x * (kJoinThreads / 32) + warp : blockIdx.x;
+  if (id >= (long long)a.d.B * a.d.Hq) return;  // kWarps 1 only: a whole warp, and no block barrier below
+  const int b = (int)(id / a.d.Hq), hq = (int)(id - (long long)b * a.d.Hq);
+  const int w0 = kWarps == 1 ? 0 : warp;  // this warp's place among the row's
+  float *sw = s_w[kWarps == 1 ? warp : 0];
+  // all that hangs on the request alone, at once
+  const int g = a.group_of[b], own = a.own_len[b], skip = a.skip[b], rank = a.rank[b];
+  const int count = a.d.split_count[b], first_piece = a.d.split_first[b];
+  const uint32_t pre = a.pre_st[b];
+  uint32_t st = pre | a.check_st[b];
+  const PrefixHdr hdr = *a.hdr;
   // own pages
   int n_own = 0, c0 = 0;
-  if (a.own_len[b] > 0) {
-    n_own = a.d.split_count[b];
-    c0 = a.d.split_first[b];
+  if (own > 0) {
+    n_own = count;
+    c0 = first_piece;
     if (n_own < 1 || n_own > a.d.max_splits || c0 < 0 || c0 > a.d.B * a.d.max_splits - n_own) {
       n_own = c0 = 0;  // a CTA of the split gave up before it wrote them
       st |= PFKV_ST_TIMEOUT;
@@ -186,87 +170,81 @@ __global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(const PrefixA
   // prefix: a piece per range; of an item of at most kRows / 2 rows, one per range and half (kRows / 2 rows on)
   int n_pre = 0, row = 0, sh = 0;
   long long slot0 = 0;
-  const int g = a.group_of[b];
-  if (!a.pre_st[b] && g >= 0 && a.skip[b] > 0) {
-    const PrefixHdr hdr = *a.hdr;
+  if (!pre && g >= 0 && skip > 0) {
     const PrefixGroup gr = a.groups[g];
-    const int r = a.rank[b] * a.G + hq % a.G, blk = r / kRows;
-    const int item = hq / a.G * row_blocks(gr.n, a.G) + blk;
-    const long long first = gr.unit0 + (long long)item * gr.pages;
+    const HeadLine line = head_line(gr.n, a.G, gr.pages, a.c0);
+    const int h = hq / a.G, r = rank * a.G + hq % a.G, blk = r / kRows;
+    const int item = h * line.blocks + blk, cost = page_cost(line, blk);
+    const long long first = gr.unit0 + h * line.head + blk * line.full + a.c0;  // unit of its first page
     const int k0 = range_of(hdr, first);
-    sh = gr.n * a.G - blk * kRows <= kRows / 2;
-    n_pre = (range_of(hdr, first + gr.pages - 1) - k0 + 1) << sh;
+    sh = cost == kCostHalf;
+    n_pre = (range_of(hdr, first + (long long)cost * (gr.pages - 1)) - k0 + 1) << sh;
     slot0 = (long long)k0 + gr.item0 + item;
     row = r - blk * kRows;
   }
   auto pre_row = [&](int i) { return (size_t)(slot0 + (i >> sh)) * kRows + row + (sh ? (i & 1) * (kRows / 2) : 0); };
   const int n = n_own + n_pre;
-  uint32_t bits = 0u;
-  for (int i = t; i < n_own * a.d.st_groups; i += kJoinThreads) bits |= a.d.part_st[(size_t)c0 * a.d.st_groups + i];
-  int any = 0;
-  if (hq == 0) {
-    for (int i = t; i < a.d.n_ctas; i += kJoinThreads) any |= a.d.cta_abort[i];
-    for (int i = t; i < a.ctas; i += kJoinThreads) any |= a.aborts[i];
-  }
+  for (int i = lane; i < n_own * a.d.st_groups; i += 32) st |= a.d.part_st[(size_t)c0 * a.d.st_groups + i];
+  // the pieces' maxima, then their weights
   float mx = kNegInf;
-  for (int i = t; i < n; i += kJoinThreads) {
+  for (int i = lane; i < n; i += 32) {
     const float2 ml = i < n_own ? a.d.part_ml[(size_t)(c0 + i) * a.d.Hq + hq] : a.ml[pre_row(i - n_own)];
-    s_w[i] = ml.x;
-    s_l[i] = ml.y;
     mx = fmaxf(mx, ml.x);
   }
   for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-  if (lane == 0) s_red[0][warp] = mx;
-  if (__syncthreads_or(bits != 0u)) {  // rare: gather which bits
-    __shared__ uint32_t s_bits;
-    if (t == 0) s_bits = 0u;
-    __syncthreads();
-    if (bits) atomicOr(&s_bits, bits);
-    __syncthreads();
-    st |= s_bits;
-  }
-  if (hq == 0) {
-    const bool gave_up = __syncthreads_or(any) != 0;
-    if (t == 0) a.d.status[b] = st | (gave_up ? (uint32_t)PFKV_ST_TIMEOUT : 0u);
-  }
-  mx = fmaxf(fmaxf(s_red[0][0], s_red[0][1]), fmaxf(s_red[0][2], s_red[0][3]));
+  st = __reduce_or_sync(0xffffffffu, st);
   float W = 0.f;
-  for (int i = t; i < n; i += kJoinThreads) {
-    const float w = fast_exp2(s_w[i] - mx);
-    W += w * s_l[i];
-    s_w[i] = w;
+  for (int i = lane; i < n; i += 32) {
+    const float2 ml = i < n_own ? a.d.part_ml[(size_t)(c0 + i) * a.d.Hq + hq] : a.ml[pre_row(i - n_own)];
+    const float w = fast_exp2(ml.x - mx);
+    W += w * ml.y;
+    if (w0 == 0) sw[i] = w;
   }
   for (int o = 16; o; o >>= 1) W += __shfl_xor_sync(0xffffffffu, W, o);
-  if (lane == 0) s_red[1][warp] = W;
-  __syncthreads();
-  W = s_red[1][0] + s_red[1][1] + s_red[1][2] + s_red[1][3];
-  const int col = t % kCols, par = t / kCols;
+  if (kWarps == 1) __syncwarp();
+  else __syncthreads();
+  if (hq == 0 && w0 == 0) {
+    int any = 0;
+    for (int i = lane; i < a.d.n_ctas; i += 32) any |= a.d.cta_abort[i];
+    for (int i = lane; i < a.ctas; i += 32) any |= a.aborts[i];
+    if (__any_sync(0xffffffffu, any != 0)) st |= PFKV_ST_TIMEOUT;
+    if (lane == 0) a.d.status[b] = st;
+  }
+  const int col = lane % kCols;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   if (!st) {
-#pragma unroll 4
-    for (int i = par; i < n; i += kPar) {
-      const float *src = i < n_own ? a.d.part_o + ((size_t)(c0 + i) * a.d.Hq + hq) * kD
-                                   : a.o + pre_row(i - n_own) * kD;
+#pragma unroll 8
+    for (int i = w0 * kPar + lane / kCols; i < n; i += kWarps * kPar) {
+      const float *src = i < n_own ? a.d.part_o + ((size_t)(c0 + i) * a.d.Hq + hq) * kD : a.o + pre_row(i - n_own) * kD;
       const float4 v = __ldcg(reinterpret_cast<const float4 *>(src) + col);
-      const float w = s_w[i];
+      const float w = sw[i];
       acc.x += w * v.x; acc.y += w * v.y; acc.z += w * v.z; acc.w += w * v.w;
     }
   }
-  s_acc[t] = acc;
-  __syncthreads();
-  if (t < kCols) {
-    for (int k = 1; k < kPar; ++k) {
-      const float4 v = s_acc[t + k * kCols];
+  if (kPar == 2) {
+    acc.x += __shfl_xor_sync(0xffffffffu, acc.x, 16);
+    acc.y += __shfl_xor_sync(0xffffffffu, acc.y, 16);
+    acc.z += __shfl_xor_sync(0xffffffffu, acc.z, 16);
+    acc.w += __shfl_xor_sync(0xffffffffu, acc.w, 16);
+  }
+  if (kWarps > 1) {
+    s_acc[kWarps == 1 ? 0 : warp][lane] = acc;
+    __syncthreads();
+    if (warp > 0) return;
+#pragma unroll
+    for (int k = 1; k < kWarps; ++k) {
+      const float4 v = s_acc[kWarps == 1 ? 0 : k][lane];
       acc.x += v.x; acc.y += v.y; acc.z += v.z; acc.w += v.w;
     }
-    const float inv = st ? 0.f : 1.f / W;
-    acc.x *= inv; acc.y *= inv; acc.z *= inv; acc.w *= inv;
-    const size_t at = ((size_t)b * a.d.Hq + hq) * kCols + t;
-    if (a.out_bf16)
-      reinterpret_cast<uint2 *>(a.d.out)[at] = make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
-    else
-      reinterpret_cast<float4 *>(a.d.out)[at] = acc;
   }
+  if (lane >= kCols) return;
+  const float inv = st ? 0.f : 1.f / W;
+  acc.x *= inv; acc.y *= inv; acc.z *= inv; acc.w *= inv;
+  const size_t at = (size_t)id * kCols + lane;
+  if (a.out_bf16)
+    reinterpret_cast<uint2 *>(a.d.out)[at] = make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
+  else
+    reinterpret_cast<float4 *>(a.d.out)[at] = acc;
 }
 
 // ---------------------------------------------------------------- host side
@@ -274,7 +252,7 @@ __global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(const PrefixA
 size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 
 struct PrefixLayout {
-  size_t own_len, skip, pre_st, rank, members, groups, hdr, ml, o, aborts, total;
+  size_t own_len, skip, pre_st, check_st, rank, members, groups, hdr, ml, o, aborts, total;
 };
 
 // Slots: pieces of the work line, at most one per range and one per item more.
@@ -287,7 +265,8 @@ PrefixLayout prefix_layout(size_t first, int batch, int q_heads, int kv_heads, i
   w.own_len = first;
   w.skip = w.own_len + up256(4 * B);
   w.pre_st = w.skip + up256(4 * B);
-  w.rank = w.pre_st + up256(4 * B);
+  w.check_st = w.pre_st + up256(4 * B);
+  w.rank = w.check_st + up256(4 * B);
   w.members = w.rank + up256(4 * B);
   w.groups = w.members + up256(4 * B);
   w.hdr = w.groups + up256(sizeof(PrefixGroup) * (size_t)n_groups);
@@ -311,7 +290,10 @@ int run_prefix(PrefixArgs a, cudaStream_t s) {
     if (dev < 64) attr_set.fetch_or(1ull << dev);
   }
   a.ctas = a.n_groups == 0 ? 0 : num_sms() < kMaxRanges ? num_sms() : kMaxRanges;
-  a.min_pages = (256 + a.d.S - 1) / a.d.S;
+  // an item's set-up and read-out cost about what 512 tokens of a small block do, and a range holds that and 256
+  // tokens of one at least
+  a.c0 = kCostHalf * ((512 + a.d.S - 1) / a.d.S);
+  a.min_units = a.c0 + kCostHalf * ((256 + a.d.S - 1) / a.d.S);
   int rc = cuda_ok(launch_dependent(prefix_plan_kernel, dim3((unsigned)a.d.B + 1u), kPlanThreads,
                                     4 * (size_t)a.n_groups, s, a),
                    "prefix plan launch");
@@ -327,7 +309,12 @@ int run_prefix(PrefixArgs a, cudaStream_t s) {
   if (rc) return rc;
   a.d.n_ctas = own.n_ctas;
   a.d.st_groups = own.st_groups;
-  return cuda_ok(launch_dependent(prefix_join_kernel<kD>, dim3((unsigned)a.d.B * (unsigned)a.d.Hq), kJoinThreads, 0, s, a),
+  // eight warps a row where one each would leave SMs idle
+  const long long rows = (long long)a.d.B * a.d.Hq;
+  const bool few = rows < 8LL * num_sms();
+  const dim3 grid((unsigned)(few ? rows : (rows + kJoinThreads / 32 - 1) / (kJoinThreads / 32)));
+  return cuda_ok(few ? launch_dependent(prefix_join_kernel<kD, kJoinThreads / 32>, grid, kJoinThreads, 0, s, a)
+                     : launch_dependent(prefix_join_kernel<kD, 1>, grid, kJoinThreads, 0, s, a),
                  "prefix join launch");
 }
 
@@ -353,6 +340,7 @@ int launch_prefix_decode(const DecodeArgs &d, size_t ws_first, uint8_t *ws, cons
   a.own_len = reinterpret_cast<int *>(ws + L.own_len);
   a.skip = reinterpret_cast<int *>(ws + L.skip);
   a.pre_st = reinterpret_cast<uint32_t *>(ws + L.pre_st);
+  a.check_st = reinterpret_cast<uint32_t *>(ws + L.check_st);
   a.rank = reinterpret_cast<int *>(ws + L.rank);
   a.members = reinterpret_cast<int *>(ws + L.members);
   a.groups = reinterpret_cast<PrefixGroup *>(ws + L.groups);

@@ -28,6 +28,7 @@
 //                   rows lie (bounds-checked page ids), so that nobody else
 //                   waits for a table entry; FP8: bulk-copies the codes into
 //                   a staging ring of three tiles (48 KB in flight).
+//   warp 15         compares the requests' prefix pages, all CTAs together.
 // An item of more than 128 rows has 128 in each half, over the same tokens.
 // One of at most 128 rows gives both halves the same rows, half 0 the first 64
 // tokens of each tile and half 1 the others; each half then leaves a partial
@@ -48,7 +49,7 @@
 namespace pfkv {
 namespace {
 
-constexpr int kPThreads = 16 * 32;  // four warpgroups; warp 15 only lends its registers
+constexpr int kPThreads = 16 * 32;  // four warpgroups
 constexpr int kScaleSlots = 4;   // tiles whose per-token scales are kept
 constexpr int kItemSlots = 4;    // items announced ahead
 constexpr int kTileSlots = 8;    // tiles announced ahead
@@ -113,27 +114,36 @@ struct PWalk {
   int k;
 };
 
+// The next piece with pages; whole warp or one thread.
 __device__ __forceinline__ bool walk_next(const PrefixArgs &a, PWalk &w, PItem &it) {
-  if (w.u >= w.u1) return false;
-  int lo = 0, hi = a.n_groups - 1;  // the last group that starts at or before u
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (a.groups[mid].unit0 <= w.u) lo = mid;
-    else hi = mid - 1;
+  while (w.u < w.u1) {
+    int lo = 0, hi = a.n_groups - 1;  // the last group that starts at or before u
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (a.groups[mid].unit0 <= w.u) lo = mid;
+      else hi = mid - 1;
+    }
+    const PrefixGroup g = a.groups[lo];
+    const HeadLine line = head_line(g.n, a.G, g.pages, a.c0);
+    const long long rel = w.u - g.unit0;
+    it.h = (int)(rel / line.head);
+    const long long in_head = rel - it.h * line.head;
+    const int blk = (int)min((long long)(line.blocks - 1), in_head / line.full);
+    const long long off = in_head - blk * line.full, seg = blk < line.blocks - 1 ? line.full : line.last;
+    const long long end = min(seg, off + (w.u1 - w.u));
+    const int cost = page_cost(line, blk);
+    it.p0 = (int)((max(0LL, off - a.c0) + cost - 1) / cost);
+    it.p1 = (int)((max(0LL, end - a.c0) + cost - 1) / cost);
+    w.u += end - off;
+    if (it.p1 <= it.p0) continue;
+    it.first = g.first;
+    it.row0 = blk * kRows;
+    it.n_rows = blk < line.blocks - 1 ? kRows : line.last_rows;
+    it.slot = (long long)w.k + g.item0 + it.h * line.blocks + blk;
+    it.split = cost == kCostHalf;
+    return true;
   }
-  const PrefixGroup g = a.groups[lo];
-  const int item = (int)((w.u - g.unit0) / g.pages);
-  const int mb = row_blocks(g.n, a.G);
-  it.first = g.first;
-  it.p0 = (int)(w.u - g.unit0 - (long long)item * g.pages);
-  it.p1 = (int)(w.u1 - w.u < g.pages - it.p0 ? it.p0 + (w.u1 - w.u) : g.pages);
-  it.h = item / mb;
-  it.row0 = (item - it.h * mb) * kRows;
-  it.n_rows = min(kRows, g.n * a.G - it.row0);
-  it.slot = (long long)w.k + g.item0 + item;
-  it.split = it.n_rows <= kRows / 2;
-  w.u += it.p1 - it.p0;
-  return true;
+  return false;
 }
 
 constexpr int kMaxSlots = 4;
@@ -269,6 +279,34 @@ __device__ __forceinline__ void plan_tiles(const PrefixArgs &a, uint8_t *smem, c
       while (!mbar_try_wait(&B.code_full[i % C::kStage], (i / C::kStage) & 1u))
         if (global_timer_ns() - t0 > kWaitLimitNs / 8) break;
     }
+  }
+}
+
+// ---------------------------------------------------------------- prefix check (warp 15)
+
+// Every member's first pages are the group's (those of its first request), lie
+// inside the pool and, under the tag check, have the tag of the member's
+// mapping.  (Request, 512 pages) at a time, over all CTAs.
+__device__ __forceinline__ void check_prefixes(const PrefixArgs &a) {
+  constexpr int kChunk = 512;
+  const int lane = threadIdx.x & 31;
+  const long long chunks = (a.d.MP + kChunk - 1) / kChunk;
+  const bool tag_check = (a.d.flags & PFKV_FLAG_TAG_CHECK) != 0u;
+  for (long long id = blockIdx.x; id < a.d.B * chunks; id += gridDim.x) {
+    const int b = (int)(id / chunks), lo = (int)(id - b * chunks) * kChunk;
+    if (a.pre_st[b] || lo >= a.skip[b]) continue;  // refused already, or no prefix there
+    const int hi = min(lo + kChunk, a.skip[b]), lead = a.members[a.groups[a.group_of[b]].first];
+    const int *row = a.d.block_table + (size_t)b * a.d.MP, *first = a.d.block_table + (size_t)lead * a.d.MP;
+    const uint32_t *want = a.d.block_tags + (size_t)b * a.d.MP;  // read under the tag check only
+    uint32_t bits = 0u;
+#pragma unroll 4
+    for (int i = lo + lane; i < hi; i += 32) {
+      const int p = row[i];
+      if (p < 0 || p >= a.d.P) bits |= PFKV_ST_PAGE_OOB;
+      else if (tag_check && a.d.page_tags[p] != want[i]) bits |= PFKV_ST_STALE_TAG;
+      if (p != first[i]) bits |= PFKV_ST_PREFIX_DIFFERS;
+    }
+    if (bits) atomicOr(&a.check_st[b], bits);
   }
 }
 
@@ -829,6 +867,7 @@ __global__ void __launch_bounds__(kPThreads, 1) prefix_kernel(const PrefixArgs a
       }
     }
   }
+  if (warp == 15) check_prefixes(a);
   __syncwarp();
   tc_fence_before();
   __syncthreads();

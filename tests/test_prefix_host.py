@@ -53,9 +53,9 @@ def test_workspace_bytes():
     d = desc()
     plain = abi.lib.pfkv_decode_workspace_bytes(ctypes.byref(d), 64, 32, 64)
     one = f(ctypes.byref(d), 64, 32, 1, 64)
-    # a slot per range (512 at most) and per row block of a KV head: 256 rows of 128 fp32 values and (m, l) at most
+    # a slot per range (256 at most) and per row block of a KV head, of 256 rows of 128 fp32 values and (m, l)
     rows = one - plain
-    assert 512 * 128 * 520 <= rows <= (512 + 8 * (64 * 4 // 128 + 1)) * 256 * 520 + 64 * 1024
+    assert rows - (256 + 8 * (64 * 4 // 256 + 1)) * 256 * 520 in range(64 * 1024)
     assert f(ctypes.byref(d), 64, 32, 5, 64) > one
     assert plain < f(ctypes.byref(d), 64, 32, 0, 64) < plain + 64 * 1024
     for bad in ((64, 33, 1, 64), (64, 32, 4097, 64), (64, 32, 1, 300)):
@@ -63,29 +63,34 @@ def test_workspace_bytes():
     assert f(None, 64, 32, 1, 64) == 0 and f(ctypes.byref(d), 64, 32, -1, 64) == 0
 
 
-def line(groups, H, G, rows, ctas, min_pages):
-    """The plan restated: [(members, pages)] -> (T, R, per group (pages, first item, first unit, row blocks))."""
+ROWS, HALF, FULL = 256, 4, 7  # rows of an item; a page's cost in a block of at most half the rows, and in others
+
+
+def line(groups, H, G, ctas, c0, min_units):
+    """The plan restated: [(members, pages)] -> (T, R, per group (pages, first item, first unit, block costs), items)."""
     unit = item = 0
     out = []
     for n, p in groups:
         p = p if n else 0
-        blocks = -(-n * G // rows)
-        out.append((p, item, unit, blocks))
-        items = H * blocks if p else 0
-        item += items
-        unit += items * p
-    return unit, min(-(-unit // min_pages), ctas), out, item
+        rows = n * G
+        cost = [HALF if rows - i * ROWS <= ROWS // 2 else FULL for i in range(-(-rows // ROWS))]
+        out.append((p, item, unit, cost))
+        if p:
+            item += H * len(cost)
+            unit += H * sum(c0 + c * p for c in cost)
+    return unit, 0 if unit == 0 else min(max(unit // min_units, 1), ctas), out, item
 
 
-@pytest.mark.parametrize("seed", range(40))
+@pytest.mark.parametrize("seed", range(60))
 def test_work_line_covers_every_item_once(seed):
-    """Pieces of the ranges, as the prefix kernel walks them, against the
-    slots that the join looks for: every page of every item once, distinct
-    slots inside the workspace, and the join's range of pieces is the walk's."""
+    """Pieces of the ranges, as the planner walks them, against the slots that
+    the join looks for: every page of every item once, distinct slots inside
+    the workspace, and the join's range of pieces is the walk's."""
     rng = np.random.default_rng(seed)
-    H, G, rows = int(rng.integers(1, 9)), int(rng.integers(1, 17)), int(rng.choice([128, 256]))
+    H, G, S = int(rng.integers(1, 9)), int(rng.integers(1, 17)), int(rng.choice([16, 48, 64, 256]))
     groups = [(int(rng.integers(0, 70)), int(rng.integers(0, 300))) for _ in range(int(rng.integers(1, 12)))]
-    T, R, g, items = line(groups, H, G, rows, int(rng.choice([1, 7, 152, 512])), int(rng.choice([1, 4, 16])))
+    c0 = HALF * -(-512 // S)
+    T, R, g, items = line(groups, H, G, int(rng.choice([1, 7, 152, 256])), c0, c0 + HALF * -(-256 // S))
     if T == 0:
         assert R == 0
         return
@@ -94,20 +99,27 @@ def test_work_line_covers_every_item_once(seed):
         u, u1 = k * T // R, (k + 1) * T // R
         while u < u1:
             lo = max(i for i, x in enumerate(g) if x[2] <= u)
-            p, item0, unit0, blocks = g[lo]
-            it, p0 = divmod(u - unit0, p)
-            p1 = min(p, p0 + u1 - u)
-            assert it < H * blocks
-            seen.setdefault((lo, it), []).append((p0, p1, k, k + item0 + it))
-            assert k + item0 + it not in slots
-            slots.add(k + item0 + it)
-            u += p1 - p0
-    for i, (p, item0, unit0, blocks) in enumerate(g):
-        for it in range(H * blocks if p else 0):
-            pieces = seen.pop((i, it))
-            assert [x[0] for x in pieces] == [0] + [x[1] for x in pieces[:-1]] and pieces[-1][1] == p
-            first = unit0 + it * p
-            k0, k1 = ((first + 1) * R - 1) // T, ((first + p) * R - 1) // T
-            assert [x[2] for x in pieces] == list(range(k0, k1 + 1))
-            assert [x[3] for x in pieces] == [k + item0 + it for k in range(k0, k1 + 1)]
-    assert not seen and max(slots) < R + items - 1 + 1
+            p, item0, unit0, cost = g[lo]
+            full, segs = c0 + FULL * p, [c0 + c * p for c in cost]
+            h, rel = divmod(u - unit0, sum(segs))
+            blk = min(len(cost) - 1, rel // full)
+            off = rel - blk * full
+            end = min(segs[blk], off + u1 - u)
+            p0, p1 = -(-max(0, off - c0) // cost[blk]), -(-max(0, end - c0) // cost[blk])
+            u += end - off
+            if p1 <= p0:
+                continue
+            slot = k + item0 + h * len(cost) + blk
+            assert h < H and slot not in slots
+            slots.add(slot)
+            seen.setdefault((lo, h, blk), []).append((p0, p1, k, slot))
+    for i, (p, item0, unit0, cost) in enumerate(g):
+        for h in range(H if p else 0):
+            for blk, w in enumerate(cost):
+                pieces = seen.pop((i, h, blk))
+                assert [x[0] for x in pieces] == [0] + [x[1] for x in pieces[:-1]] and pieces[-1][1] == p
+                first = unit0 + h * sum(c0 + c * p for c in cost) + blk * (c0 + FULL * p) + c0
+                k0, k1 = ((first + 1) * R - 1) // T, ((first + w * (p - 1) + 1) * R - 1) // T
+                assert [x[2] for x in pieces] == list(range(k0, k1 + 1))
+                assert [x[3] for x in pieces] == [k + item0 + h * len(cost) + blk for k in range(k0, k1 + 1)]
+    assert not seen and max(slots) < R + items
