@@ -198,7 +198,8 @@ __device__ __forceinline__ void regs_dec() {
 // and V; 1: V): lane g takes 16 tokens' codes, which are contiguous.
 template <typename C, int kD>
 __device__ __forceinline__ bool stage_codes(const PrefixArgs &a, uint8_t *smem, const PBars &B, const PTile &d,
-                                            uint32_t i, int part, bool per_token, volatile int *abort) {
+                                            uint32_t i, int part, bool per_token, uint64_t policy,
+                                            volatile int *abort) {
   const int lane = threadIdx.x & 31;
   const uint32_t s = i % C::kStage;
   if (!mbar_wait_warp(&B.code_empty[s], ((i / C::kStage) & 1u) ^ 1u, abort)) return false;
@@ -208,11 +209,12 @@ __device__ __forceinline__ bool stage_codes(const PrefixArgs &a, uint8_t *smem, 
   if (lane < 8 && (d.rows >> lane & 1u)) {
     const long long row = d.row[lane];
     const uint8_t *pool = static_cast<const uint8_t *>(part ? a.d.v_pool : a.d.k_pool);
-    bulk_load(smem + C::kOffCode + s * C::kCodeBytes + lane * 16 * kD, pool + row * kD, 16 * kD, &B.code_full[s]);
+    bulk_load_stream(smem + C::kOffCode + s * C::kCodeBytes + lane * 16 * kD, pool + row * kD, 16 * kD,
+                     &B.code_full[s], policy);
     if (per_token && part == 0) {
       float *dst = reinterpret_cast<float *>(smem + C::kOffCodeScale) + s * 2 * kTok + 16 * lane;
-      bulk_load(dst, a.d.k_scale + row, 64, &B.code_full[s]);
-      bulk_load(dst + kTok, a.d.v_scale + row, 64, &B.code_full[s]);
+      bulk_load_stream(dst, a.d.k_scale + row, 64, &B.code_full[s], policy);
+      bulk_load_stream(dst + kTok, a.d.v_scale + row, 64, &B.code_full[s], policy);
     }
   }
   return true;
@@ -226,6 +228,7 @@ __device__ __forceinline__ void plan_tiles(const PrefixArgs &a, uint8_t *smem, c
   PTile *tiles = reinterpret_cast<PTile *>(smem + C::kOffItems + kItemSlots * sizeof(PItem));
   const int lane = threadIdx.x & 31, S = a.d.S, H = a.d.cache.num_kv_heads;
   const bool per_token = kFp8 && a.d.scale_mode == PFKV_SCALE_PER_TOKEN;
+  const uint64_t policy = l2_evict_first_policy();
   constexpr int kGroups = kTok / 16, kAtOnce = 32 / kGroups;  // 16-token groups of a tile; tiles per look-up
   PWalk w{range_start(hdr, blockIdx.x), range_start(hdr, blockIdx.x + 1), (int)blockIdx.x};
   uint32_t n = 0;
@@ -264,7 +267,7 @@ __device__ __forceinline__ void plan_tiles(const PrefixArgs &a, uint8_t *smem, c
         if (lane == 0) mbar_arrive(&B.tile_full[n % kTileSlots]);
         if constexpr (kFp8) {
           for (int part = 0; part < 2 && have && ok; ++part)
-            ok = stage_codes<C, kD>(a, smem, B, d, 2 * n + part, part, per_token, abort);
+            ok = stage_codes<C, kD>(a, smem, B, d, 2 * n + part, part, per_token, policy, abort);
         }
         if (!ok) break;
       }
