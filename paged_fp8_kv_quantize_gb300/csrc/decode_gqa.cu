@@ -188,7 +188,10 @@ __global__ void __launch_bounds__(Cfg<kFp8, kD, kG, kNCW>::kThreads, Cfg<kFp8, k
     mbar_init_fence();
   }
   __syncthreads();
-  pdl_wait();  // the kernel before this one (the previous call's merge) is complete from here on
+  // The kernel before this one (the previous call's merge) is complete from
+  // here on; after a prefix kernel, which this one does not read from, only
+  // when it ends, so that this grid fills the SMs as that one's blocks leave.
+  if (a.join != kJoinBeside) pdl_wait();
   pdl_launch_dependents();  // the merge kernel may be scheduled; it waits for this grid to finish
 
   if (warp == kNCW) {
@@ -743,6 +746,7 @@ __global__ void __launch_bounds__(Cfg<kFp8, kD, kG, kNCW>::kThreads, Cfg<kFp8, k
   // every request of the call as timed out (its output is not valid).
   __syncthreads();
   if (threadIdx.x == 0) a.cta_abort[blockIdx.x] = *abort_flag != 0;
+  if (a.join == kJoinBeside) pdl_wait();
 }
 
 // ---------------------------------------------------------------- host side

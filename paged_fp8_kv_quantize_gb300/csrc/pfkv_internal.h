@@ -21,6 +21,8 @@ constexpr int kMaxCtas = 4096;  // decode split grid: at most this many CTAs (on
 WsLayout ws_layout(int batch, int q_heads, int v_dim, int max_splits, bool latent);
 constexpr size_t kLatentQTermBytes = 128 * 576;  // 128 operand rows (two terms x 64 heads) x 576 codes
 
+enum { kJoin = 1, kJoinBeside = 2 };  // DecodeArgs::join
+
 struct DecodeArgs {
   // cache
   int P, S, Hkv, D, Dv, scale_mode, dtype, kv_shared;
@@ -71,9 +73,11 @@ struct DecodeArgs {
   uint8_t *qterms;
   float *qfac;
   // Shared-prefix decode: request b's pages begin at table entry skip[b], and
-  // seq_lens counts the tokens from there on (NULL: 0).  join: every piece
+  // seq_lens counts the tokens from there on (NULL: 0).  join != 0: every piece
   // leaves a partial result (a one-piece request is not finished in the split
-  // kernel), and the caller's own kernel merges.
+  // kernel), and the caller's own kernel merges; kJoinBeside: the stream's
+  // kernel before the split kernel is one whose start means that all the split
+  // kernel reads is there, and whose end only the caller's merge waits for.
   const int *skip;
   int join;
   int piece_cost;  // cut rule: pages' worth of time one piece costs beyond its pages

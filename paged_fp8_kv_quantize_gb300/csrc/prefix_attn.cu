@@ -46,6 +46,7 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const PrefixA
   extern __shared__ int s_count[];  // block B: requests of each group
   __shared__ int s_sum[kPlanThreads / 32];
   pdl_wait();
+  pdl_launch_dependents();
   const int t = threadIdx.x, B = a.d.B, MP = a.d.MP, S = a.d.S;
   if ((int)blockIdx.x == B) {
     for (int g = t; g < a.n_groups; g += kPlanThreads) s_count[g] = 0;
@@ -290,10 +291,9 @@ int run_prefix(PrefixArgs a, cudaStream_t s) {
     if (dev < 64) attr_set.fetch_or(1ull << dev);
   }
   a.ctas = a.n_groups == 0 ? 0 : num_sms() < kMaxRanges ? num_sms() : kMaxRanges;
-  // an item's set-up and read-out cost about what 512 tokens of a small block do, and a range holds that and 256
-  // tokens of one at least
+  // an item's set-up and read-out cost about what 512 tokens of a small block do; a range holds 256 of them at least
   a.c0 = kCostHalf * ((512 + a.d.S - 1) / a.d.S);
-  a.min_units = a.c0 + kCostHalf * ((256 + a.d.S - 1) / a.d.S);
+  a.min_units = kCostHalf * ((256 + a.d.S - 1) / a.d.S);
   int rc = cuda_ok(launch_dependent(prefix_plan_kernel, dim3((unsigned)a.d.B + 1u), kPlanThreads,
                                     4 * (size_t)a.n_groups, s, a),
                    "prefix plan launch");
@@ -304,6 +304,7 @@ int run_prefix(PrefixArgs a, cudaStream_t s) {
     if (rc) return rc;
   }
   DecodeArgs own = a.d;
+  own.join = a.ctas > 0 ? kJoinBeside : kJoin;
   own.seq_lens = a.own_len;
   rc = launch_gqa_split(own, s);
   if (rc) return rc;
@@ -349,7 +350,6 @@ int launch_prefix_decode(const DecodeArgs &d, size_t ws_first, uint8_t *ws, cons
   a.ml = reinterpret_cast<float2 *>(ws + L.ml);
   a.o = reinterpret_cast<float *>(ws + L.o);
   a.d.skip = a.skip;
-  a.d.join = 1;
   const bool fp8 = d.dtype == PFKV_DTYPE_FP8_E4M3;
   if (d.D == 128) {
     if (fp8) return out_bf16 ? run_prefix<true, 128, 1>(a, s) : run_prefix<true, 128, 2>(a, s);

@@ -90,7 +90,7 @@ def test_work_line_covers_every_item_once(seed):
     H, G, S = int(rng.integers(1, 9)), int(rng.integers(1, 17)), int(rng.choice([16, 48, 64, 256]))
     groups = [(int(rng.integers(0, 70)), int(rng.integers(0, 300))) for _ in range(int(rng.integers(1, 12)))]
     c0 = HALF * -(-512 // S)
-    T, R, g, items = line(groups, H, G, int(rng.choice([1, 7, 152, 256])), c0, c0 + HALF * -(-256 // S))
+    T, R, g, items = line(groups, H, G, int(rng.choice([1, 7, 152, 256])), c0, HALF * -(-256 // S))
     if T == 0:
         assert R == 0
         return
