@@ -57,9 +57,11 @@ struct PrefixArgs {
 };
 
 // floor(k T / R): first unit of range k.
-__device__ __forceinline__ long long range_start(const PrefixHdr &h, long long k) { return k * h.T / h.R; }
+__device__ __forceinline__ long long range_start(const PrefixHdr &h, long long k) { return div_floor(k * h.T, h.R); }
 // The range that holds unit u.
-__device__ __forceinline__ int range_of(const PrefixHdr &h, long long u) { return (int)(((u + 1) * h.R - 1) / h.T); }
+__device__ __forceinline__ int range_of(const PrefixHdr &h, long long u) {
+  return (int)div_floor((u + 1) * h.R - 1, h.T);
+}
 
 // A group's items of one KV head on the line.
 constexpr int kCostHalf = 4, kCostFull = 7;  // a page's cost; measured 1.2 and 2.1 us per 128 tokens (FP8, D 128)

@@ -140,6 +140,17 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const PrefixA
 constexpr int kJoinThreads = 256;
 constexpr int kMaxJoin = 256 + 2 * kMaxRanges;
 
+// A lane's share of the OR of n words (16-byte aligned, room for a multiple of four).
+__device__ __forceinline__ int any_word(const int *words, int n, int lane) {
+  int any = 0;
+#pragma unroll 4
+  for (int i = 4 * lane; i < n; i += 128) {
+    const int4 v = *reinterpret_cast<const int4 *>(words + i);
+    any |= v.x | (i + 1 < n ? v.y : 0) | (i + 2 < n ? v.z : 0) | (i + 3 < n ? v.w : 0);
+  }
+  return any;
+}
+
 template <int kD, int kWarps>
 __global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(const PrefixArgs a) {
   constexpr int kCols = kD / 4, kPar = 32 / kCols;  // float4 columns; pieces a warp reads at once
@@ -147,9 +158,9 @@ __global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(const PrefixA
   __shared__ float4 s_acc[kWarps == 1 ? 1 : kWarps][32];
   pdl_wait();
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
-  const long long id = kWarps == 1 ? (long long)blockIdx.x * (kJoinThreads / 32) + warp : blockIdx.x;
-  if (id >= (long long)a.d.B * a.d.Hq) return;  // kWarps 1 only: a whole warp, and no block barrier below
-  const int b = (int)(id / a.d.Hq), hq = (int)(id - (long long)b * a.d.Hq);
+  const unsigned id = kWarps == 1 ? blockIdx.x * (kJoinThreads / 32) + warp : blockIdx.x;
+  if (id >= (unsigned)a.d.B * (unsigned)a.d.Hq) return;  // kWarps 1 only: a whole warp, and no block barrier below
+  const int b = (int)(id / (unsigned)a.d.Hq), hq = (int)(id - (unsigned)b * (unsigned)a.d.Hq);
   const int w0 = kWarps == 1 ? 0 : warp;  // this warp's place among the row's
   float *sw = s_w[kWarps == 1 ? warp : 0];
   // all that hangs on the request alone, at once
@@ -158,6 +169,12 @@ __global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(const PrefixA
   const uint32_t pre = a.pre_st[b];
   uint32_t st = pre | a.check_st[b];
   const PrefixHdr hdr = *a.hdr;
+  // whether a CTA of either kernel gave up: four words a load, all of them on their way beside the rest
+  int any = 0;
+  if (hq == 0 && w0 == 0) {
+    any |= any_word(a.d.cta_abort, a.d.n_ctas, lane);
+    any |= any_word(a.aborts, a.ctas, lane);
+  }
   // own pages
   int n_own = 0, c0 = 0;
   if (own > 0) {
@@ -205,9 +222,6 @@ __global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(const PrefixA
   if (kWarps == 1) __syncwarp();
   else __syncthreads();
   if (hq == 0 && w0 == 0) {
-    int any = 0;
-    for (int i = lane; i < a.d.n_ctas; i += 32) any |= a.d.cta_abort[i];
-    for (int i = lane; i < a.ctas; i += 32) any |= a.aborts[i];
     if (__any_sync(0xffffffffu, any != 0)) st |= PFKV_ST_TIMEOUT;
     if (lane == 0) a.d.status[b] = st;
   }

@@ -126,14 +126,14 @@ __device__ __forceinline__ bool walk_next(const PrefixArgs &a, PWalk &w, PItem &
     const PrefixGroup g = a.groups[lo];
     const HeadLine line = head_line(g.n, a.G, g.pages, a.c0);
     const long long rel = w.u - g.unit0;
-    it.h = (int)(rel / line.head);
+    it.h = (int)div_floor(rel, line.head);
     const long long in_head = rel - it.h * line.head;
-    const int blk = (int)min((long long)(line.blocks - 1), in_head / line.full);
+    const int blk = (int)min((long long)(line.blocks - 1), div_floor(in_head, line.full));
     const long long off = in_head - blk * line.full, seg = blk < line.blocks - 1 ? line.full : line.last;
     const long long end = min(seg, off + (w.u1 - w.u));
     const int cost = page_cost(line, blk);
-    it.p0 = (int)((max(0LL, off - a.c0) + cost - 1) / cost);
-    it.p1 = (int)((max(0LL, end - a.c0) + cost - 1) / cost);
+    it.p0 = (int)div_floor(max(0LL, off - a.c0) + cost - 1, cost);
+    it.p1 = (int)div_floor(max(0LL, end - a.c0) + cost - 1, cost);
     w.u += end - off;
     if (it.p1 <= it.p0) continue;
     it.first = g.first;
