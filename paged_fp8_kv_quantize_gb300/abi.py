@@ -175,16 +175,21 @@ def _dev(t, name, dtype=None):
     return t
 
 
-def _vec(t, name, n, dtype=torch.int32):
-    """An optional contiguous device tensor of n elements on the current device."""
+def _arg(t, name, n, dev, dtype=torch.int32):
+    """Address of an optional contiguous tensor of n elements on device dev (None: NULL).  One test for the sound
+    case: a call has a dozen of these."""
     if t is None:
         return None
-    _dev(t, name, dtype)
-    if t.numel() != n:
-        raise ValueError(f"{name} must have {n} elements, got {t.numel()}")
-    if t.device.index != torch.cuda.current_device():
+    if t.dtype is not dtype or t.get_device() != dev or t.numel() != n or not t.is_contiguous():
+        _dev(t, name, dtype)
+        if t.numel() != n:
+            raise ValueError(f"{name} must have {n} elements, got {t.numel()}")
         raise ValueError(f"{name} is on {t.device}, not on the current device")
-    return t
+    return t.data_ptr()
+
+
+def _raw_stream(stream, dev):
+    return stream.cuda_stream if stream is not None else torch.cuda.current_stream(dev).cuda_stream
 
 
 class PagedCache:
@@ -226,6 +231,18 @@ class PagedCache:
         return CacheDesc(self.P, self.S, self.H, self.D, self.Dv, int(self.kv_shared), self.dtype, self.scale_mode,
                          _ptr(self.k_pool), _ptr(self.v_pool), _ptr(self.k_scale), _ptr(self.v_scale),
                          _ptr(self.page_tags))
+
+    def _ref(self):
+        """desc() by reference, its struct kept from call to call and the addresses filled in anew."""
+        d = self.__dict__.get("_desc")
+        if d is None:
+            d = self._desc = self.desc()
+        d.k_pool = self.k_pool.data_ptr() if self.k_pool is not None else None
+        d.v_pool = self.v_pool.data_ptr() if self.v_pool is not None else None
+        d.k_scale = self.k_scale.data_ptr() if self.k_scale is not None else None
+        d.v_scale = self.v_scale.data_ptr() if self.v_scale is not None else None
+        d.page_tags = self.page_tags.data_ptr()
+        return ctypes.byref(d)
 
     def k_rows(self):
         return self.k_pool.view(self.P, self.H, self.S, self.D)
@@ -324,6 +341,7 @@ def prefix_workspace_bytes(cache: PagedCache, batch, num_q_heads, n_groups, max_
 
 
 _OUT_DTYPES = {torch.float32: 0, torch.bfloat16: 1}  # PFKV_OUT_*
+_prefix = lib.pfkv_paged_decode_attention_prefix
 
 
 def paged_decode_attention_prefix(cache, q, seq_lens, block_table, block_tags, prefix_group, prefix_pages,
@@ -334,31 +352,29 @@ def paged_decode_attention_prefix(cache, q, seq_lens, block_table, block_tags, p
     B, Hq, D = q.shape
     MP = block_table.shape[1]
     n_groups = prefix_pages.numel()
-    dev = q.device
     if D != cache.D:
         raise ValueError(f"q must have head_dim {cache.D}, got {D}")
     if workspace is None:
         n = prefix_workspace_bytes(cache, B, Hq, n_groups, max_splits)
         if n >= 1 << 62:
             raise PfkvError("pfkv_prefix_workspace_bytes", -2)
-        workspace = torch.empty(n, dtype=torch.uint8, device=dev)
+        workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
     if out is None:
-        out = torch.empty(B, Hq, cache.Dv, dtype=out_dtype, device=dev)
-    if out.dtype not in _OUT_DTYPES:
+        out = torch.empty((B, Hq, cache.Dv), dtype=out_dtype, device=q.device)
+    kind = _OUT_DTYPES.get(out.dtype)
+    if kind is None:
         raise ValueError(f"out must be torch.float32 or torch.bfloat16, got {out.dtype}")
     if status is None:
-        status = torch.empty(B, dtype=torch.int32, device=dev)
-    rows = B * cache.H * cache.D
-    d = cache.desc()
-    rc = lib.pfkv_paged_decode_attention_prefix(
-        ctypes.byref(d), _ptr(_vec(k_new, "k_new", rows, torch.bfloat16)),
-        _ptr(_vec(v_new, "v_new", rows, torch.bfloat16)), _ptr(_vec(q, "q", B * Hq * D, torch.bfloat16)), Hq,
-        _ptr(_vec(seq_lens, "seq_lens", B)), _ptr(_vec(block_table, "block_table", B * MP)),
-        _ptr(_vec(block_tags, "block_tags", B * MP)), B, MP, _ptr(_vec(prefix_group, "prefix_group", B)),
-        _ptr(_vec(prefix_pages, "prefix_pages", n_groups)), n_groups, float(softmax_scale), int(flags),
-        int(max_splits), _ptr(_dev(workspace, "workspace", torch.uint8)), workspace.numel(),
-        _ptr(_vec(out, "out", B * Hq * D, out.dtype)), _OUT_DTYPES[out.dtype],
-        _ptr(_vec(status, "status", B)), _stream(stream))
+        status = seq_lens.new_empty(B)
+    bf16, rows, dev = torch.bfloat16, B * cache.H * cache.D, torch.cuda.current_device()
+    rc = _prefix(
+        cache._ref(), _arg(k_new, "k_new", rows, dev, bf16), _arg(v_new, "v_new", rows, dev, bf16),
+        _arg(q, "q", B * Hq * D, dev, bf16), Hq, _arg(seq_lens, "seq_lens", B, dev),
+        _arg(block_table, "block_table", B * MP, dev), _arg(block_tags, "block_tags", B * MP, dev), B, MP,
+        _arg(prefix_group, "prefix_group", B, dev), _arg(prefix_pages, "prefix_pages", n_groups, dev), n_groups,
+        softmax_scale, flags, max_splits, _arg(workspace, "workspace", workspace.numel(), dev, torch.uint8),
+        workspace.numel(), _arg(out, "out", B * Hq * D, dev, out.dtype), kind, _arg(status, "status", B, dev),
+        _raw_stream(stream, dev))
     _check("pfkv_paged_decode_attention_prefix", rc)
     return out, status
 
@@ -410,16 +426,18 @@ def handoff_bf16_to_fp8(src: PagedCache, dst: PagedCache, src_pages, dst_pages, 
     return page_status
 
 
+_page_copy, _page_fork = lib.pfkv_page_copy, lib.pfkv_page_fork
+_page_release, _page_compact = lib.pfkv_page_release, lib.pfkv_page_compact
+
+
 def page_copy(cache: PagedCache, src_pages, dst_pages, slots=None, page_status=None, stream=None):
     """Copy pages src_pages[i] to dst_pages[i] of the same cache, the first slots[i] slots of each (None: all)."""
-    n = src_pages.numel()
-    _vec(dst_pages, "dst_pages", n)
-    _vec(slots, "slots", n)
+    n, dev = src_pages.numel(), torch.cuda.current_device()
     if page_status is None:
-        page_status = torch.empty(n, dtype=torch.int32, device=src_pages.device)
-    d = cache.desc()
-    rc = lib.pfkv_page_copy(ctypes.byref(d), _ptr(_vec(src_pages, "src_pages", n)), _ptr(dst_pages), _ptr(slots), n,
-                            _ptr(_vec(page_status, "page_status", n)), _stream(stream))
+        page_status = src_pages.new_empty(n)
+    rc = _page_copy(cache._ref(), _arg(src_pages, "src_pages", n, dev), _arg(dst_pages, "dst_pages", n, dev),
+                    _arg(slots, "slots", n, dev), n, _arg(page_status, "page_status", n, dev),
+                    _raw_stream(stream, dev))
     _check("pfkv_page_copy", rc)
     return page_status
 
@@ -481,26 +499,27 @@ class PageAllocator:
              stream=None):
         """Rows children[i] of block_table (and block_tags) get the first lens[i] tokens of rows parents[i]: full
         pages shared, the partly filled last one copied into a fresh page (pfkv_page_fork).  -> fork_status [n]"""
-        n = parents.numel()
+        n, dev = parents.numel(), torch.cuda.current_device()
         B, MP = block_table.shape
         if fork_status is None:
-            fork_status = torch.empty(n, dtype=torch.int32, device=parents.device)
-        d = cache.desc()
-        rc = lib.pfkv_page_fork(
-            _ptr(self.state), _ptr(_vec(cache.page_tags, "page_tags", cache.P)), _ptr(self.refs), ctypes.byref(d),
-            _ptr(_vec(parents, "parents", n)), _ptr(_vec(children, "children", n)), _ptr(_vec(lens, "lens", n)), n,
-            _ptr(_vec(block_table, "block_table", B * MP)), _ptr(_vec(block_tags, "block_tags", B * MP)), B, MP,
-            int(flags), _ptr(_vec(fork_status, "fork_status", n)), _stream(stream))
+            fork_status = parents.new_empty(n)
+        rc = _page_fork(
+            self.state.data_ptr(), _arg(cache.page_tags, "page_tags", cache.P, dev),
+            _arg(self.refs, "refs", self.num_pages, dev), cache._ref(), _arg(parents, "parents", n, dev),
+            _arg(children, "children", n, dev), _arg(lens, "lens", n, dev), n,
+            _arg(block_table, "block_table", B * MP, dev), _arg(block_tags, "block_tags", B * MP, dev), B, MP, flags,
+            _arg(fork_status, "fork_status", n, dev), _raw_stream(stream, dev))
         _check("pfkv_page_fork", rc)
         return fork_status
 
     def release(self, pages, page_status=None, stream=None):
         """Take one holder off each listed page; a page returns to the free list with its last (pfkv_page_release)."""
-        n = pages.numel()
+        n, dev = pages.numel(), torch.cuda.current_device()
         if page_status is None:
-            page_status = torch.empty(n, dtype=torch.int32, device=pages.device)
-        rc = lib.pfkv_page_release(_ptr(self.state), _ptr(self.refs), _ptr(_vec(pages, "pages", n)), n,
-                                   _ptr(_vec(page_status, "page_status", n)), _stream(stream))
+            page_status = pages.new_empty(n)
+        rc = _page_release(self.state.data_ptr(), _arg(self.refs, "refs", self.num_pages, dev),
+                           _arg(pages, "pages", n, dev), n, _arg(page_status, "page_status", n, dev),
+                           _raw_stream(stream, dev))
         _check("pfkv_page_release", rc)
         return page_status
 
@@ -510,17 +529,14 @@ class PageAllocator:
         -> (moved_src, moved_dst, n_moved [1]) on the device; the lists are filled up to n_moved."""
         B, MP = block_table.shape
         room = self.num_pages // 2  # no pool needs more moves
-        m = room if max_moves is None else min(int(max_moves), room)
-        dev = self.state.device
-        src = torch.empty(max(m, 1), dtype=torch.int32, device=dev)[:m]
-        dst = torch.empty(max(m, 1), dtype=torch.int32, device=dev)[:m]
-        n_moved = torch.empty(1, dtype=torch.int32, device=dev)
-        d = cache.desc()
-        rc = lib.pfkv_page_compact(
-            _ptr(self.state), _ptr(_vec(cache.page_tags, "page_tags", cache.P)), _ptr(self.refs), ctypes.byref(d),
-            _ptr(_vec(block_table, "block_table", B * MP)), _ptr(_vec(block_tags, "block_tags", B * MP)),
-            _ptr(_vec(used, "used", B)), B, MP, m, _ptr(src) if m else None, _ptr(dst) if m else None, _ptr(n_moved),
-            _stream(stream))
+        m, dev = room if max_moves is None else min(int(max_moves), room), torch.cuda.current_device()
+        src, dst, n_moved = block_table.new_empty(max(m, 0)), block_table.new_empty(max(m, 0)), block_table.new_empty(1)
+        rc = _page_compact(
+            self.state.data_ptr(), _arg(cache.page_tags, "page_tags", cache.P, dev),
+            _arg(self.refs, "refs", self.num_pages, dev), cache._ref(),
+            _arg(block_table, "block_table", B * MP, dev), _arg(block_tags, "block_tags", B * MP, dev),
+            _arg(used, "used", B, dev), B, MP, m, src.data_ptr() or None, dst.data_ptr() or None, n_moved.data_ptr(),
+            _raw_stream(stream, dev))
         _check("pfkv_page_compact", rc)
         return src, dst, n_moved
 

@@ -172,7 +172,9 @@ __global__ void __launch_bounds__(kCopyThreads) fork_apply_kernel(const ForkArgs
 enum { kShared = 0x10000u, kLast = 0x20000u, kOver = 0x40000u };
 constexpr int kOverBase = 1 << 30;
 constexpr int kReleaseOneBlock = 4096;
-constexpr int kReleasePer = 4;  // consecutive entries per thread of the ordered walk
+// Consecutive entries per thread of the ordered walk (64 rows of 1875 shared
+// pages given back: 42 us in the apply kernel with 4, 20 with 16).
+constexpr int kReleasePer = 16;
 
 struct ReleaseArgs {
   void *state;
@@ -223,34 +225,39 @@ __device__ __forceinline__ void release_shared(const ReleaseArgs &r, const Alloc
 // One block, in list order: pushes the pages that nobody holds any more.
 __device__ __forceinline__ void release_push(const ReleaseArgs &r, const AllocView &v, int *s_warp) {
   const int fc = v.hdr->free_count, t = threadIdx.x, lane = t & 31, warp = t >> 5;
+  const bool vec = (reinterpret_cast<uintptr_t>(r.status) & 15u) == 0;
   int pushed = 0;
   for (int base = 0; base < r.n; base += kAT * kReleasePer) {
-    int out[kReleasePer], cnt = 0;
+    const long long i0 = (long long)base + t * kReleasePer;
+    uint32_t st[kReleasePer];
+    if (vec && i0 + kReleasePer <= r.n) {
+#pragma unroll
+      for (int j = 0; j < kReleasePer; j += 4) {
+        const uint4 x = __ldcg(reinterpret_cast<const uint4 *>(r.status + i0 + j));
+        st[j] = x.x; st[j + 1] = x.y; st[j + 2] = x.z; st[j + 3] = x.w;
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < kReleasePer; ++j) st[j] = i0 + j < r.n ? __ldcg(&r.status[i0 + j]) : 0u;
+    }
+    uint32_t push = 0u;  // bit j: entry j returns its page
 #pragma unroll
     for (int j = 0; j < kReleasePer; ++j) {
-      const long long i = (long long)base + t * kReleasePer + j;
-      out[j] = -1;
-      if (i >= r.n) continue;
-      const uint32_t st = __ldcg(&r.status[i]);
-      if (st != kLast && st != kOver) continue;
-      const int p = r.pages[i];
-      bool push;
+      if (!(st[j] & (kLast | kOver))) continue;
+      const int i = (int)i0 + j, p = r.pages[i];
       uint32_t fin = 0u;
-      if (st == kLast) {
-        push = __ldcg(&v.mark[p]) == -((int)i + 1);
+      if (st[j] == kLast) {
+        push |= (uint32_t)(__ldcg(&v.mark[p]) == -(i + 1)) << j;
       } else {
         const int h = holders(r, p);
         int earlier = 0;
-        for (int k = 0; k < (int)i && earlier < h; ++k) earlier += r.pages[k] == p;
-        push = earlier == h - 1;
+        for (int k = 0; k < i && earlier < h; ++k) earlier += r.pages[k] == p;
+        push |= (uint32_t)(earlier == h - 1) << j;
         if (earlier >= h) fin = PFKV_ST_NOT_HELD;
       }
       r.status[i] = fin;
-      if (push) {
-        out[j] = p;
-        ++cnt;
-      }
     }
+    const int cnt = __popc(push);
     // exclusive scan of cnt over the block
     int incl = cnt;
 #pragma unroll
@@ -273,9 +280,7 @@ __device__ __forceinline__ void release_push(const ReleaseArgs &r, const AllocVi
     }
     __syncthreads();
     int at = fc + pushed + s_warp[warp] + incl - cnt;
-#pragma unroll
-    for (int j = 0; j < kReleasePer; ++j)
-      if (out[j] >= 0) v.stack[at++] = out[j];
+    for (uint32_t m = push; m; m &= m - 1) v.stack[at++] = r.pages[i0 + __ffs(m) - 1];
     pushed += s_warp[32];
     __syncthreads();  // s_warp is reused, and the pushed ids are read below
   }

@@ -265,17 +265,22 @@ def test_release_without_sharing_is_free():
     assert not b.refs.any()
 
 
-def test_compact_bounds_stale_rows_and_no_tags():
-    p = Pair("fp8_token", 3000, 5, 400, 8)  # three chunks of the scan
+@pytest.mark.parametrize("P", [3000, 20000])  # one block plans the moves; many do
+def test_compact_bounds_and_stale_rows(P):
+    p = Pair("one_slot" if P > 3000 else "fp8_token", P, 5, 400, 8)
+    others = p.ref.alloc(P // 3)  # pages of other owners among the rows', two in three given back
+    assert p.alloc.alloc(P // 3, p.cache.page_tags)[0].tolist() == others
     for b in range(5):
-        p.fill_row(b, 380 * 16)
+        p.fill_row(b, 220 * p.S if P == 3000 else 380 * p.S)
+        assert p.lens[b]
+    p.release(p.rng.permutation(others)[: 2 * len(others) // 3].tolist())
     for b in (0, 2):
-        p.release(p.table[b, :380].tolist())
+        p.release(p.table[b, :220 if P == 3000 else 380].tolist())
         p.table[b] = -1
-    p.table[4, 390:] = p.table[4, 370:380]  # past the live entries: left as they were
+    p.table[4, 390:] = p.table[4, 210:220]  # past the live entries: left as they were
     p.btags[4, 5] ^= np.uint32(1)  # a stale mapping stays stale
     p.upload()
-    used = [0, 380, 0, 380, 380]
+    used = [0, *([220] if P == 3000 else [380]), 0, *([220, 220] if P == 3000 else [380, 380])]
     before = p.table.copy()
     assert p.compact(used=used, max_moves=0) == []
     assert len(p.compact(used=used, max_moves=33)) == 33
@@ -285,6 +290,25 @@ def test_compact_bounds_stale_rows_and_no_tags():
     assert moves and p.table[4, 5] == before[4, 5] and np.array_equal(p.table[4, 390:], before[4, 390:])
     assert p.compact(used=used) == []
     p.check("nothing left")
+
+
+@pytest.mark.parametrize("P", [1, 2, 15, 16, 17, 1024, 16384, 16385])
+def test_compact_pool_sizes(P):
+    p = Pair("one_slot", P, 3, P, 14)
+    p.fill_row(0, max(1, P // 2))
+    p.fill_row(1, P - max(1, P // 2) - P // 5)
+    if P > 1:
+        gone = p.rng.permutation(p.table[0, : p.lens[0]])[: P // 3].tolist()
+        p.release(gone)
+        p.table[0][np.isin(p.table[0], gone)] = -1
+        p.upload()
+    p.compact(max_moves=P // 9)
+    p.check("some")
+    p.compact()
+    p.check("all")
+
+
+def test_compact_empty_full_and_without_tags():
     # an empty pool and a full one
     for n in (0, 50):
         q = Pair("one_slot", 50, 1, 50, 9)
