@@ -23,7 +23,7 @@
 //                   128-byte-swizzled layout.  FP8: e4m3 -> f16 from staged
 //                   codes, once per CTA.  BF16: asynchronous copies from the
 //                   pool, two tiles ahead.
-//   warps 12, 14    issue the MMAs of QK^T and of PV.
+//   warps 12, 14    issue the MMAs of half 0 and 1.
 //   warp 13         planner: works out the CTA's items and where each tile's
 //                   rows lie (bounds-checked page ids), so that nobody else
 //                   waits for a table entry; FP8: bulk-copies the codes into
@@ -94,10 +94,12 @@ struct PCfg {
   __host__ __device__ static constexpr uint32_t col_x(int t, int b) { return 128 * kBufs + (uint32_t)(t * kBufs + b) * 32; }
   __host__ __device__ static constexpr uint32_t col_o(int t) { return 512 - (uint32_t)(2 - t) * kD; }
   static_assert((kTerms == 3 ? 192 : 128) * kBufs + 2 * kD <= 512, "tensor memory plan");
-  // Growth of a row's maximum (log2) that moves its reference.  f16: weights up
-  // to 2^14, times V scales of at most twice their reference, stay below 65504;
-  // bf16 has the range of fp32.
-  static constexpr float kGrow = kFp8 ? 14.f : 60.f;
+  // A row's reference is set kHead above its maximum (log2) and moves when a
+  // score exceeds it by kGrow.  f16: weights up to 2^14, times V scales of at
+  // most twice their reference, stay below 65504; bf16 has the range of fp32.
+  // Headroom saves moves and costs small weights bits (f16 steps are 2^-24 of
+  // the reference at least), which one term, of a bf16 output, can spare.
+  static constexpr float kHead = kFp8 && kTerms == 1 ? 4.f : 0.f, kGrow = kFp8 ? 14.f : 60.f;
   static constexpr uint32_t kOffQ = 0, kOffT = 2 * kQBytes, kOffCode = kOffT + kSlots * kTBytes;
   static constexpr uint32_t kOffCodeScale = kOffCode + kStage * kCodeBytes;  // K and V scales beside the codes of K
   static constexpr uint32_t kOffScale = kOffCodeScale + kStage * 2 * kTok * 4;
@@ -465,11 +467,6 @@ __device__ __forceinline__ void loader_bf16(const PrefixArgs &a, uint8_t *smem, 
 
 // ---------------------------------------------------------------- MMA issuers (warps 12 and 14)
 
-// A half's unit is 64 tokens of a tile; the units of a tile in the order
-// (64 tokens, half), in split mode half t takes the t-th 64 tokens.  Unit u of
-// a half has score buffer u % kBufs.
-
-//
 // The whole warp runs the loops and one elected lane issues: everything that an
 // MMA takes is then the same in all lanes and lives in uniform registers.
 // (With one thread running the loops, each MMA paid for moving its
@@ -503,97 +500,93 @@ __device__ __forceinline__ int next_item(uint8_t *smem, const PBars &B, uint32_t
   return n_tok;
 }
 
-// S[t][b] = Q_t K^T, once the PV that last read P from the buffer is done.
+// Half t's products.  Unit v of an item is 64 of its tokens: QK^T of the first
+// kBufs units, then for each unit PV, once P is in place, and the QK^T kBufs
+// units further on into the score buffer that this PV reads P from.  MMAs that
+// one thread issues execute in the order of issue, so that no wait lies between
+// the two; and with a warp of its own a half that waits for a moved reference
+// does not hold up the other.
 template <bool kFp8, int kD, int kTerms>
-__device__ __forceinline__ void issue_qk(const PrefixArgs &a, uint8_t *smem, const PBars &B, uint32_t tmem,
-                                         volatile int *abort) {
+__device__ __forceinline__ void issue_half(const PrefixArgs &a, uint8_t *smem, const PBars &B, uint32_t tmem, int t,
+                                           volatile int *abort) {
   using C = PCfg<kFp8, kD, kTerms>;
-  const uint64_t dq = umma_sdesc(smem_addr(smem + C::kOffQ), 16, 1024, 2);
+  const uint64_t dq = umma_sdesc(smem_addr(smem + C::kOffQ) + t * C::kQBytes, 16, 1024, 2);
   const uint64_t dk = umma_sdesc(smem_addr(smem + C::kOffT), 16, 1024, 2);
-  uint32_t tile = 0, u[2] = {0, 0};
-  bool ok = true, split = false;
-  for (uint32_t i = 0; ok; ++i) {
-    const int n_tok = next_item<C>(smem, B, i, a.d.S, split, abort);
-    if (n_tok == 0) break;
-    ok = mbar_wait_warp(&B.q_ready[0], i & 1u, abort) && mbar_wait_warp(&B.q_ready[1], i & 1u, abort);
-    for (int t0 = 0; ok && t0 < n_tok; t0 += kTok, ++tile) {
-      const uint32_t ik = 2 * tile, slot = ik % C::kSlots;
-      ok = mbar_wait_warp(&B.full[slot], (ik / C::kSlots) & 1u, abort);
-      const uint64_t dks = dk + (uint64_t)((slot * C::kTBytes) >> 4);
-#pragma unroll
-      for (int c = 0; c < 2; ++c)
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          if (!ok || t0 + 64 * c >= n_tok || (split && c != t)) continue;
-          const uint32_t b = u[t] % C::kBufs;
-          ok = mbar_wait_warp(&B.pv_done[2 * t + b], ((u[t] / C::kBufs) & 1u) ^ 1u, abort);
-          if (!ok) continue;
-          ++u[t];
-          tc_fence_after();
-          const uint32_t d = tmem + C::col_s(t, 0) + 64 * b;
-          if (elect_one()) {
-#pragma unroll
-            for (int s = 0; s < kD / 16; ++s)
-              umma_f16(d, dq + (uint64_t)((t * C::kQBytes + (s >> 2) * C::kBlk + (s & 3) * 32) >> 4),
-                       dks + (uint64_t)(((s >> 2) * C::kBlk + c * 64 * 128 + (s & 3) * 32) >> 4), C::kIdQK, s ? 1u : 0u);
-            umma_commit(&B.s_full[2 * t + b]);
-          }
-          __syncwarp();
-        }
-      if (ok && elect_one()) umma_commit(&B.empty[slot]);
-    }
-    // the query operands may be replaced
-    if (elect_one()) {
-      umma_commit(&B.q_read[0]);
-      umma_commit(&B.q_read[1]);
-    }
-  }
-  drain_mmas(&B.drain[0]);
-}
-
-// O[t] += P V, once P is in place.
-template <bool kFp8, int kD, int kTerms>
-__device__ __forceinline__ void issue_pv(const PrefixArgs &a, uint8_t *smem, const PBars &B, uint32_t tmem,
-                                         volatile int *abort) {
-  using C = PCfg<kFp8, kD, kTerms>;
   const uint64_t dv = umma_sdesc(smem_addr(smem + C::kOffT), C::kBlk, 1024, 2);
-  uint32_t tile = 0, u[2] = {0, 0};
+  const uint32_t s_col = tmem + C::col_s(0, 0) + (uint32_t)(t * C::kBufs) * 64;
+  const uint32_t x_col = tmem + C::col_x(0, 0) + (uint32_t)(t * C::kBufs) * 32;
+  const uint32_t o_col = tmem + C::col_o(0) + (uint32_t)t * kD;
+  uint32_t tile0 = 0, u0 = 0;  // tiles, units before this item
   bool ok = true, split = false;
   for (uint32_t i = 0; ok; ++i) {
     const int n_tok = next_item<C>(smem, B, i, a.d.S, split, abort);
     if (n_tok == 0) break;
-    uint32_t acc[2] = {0u, 0u};
-    for (int t0 = 0; ok && t0 < n_tok; t0 += kTok, ++tile) {
-      const uint32_t iv = 2 * tile + 1, slot = iv % C::kSlots;
-      ok = mbar_wait_warp(&B.full[slot], (iv / C::kSlots) & 1u, abort);
-      const uint64_t dvs = dv + (uint64_t)((slot * C::kTBytes) >> 4);
+    const int tiles = (n_tok + kTok - 1) / kTok, chunks = (n_tok + 63) / 64;
+    const int units = split ? (chunks - t + 1) / 2 : chunks;
+    // tile of unit v, which 64 tokens of it, and whether the half is done with the tile then
+    auto tile_of = [&](int v) { return split ? v : v >> 1; };
+    auto part_of = [&](int v) { return split ? t : v & 1; };
+    auto last_of = [&](int v) { return split || (v & 1) || v == units - 1; };
+    auto slot_of = [&](int k, int part) { return (2 * (tile0 + (uint32_t)k) + (uint32_t)part) % C::kSlots; };
+    auto wait_tile = [&](int k, int part) {
+      const uint32_t j = 2 * (tile0 + (uint32_t)k) + (uint32_t)part;
+      return mbar_wait_warp(&B.full[j % C::kSlots], (j / C::kSlots) & 1u, abort);
+    };
+    auto qk = [&](int v) {
+      const int k = tile_of(v), c = part_of(v);
+      if (split || !(v & 1)) {
+        ok = wait_tile(k, 0);
+        if (!ok) return;
+        tc_fence_after();
+      }
+      const uint32_t slot = slot_of(k, 0), b = (u0 + (uint32_t)v) % C::kBufs;
+      const uint64_t dks = dk + (uint64_t)((slot * C::kTBytes + c * 64 * 128) >> 4);
+      if (elect_one()) {
 #pragma unroll
-      for (int c = 0; c < 2; ++c)
+        for (int s = 0; s < kD / 16; ++s)
+          umma_f16(s_col + 64 * b, dq + (uint64_t)(((s >> 2) * C::kBlk + (s & 3) * 32) >> 4),
+                   dks + (uint64_t)(((s >> 2) * C::kBlk + (s & 3) * 32) >> 4), C::kIdQK, s ? 1u : 0u);
+        umma_commit(&B.s_full[2 * t + b]);
+        if (last_of(v)) umma_commit(&B.empty[slot]);
+      }
+      __syncwarp();
+    };
+    ok = mbar_wait_warp(&B.q_ready[t], i & 1u, abort);
+    for (int v = 0; ok && v < C::kBufs && v < units; ++v) qk(v);
+    for (int v = 0; ok && v < units; ++v) {
+      const int k = tile_of(v), c = part_of(v);
+      const uint32_t slot = slot_of(k, 1), u = u0 + (uint32_t)v, b = u % C::kBufs;
+      if (split || !(v & 1)) ok = wait_tile(k, 1);
+      ok = ok && mbar_wait_warp(&B.p_full[2 * t + b], (u / C::kBufs) & 1u, abort);
+      if (!ok) break;
+      tc_fence_after();
+      const uint64_t dvs = dv + (uint64_t)((slot * C::kTBytes + c * 64 * 128) >> 4);
+      if (elect_one()) {
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          if (!ok || t0 + 64 * c >= n_tok || (split && c != t)) continue;
-          const uint32_t b = u[t] % C::kBufs;
-          ok = mbar_wait_warp(&B.p_full[2 * t + b], (u[t] / C::kBufs) & 1u, abort);
-          if (!ok) continue;
-          ++u[t];
-          tc_fence_after();
-          const uint32_t s0 = tmem + C::col_s(t, 0) + 64 * b, x0 = tmem + C::col_x(t, 0) + 32 * b;
-          if (elect_one()) {
+        for (int q = 0; q < kTerms; ++q)
 #pragma unroll
-            for (int k = 0; k < kTerms; ++k)
-#pragma unroll
-              for (int s = 0; s < 4; ++s)
-                umma_f16_ts(tmem + C::col_o(t), (k < 2 ? s0 + 32 * k : x0) + 8 * s,
-                            dvs + (uint64_t)((c * 64 * 128 + s * 2048) >> 4), C::kIdPV, k + s ? 1u : acc[t]);
-            umma_commit(&B.pv_done[2 * t + b]);
-          }
-          __syncwarp();
-          acc[t] = 1u;
-        }
-      if (ok && elect_one()) umma_commit(&B.empty[slot]);
+          for (int s = 0; s < 4; ++s)
+            umma_f16_ts(o_col, (q < 2 ? s_col + 64 * b + 32 * q : x_col + 32 * b) + 8 * s,
+                        dvs + (uint64_t)((s * 2048) >> 4), C::kIdPV, q + s || v > 0 ? 1u : 0u);
+        umma_commit(&B.pv_done[2 * t + b]);
+        if (last_of(v)) umma_commit(&B.empty[slot]);
+      }
+      __syncwarp();
+      if (v + C::kBufs < units) qk(v + C::kBufs);
     }
+    // a tile of which this half had nothing (split, at most 64 tokens) is let go all the same
+    if (ok && split && units < tiles)
+      for (int part = 0; part < 2 && ok; ++part) {
+        ok = wait_tile(tiles - 1, part);
+        if (ok && elect_one()) umma_commit(&B.empty[slot_of(tiles - 1, part)]);
+        __syncwarp();
+      }
+    if (elect_one()) umma_commit(&B.q_read[t]);  // the query operand may be replaced
+    __syncwarp();
+    tile0 += (uint32_t)tiles;
+    u0 += (uint32_t)units;
   }
-  drain_mmas(&B.drain[1]);
+  drain_mmas(&B.drain[t]);
 }
 
 // ---------------------------------------------------------------- softmax (warps 0-7)
@@ -707,7 +700,7 @@ __device__ __forceinline__ void softmax_rows(const PrefixArgs &a, uint8_t *smem,
       // move the reference
       const bool grow = mx > m + C::kGrow || first;
       if (__any_sync(0xffffffffu, grow || moved != 1.f)) {
-        const float mn = grow ? fmaxf(m, mx) : m;
+        const float mn = grow ? mx + C::kHead : m;
         const float al = first ? 0.f : fast_exp2(m - mn);
         l *= al;
         if (!first) {
@@ -816,7 +809,7 @@ __global__ void __launch_bounds__(kPThreads, 1) prefix_kernel(const PrefixArgs a
   if (threadIdx.x == 0) {
     for (int i = 0; i < kMaxSlots; ++i) {
       mbar_init(&B.full[i], 4);
-      mbar_init(&B.empty[i], 1);
+      mbar_init(&B.empty[i], 2);  // both halves
       mbar_init(&B.code_full[i], 1);
       mbar_init(&B.code_empty[i], 4);
     }
@@ -862,9 +855,9 @@ __global__ void __launch_bounds__(kPThreads, 1) prefix_kernel(const PrefixArgs a
     } else {
       regs_dec<kRegsRest>();
       if (warp == 12) {
-        issue_qk<kFp8, kD, kTerms>(a, smem, B, tmem, abort);
+        issue_half<kFp8, kD, kTerms>(a, smem, B, tmem, 0, abort);
       } else if (warp == 14) {
-        issue_pv<kFp8, kD, kTerms>(a, smem, B, tmem, abort);
+        issue_half<kFp8, kD, kTerms>(a, smem, B, tmem, 1, abort);
       } else if (warp == 13) {
         plan_tiles<kFp8, kD, kTerms>(a, smem, B, hdr, abort);
       }

@@ -173,7 +173,7 @@ enum { kShared = 0x10000u, kLast = 0x20000u, kOver = 0x40000u };
 constexpr int kOverBase = 1 << 30;
 constexpr int kReleaseOneBlock = 4096;
 // Consecutive entries per thread of the ordered walk (64 rows of 1875 shared
-// pages given back: 42 us in the apply kernel with 4, 20 with 16).
+// pages given back: the apply kernel took 42 us with 4, 16 with 16).
 constexpr int kReleasePer = 16;
 
 struct ReleaseArgs {
