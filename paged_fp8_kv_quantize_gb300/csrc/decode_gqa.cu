@@ -845,7 +845,10 @@ int run_split(DecodeArgs &a, cudaStream_t s, const CUtensorMap &mk, const CUtens
   a.st_groups = a.Hkv;
   a.target_items = a.n_ctas * 8;
   a.min_chunk_pages = (1024 + a.S - 1) / a.S;
-  a.piece_cost = kPieceCost;
+  // (a shared-prefix call's own contexts are short, and its pages may be large:
+  // there 256 tokens' worth; 64 contexts of 32-640 tokens, page 64: 31 us
+  // against 35 with 16 pages)
+  a.piece_cost = a.join ? max(1, 16 * kPieceCost / a.S) : kPieceCost;
   if (a.n_ctas > kMaxCtas) return PFKV_ERR_UNSUPPORTED;  // more KV heads than abort words
   // The split kernel is a programmatic dependent of the stream's previous
   // kernel: its CTAs take SMs as that kernel's blocks drain and wait for it

@@ -25,6 +25,7 @@ constexpr int kRows = 256;       // query rows of an item
 
 struct PrefixGroup {
   int first, n;      // its requests: members[first .. first + n)
+  int lead, pad;     // the first of them
   int pages, item0;  // prefix pages, number of its first item
   long long unit0;   // its first unit on the line
 };
@@ -33,6 +34,13 @@ struct PrefixHdr {
   long long T;
   int R;  // ranges; 0 when no group has a prefix
   int pad;
+};
+
+// Where the join finds a row's pieces of the prefix: n of them, piece i in row
+// `row` of slot0 + i, or, where an item's halves left one each (sh = 1), in row
+// `row` + (i & 1) kRows / 2 of slot0 + i / 2.
+struct PrefixRow {
+  int slot0, n, row, sh;
 };
 
 struct PrefixArgs {
@@ -50,6 +58,7 @@ struct PrefixArgs {
   uint32_t *check_st;   // [B] status bits of the prefix pages
   int *rank, *members;  // [B] place of a request in its group; requests by group
   PrefixGroup *groups;  // [n_groups]
+  PrefixRow *rows;      // [B][Hq], written beside the products
   PrefixHdr *hdr;
   float2 *ml;   // [slot][kRows]
   float *o;     // [slot][kRows][D]

@@ -43,17 +43,23 @@ __device__ __forceinline__ int block_sum(int v, int *s_sum) {
 
 // Block b < B: request b.  Block B: the groups' segments of the work line.
 __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const PrefixArgs a) {
-  extern __shared__ int s_count[];  // block B: requests of each group
+  extern __shared__ int s_count[];  // block B: requests of each group, then the first of each
   __shared__ int s_sum[kPlanThreads / 32];
   pdl_wait();
   pdl_launch_dependents();
   const int t = threadIdx.x, B = a.d.B, MP = a.d.MP, S = a.d.S;
   if ((int)blockIdx.x == B) {
-    for (int g = t; g < a.n_groups; g += kPlanThreads) s_count[g] = 0;
+    int *s_lead = s_count + a.n_groups;
+    for (int g = t; g < a.n_groups; g += kPlanThreads) {
+      s_count[g] = 0;
+      s_lead[g] = B;
+    }
     __syncthreads();
     for (int b = t; b < B; b += kPlanThreads) {
       const int g = a.group_of[b];
-      if (g >= 0 && g < a.n_groups) atomicAdd(&s_count[g], 1);
+      if (g < 0 || g >= a.n_groups) continue;
+      atomicAdd(&s_count[g], 1);
+      atomicMin(&s_lead[g], b);
     }
     __syncthreads();
     if (t < 32) {  // 32 groups at a time, their sums carried along
@@ -79,7 +85,7 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const PrefixA
             xu += yu;
           }
         }
-        if (g < a.n_groups) a.groups[g] = PrefixGroup{first + xn - n, n, pages, item + xi - items, unit + xu - units};
+        if (g < a.n_groups) a.groups[g] = PrefixGroup{first + xn - n, n, s_lead[g], 0, pages, item + xi - items, unit + xu - units};
         first += __shfl_sync(0xffffffffu, xn, 31);
         item += __shfl_sync(0xffffffffu, xi, 31);
         unit += __shfl_sync(0xffffffffu, xu, 31);
@@ -139,6 +145,7 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const PrefixA
 // of many pieces each.
 constexpr int kJoinThreads = 256;
 constexpr int kMaxJoin = 256 + 2 * kMaxRanges;
+constexpr int kAhead = 6;  // rows a warp has in flight before it knows their weights
 
 // A lane's share of the OR of n words (16-byte aligned, room for a multiple of four).
 __device__ __forceinline__ int any_word(const int *words, int n, int lane) {
@@ -164,11 +171,11 @@ __global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(const PrefixA
   const int w0 = kWarps == 1 ? 0 : warp;  // this warp's place among the row's
   float *sw = s_w[kWarps == 1 ? warp : 0];
   // all that hangs on the request alone, at once
-  const int g = a.group_of[b], own = a.own_len[b], skip = a.skip[b], rank = a.rank[b];
+  const int own = a.own_len[b];
   const int count = a.d.split_count[b], first_piece = a.d.split_first[b];
   const uint32_t pre = a.pre_st[b];
   uint32_t st = pre | a.check_st[b];
-  const PrefixHdr hdr = *a.hdr;
+  const PrefixRow pr = a.ctas > 0 ? a.rows[id] : PrefixRow{0, 0, 0, 0};
   // whether a CTA of either kernel gave up: four words a load, all of them on their way beside the rest
   int any = 0;
   if (hq == 0 && w0 == 0) {
@@ -185,23 +192,22 @@ __global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(const PrefixA
       st |= PFKV_ST_TIMEOUT;
     }
   }
-  // prefix: a piece per range; of an item of at most kRows / 2 rows, one per range and half (kRows / 2 rows on)
-  int n_pre = 0, row = 0, sh = 0;
-  long long slot0 = 0;
-  if (!pre && g >= 0 && skip > 0) {
-    const PrefixGroup gr = a.groups[g];
-    const HeadLine line = head_line(gr.n, a.G, gr.pages, a.c0);
-    const int h = hq / a.G, r = rank * a.G + hq % a.G, blk = r / kRows;
-    const int item = h * line.blocks + blk, cost = page_cost(line, blk);
-    const long long first = gr.unit0 + h * line.head + blk * line.full + a.c0;  // unit of its first page
-    const int k0 = range_of(hdr, first);
-    sh = cost == kCostHalf;
-    n_pre = (range_of(hdr, first + (long long)cost * (gr.pages - 1)) - k0 + 1) << sh;
-    slot0 = (long long)k0 + gr.item0 + item;
-    row = r - blk * kRows;
+  auto pre_row = [&](int i) {
+    return (size_t)(pr.slot0 + (i >> pr.sh)) * kRows + pr.row + (pr.sh ? (i & 1) * (kRows / 2) : 0);
+  };
+  const int n = n_own + pr.n;
+  // this warp's first rows, on their way beside the pieces' maxima
+  const int col = lane % kCols, i0 = w0 * kPar + lane / kCols;
+  auto row_of = [&](int i) {
+    const float *src = i < n_own ? a.d.part_o + ((size_t)(c0 + i) * a.d.Hq + hq) * kD : a.o + pre_row(i - n_own) * kD;
+    return __ldcg(reinterpret_cast<const float4 *>(src) + col);
+  };
+  float4 ahead[kAhead];
+#pragma unroll
+  for (int k = 0; k < kAhead; ++k) {
+    const int i = i0 + k * kWarps * kPar;
+    ahead[k] = i < n ? row_of(i) : make_float4(0.f, 0.f, 0.f, 0.f);
   }
-  auto pre_row = [&](int i) { return (size_t)(slot0 + (i >> sh)) * kRows + row + (sh ? (i & 1) * (kRows / 2) : 0); };
-  const int n = n_own + n_pre;
   for (int i = lane; i < n_own * a.d.st_groups; i += 32) st |= a.d.part_st[(size_t)c0 * a.d.st_groups + i];
   // the pieces' maxima, then their weights
   float mx = kNegInf;
@@ -225,16 +231,16 @@ __global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(const PrefixA
     if (__any_sync(0xffffffffu, any != 0)) st |= PFKV_ST_TIMEOUT;
     if (lane == 0) a.d.status[b] = st;
   }
-  const int col = lane % kCols;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   if (!st) {
-#pragma unroll 8
-    for (int i = w0 * kPar + lane / kCols; i < n; i += kWarps * kPar) {
-      const float *src = i < n_own ? a.d.part_o + ((size_t)(c0 + i) * a.d.Hq + hq) * kD : a.o + pre_row(i - n_own) * kD;
-      const float4 v = __ldcg(reinterpret_cast<const float4 *>(src) + col);
-      const float w = sw[i];
+    auto add = [&](float w, float4 v) {
       acc.x += w * v.x; acc.y += w * v.y; acc.z += w * v.z; acc.w += w * v.w;
-    }
+    };
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k)
+      if (i0 + k * kWarps * kPar < n) add(sw[i0 + k * kWarps * kPar], ahead[k]);
+#pragma unroll 8
+    for (int i = i0 + kAhead * kWarps * kPar; i < n; i += kWarps * kPar) add(sw[i], row_of(i));
   }
   if (kPar == 2) {
     acc.x += __shfl_xor_sync(0xffffffffu, acc.x, 16);
@@ -267,7 +273,7 @@ __global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(const PrefixA
 size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 
 struct PrefixLayout {
-  size_t own_len, skip, pre_st, check_st, rank, members, groups, hdr, ml, o, aborts, total;
+  size_t own_len, skip, pre_st, check_st, rank, members, groups, rows, hdr, ml, o, aborts, total;
 };
 
 // Slots: pieces of the work line, at most one per range and one per item more.
@@ -275,7 +281,7 @@ PrefixLayout prefix_layout(size_t first, int batch, int q_heads, int kv_heads, i
   const size_t B = (size_t)batch, G = (size_t)(q_heads / kv_heads);
   const size_t full = (size_t)n_groups < B ? (size_t)n_groups : B;  // groups that can have members
   const size_t items = (size_t)kv_heads * (B * G / kRows + full);
-  const size_t rows = n_groups ? (items + kMaxRanges) * kRows : 0;
+  const size_t slots = n_groups ? (items + kMaxRanges) * kRows : 0;
   PrefixLayout w;
   w.own_len = first;
   w.skip = w.own_len + up256(4 * B);
@@ -284,11 +290,12 @@ PrefixLayout prefix_layout(size_t first, int batch, int q_heads, int kv_heads, i
   w.rank = w.check_st + up256(4 * B);
   w.members = w.rank + up256(4 * B);
   w.groups = w.members + up256(4 * B);
-  w.hdr = w.groups + up256(sizeof(PrefixGroup) * (size_t)n_groups);
+  w.rows = w.groups + up256(sizeof(PrefixGroup) * (size_t)n_groups);
+  w.hdr = w.rows + (n_groups ? up256(sizeof(PrefixRow) * B * (size_t)q_heads) : 0);
   w.aborts = w.hdr + up256(sizeof(PrefixHdr));
   w.ml = w.aborts + up256(4 * (size_t)kMaxRanges);
-  w.o = w.ml + up256(sizeof(float2) * rows);
-  w.total = w.o + up256(sizeof(float) * rows * dim);
+  w.o = w.ml + up256(sizeof(float2) * slots);
+  w.total = w.o + up256(sizeof(float) * slots * dim);
   return w;
 }
 
@@ -309,7 +316,7 @@ int run_prefix(PrefixArgs a, cudaStream_t s) {
   a.c0 = kCostHalf * ((512 + a.d.S - 1) / a.d.S);
   a.min_units = kCostHalf * ((256 + a.d.S - 1) / a.d.S);
   int rc = cuda_ok(launch_dependent(prefix_plan_kernel, dim3((unsigned)a.d.B + 1u), kPlanThreads,
-                                    4 * (size_t)a.n_groups, s, a),
+                                    8 * (size_t)a.n_groups, s, a),
                    "prefix plan launch");
   if (rc) return rc;
   if (a.ctas > 0) {
@@ -359,6 +366,7 @@ int launch_prefix_decode(const DecodeArgs &d, size_t ws_first, uint8_t *ws, cons
   a.rank = reinterpret_cast<int *>(ws + L.rank);
   a.members = reinterpret_cast<int *>(ws + L.members);
   a.groups = reinterpret_cast<PrefixGroup *>(ws + L.groups);
+  a.rows = reinterpret_cast<PrefixRow *>(ws + L.rows);
   a.hdr = reinterpret_cast<PrefixHdr *>(ws + L.hdr);
   a.aborts = reinterpret_cast<int *>(ws + L.aborts);
   a.ml = reinterpret_cast<float2 *>(ws + L.ml);

@@ -28,7 +28,8 @@
 //                   rows lie (bounds-checked page ids), so that nobody else
 //                   waits for a table entry; FP8: bulk-copies the codes into
 //                   a staging ring of three tiles (48 KB in flight).
-//   warp 15         compares the requests' prefix pages, all CTAs together.
+//   warp 15         works out where the join finds each row's pieces and
+//                   compares the requests' prefix pages, all CTAs together.
 // An item of more than 128 rows has 128 in each half, over the same tokens.
 // One of at most 128 rows gives both halves the same rows, half 0 the first 64
 // tokens of each tile and half 1 the others; each half then leaves a partial
@@ -62,12 +63,11 @@ static_assert(kRegsSoftmax >= 128 && kRegsLoader <= 128 && kRegsRest <= 128 &&
 
 // One piece of work, announced by the planner; n_rows 0 ends the work.
 struct PItem {
-  int first, row0, n_rows, h, p0, p1;
+  int first, lead, row0, n_rows, h, p0, p1;
   long long slot;
   int split;  // at most 128 rows: each half takes 64 tokens of a tile
-  int pad;
 };
-static_assert(sizeof(PItem) == 40, "item slot");
+static_assert(sizeof(PItem) % 8 == 0, "tile slots follow");
 
 // One tile, announced by the planner: the pool row of each 16 tokens' first
 // one (they lie in one page), or -1 for tokens past the end or a page id
@@ -113,19 +113,18 @@ struct PCfg {
 
 struct PWalk {
   long long u, u1;
-  int k;
+  int k, group;  // range; a group at or before the one that holds u, by 32
 };
 
-// The next piece with pages; whole warp or one thread.
+// The next piece with pages; whole warp, the same in every lane.
 __device__ __forceinline__ bool walk_next(const PrefixArgs &a, PWalk &w, PItem &it) {
   while (w.u < w.u1) {
-    int lo = 0, hi = a.n_groups - 1;  // the last group that starts at or before u
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (a.groups[mid].unit0 <= w.u) lo = mid;
-      else hi = mid - 1;
+    // the last group that starts at or before u, 32 at a time
+    for (; w.group + 32 < a.n_groups && a.groups[w.group + 32].unit0 <= w.u; w.group += 32) {
     }
-    const PrefixGroup g = a.groups[lo];
+    const int lane = threadIdx.x & 31, gl = w.group + lane;
+    const unsigned before = __ballot_sync(0xffffffffu, gl < a.n_groups && a.groups[gl].unit0 <= w.u);
+    const PrefixGroup g = a.groups[w.group + __popc(before) - 1];
     const HeadLine line = head_line(g.n, a.G, g.pages, a.c0);
     const long long rel = w.u - g.unit0;
     it.h = (int)div_floor(rel, line.head);
@@ -139,6 +138,7 @@ __device__ __forceinline__ bool walk_next(const PrefixArgs &a, PWalk &w, PItem &
     w.u += end - off;
     if (it.p1 <= it.p0) continue;
     it.first = g.first;
+    it.lead = g.lead;
     it.row0 = blk * kRows;
     it.n_rows = blk < line.blocks - 1 ? kRows : line.last_rows;
     it.slot = (long long)w.k + g.item0 + it.h * line.blocks + blk;
@@ -232,7 +232,7 @@ __device__ __forceinline__ void plan_tiles(const PrefixArgs &a, uint8_t *smem, c
   const bool per_token = kFp8 && a.d.scale_mode == PFKV_SCALE_PER_TOKEN;
   const uint64_t policy = l2_evict_first_policy();
   constexpr int kGroups = kTok / 16, kAtOnce = 32 / kGroups;  // 16-token groups of a tile; tiles per look-up
-  PWalk w{range_start(hdr, blockIdx.x), range_start(hdr, blockIdx.x + 1), (int)blockIdx.x};
+  PWalk w{range_start(hdr, blockIdx.x), range_start(hdr, blockIdx.x + 1), (int)blockIdx.x, 0};
   uint32_t n = 0;
   bool ok = true;
   for (uint32_t i = 0; ok; ++i) {
@@ -244,7 +244,7 @@ __device__ __forceinline__ void plan_tiles(const PrefixArgs &a, uint8_t *smem, c
       mbar_arrive(&B.item_full[i % kItemSlots]);
     }
     const int n_tok = have ? (it.p1 - it.p0) * S : 1;
-    const int *trow = have ? a.d.block_table + (size_t)a.members[it.first] * a.d.MP + it.p0 : nullptr;
+    const int *trow = have ? a.d.block_table + (size_t)it.lead * a.d.MP + it.p0 : nullptr;
     auto look_up = [&](int t0) -> int {
       const int tok = t0 + 16 * lane;
       return have && tok < n_tok ? __ldg(trow + tok / S) : -1;
@@ -300,7 +300,7 @@ __device__ __forceinline__ void check_prefixes(const PrefixArgs &a) {
   for (long long id = blockIdx.x; id < a.d.B * chunks; id += gridDim.x) {
     const int b = (int)(id / chunks), lo = (int)(id - b * chunks) * kChunk;
     if (a.pre_st[b] || lo >= a.skip[b]) continue;  // refused already, or no prefix there
-    const int hi = min(lo + kChunk, a.skip[b]), lead = a.members[a.groups[a.group_of[b]].first];
+    const int hi = min(lo + kChunk, a.skip[b]), lead = a.groups[a.group_of[b]].lead;
     const int *row = a.d.block_table + (size_t)b * a.d.MP, *first = a.d.block_table + (size_t)lead * a.d.MP;
     const uint32_t *want = a.d.block_tags + (size_t)b * a.d.MP;  // read under the tag check only
     uint32_t bits = 0u;
@@ -312,6 +312,28 @@ __device__ __forceinline__ void check_prefixes(const PrefixArgs &a) {
       if (p != first[i]) bits |= PFKV_ST_PREFIX_DIFFERS;
     }
     if (bits) atomicOr(&a.check_st[b], bits);
+  }
+}
+
+// Every row's pieces, for the join; rows spread over all CTAs.
+__device__ __forceinline__ void find_pieces(const PrefixArgs &a, const PrefixHdr &hdr) {
+  const unsigned all = (unsigned)a.d.B * (unsigned)a.d.Hq;
+  for (unsigned id = blockIdx.x * 32 + (threadIdx.x & 31); id < all; id += gridDim.x * 32) {
+    const int b = (int)(id / (unsigned)a.d.Hq), hq = (int)(id - (unsigned)b * (unsigned)a.d.Hq);
+    PrefixRow pr{0, 0, 0, 0};
+    if (!a.pre_st[b] && a.group_of[b] >= 0 && a.skip[b] > 0) {
+      const PrefixGroup gr = a.groups[a.group_of[b]];
+      const HeadLine line = head_line(gr.n, a.G, gr.pages, a.c0);
+      const int h = hq / a.G, r = a.rank[b] * a.G + hq % a.G, blk = r / kRows;
+      const int item = h * line.blocks + blk, cost = page_cost(line, blk);
+      const long long first = gr.unit0 + h * line.head + blk * line.full + a.c0;  // unit of its first page
+      const int k0 = range_of(hdr, first);
+      pr.sh = cost == kCostHalf;
+      pr.n = (range_of(hdr, first + (long long)cost * (gr.pages - 1)) - k0 + 1) << pr.sh;
+      pr.slot0 = k0 + gr.item0 + item;
+      pr.row = r - blk * kRows;
+    }
+    a.rows[id] = pr;
   }
 }
 
@@ -863,7 +885,10 @@ __global__ void __launch_bounds__(kPThreads, 1) prefix_kernel(const PrefixArgs a
       }
     }
   }
-  if (warp == 15) check_prefixes(a);
+  if (warp == 15) {
+    find_pieces(a, hdr);
+    check_prefixes(a);
+  }
   __syncwarp();
   tc_fence_before();
   __syncthreads();
