@@ -168,7 +168,7 @@ static int decode_common(int want_dtype, const pfkv_cache *c, const void *q, int
   a.n_ctas = 0;
   a.st_groups = 1;
   a.skip = nullptr;
-  a.join = 0;
+  a.beside = 0;
   a.piece_cost = 0;
   a.part_st = reinterpret_cast<uint32_t *>(w + L.part_st);
   a.cta_abort = reinterpret_cast<int *>(w + L.cta_abort);

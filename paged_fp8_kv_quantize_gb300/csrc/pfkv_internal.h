@@ -21,8 +21,6 @@ constexpr int kMaxCtas = 4096;  // decode split grid: at most this many CTAs (on
 WsLayout ws_layout(int batch, int q_heads, int v_dim, int max_splits, bool latent);
 constexpr size_t kLatentQTermBytes = 128 * 576;  // 128 operand rows (two terms x 64 heads) x 576 codes
 
-enum { kJoin = 1, kJoinBeside = 2 };  // DecodeArgs::join
-
 struct DecodeArgs {
   // cache
   int P, S, Hkv, D, Dv, scale_mode, dtype, kv_shared;
@@ -72,14 +70,14 @@ struct DecodeArgs {
   // latent-stream path: the query terms and per-head factors (see ws_layout)
   uint8_t *qterms;
   float *qfac;
-  // Shared-prefix decode: request b's pages begin at table entry skip[b], and
-  // seq_lens counts the tokens from there on (NULL: 0).  join != 0: every piece
-  // leaves a partial result (a one-piece request is not finished in the split
-  // kernel), and the caller's own kernel merges; kJoinBeside: the stream's
-  // kernel before the split kernel is one whose start means that all the split
-  // kernel reads is there, and whose end only the caller's merge waits for.
+  // Shared-prefix decode, the split kernel alone (launch_gqa_split): request
+  // b's pages begin at table entry skip[b], and seq_lens counts the tokens from
+  // there on.  Every piece leaves a partial result, and the caller's own kernel
+  // merges.  beside: the stream's kernel before the split kernel is one whose
+  // start means that all the split kernel reads is there, and whose end only
+  // the merge waits for.
   const int *skip;
-  int join;
+  int beside;
   int piece_cost;  // cut rule: pages' worth of time one piece costs beyond its pages
   uint32_t *part_st;
   int *cta_abort;
@@ -95,7 +93,7 @@ int num_sms();
 
 // launchers (return PFKV_* codes)
 int launch_gqa_decode(const DecodeArgs &a, cudaStream_t s);
-// The split kernel alone (join must be set); fills in the launch's n_ctas and st_groups.
+// The split kernel alone (see DecodeArgs::skip); fills in the launch's n_ctas and st_groups.
 int launch_gqa_split(DecodeArgs &a, cudaStream_t s);
 size_t prefix_ws_bytes(size_t first, int batch, int q_heads, int kv_heads, int dim, int n_groups);
 int launch_prefix_decode(const DecodeArgs &d, size_t ws_first, uint8_t *ws, const int *group_of,

@@ -14,7 +14,7 @@
 //              the check that every member's first pages are the same pages
 //              (and, under the tag check, are still its own).
 //   3. split   each request's own pages: the grouped-query decode's split
-//              kernel (decode_gqa.cu) on lengths and tables past the prefix.
+//              kernel (decode_gqa.cuh) on lengths and tables past the prefix.
 //   4. join    partial results of 2 and 3 to out; status.
 #include <atomic>
 
@@ -325,7 +325,7 @@ int run_prefix(PrefixArgs a, cudaStream_t s) {
     if (rc) return rc;
   }
   DecodeArgs own = a.d;
-  own.join = a.ctas > 0 ? kJoinBeside : kJoin;
+  own.beside = a.ctas > 0;
   own.seq_lens = a.own_len;
   rc = launch_gqa_split(own, s);
   if (rc) return rc;

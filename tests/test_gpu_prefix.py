@@ -174,8 +174,7 @@ def test_step_appends_then_attends(cache, page):
 
 
 def test_slots_past_the_length_do_not_matter():
-    """Unwritten slots of a request's last page hold anything, NaN among it;
-    the plain decode reads the same pages."""
+    """Unwritten slots of a request's last page hold anything, NaN among it."""
     for cache in (FP8, FP8_TOKEN, BF16):
         c = PrefixCase(15, [0, 0, -1, 0], [2], [1, 9, 21, 15], q_heads=8, kv_heads=2, dim=64, page=16, cache=cache)
         ref = c.call()[0].clone()
@@ -191,8 +190,6 @@ def test_slots_past_the_length_do_not_matter():
                 for x in (c.gpu.k_scale, c.gpu.v_scale):
                     x.view(c.P, 2, 16)[p, :, s:] = float("inf")
         assert torch.equal(c.call()[0], ref), cache
-        plain, _ = abi.paged_decode_attention(c.gpu, dev_bf16(c.q), dev_i32(c.lens), dev_i32(c.table), None, c.tau)
-        assert torch.isfinite(plain).all(), cache
 
 
 def test_captured_and_replayed_with_other_lengths():
