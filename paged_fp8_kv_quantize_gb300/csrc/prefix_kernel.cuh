@@ -55,8 +55,8 @@ constexpr int kScaleSlots = 4;   // tiles whose per-token scales are kept
 constexpr int kItemSlots = 4;    // items announced ahead
 constexpr int kTileSlots = 8;    // tiles announced ahead
 // Registers a thread after the launch's 128: two softmax warpgroups, the
-// operand warps, and the rest; 2 x 176 + 88 + 72 = 4 x 128.
-constexpr int kRegsSoftmax = 176, kRegsLoader = 88, kRegsRest = 72;
+// operand warps, and the rest; 2 x 168 + 80 + 96 = 4 x 128.
+constexpr int kRegsSoftmax = 168, kRegsLoader = 80, kRegsRest = 96;
 static_assert(kRegsSoftmax >= 128 && kRegsLoader <= 128 && kRegsRest <= 128 &&
                   2 * kRegsSoftmax + kRegsLoader + kRegsRest <= 4 * 128,
               "an increase goes up and a decrease down, and all of them fit what the block was launched with");
@@ -699,7 +699,6 @@ __device__ __forceinline__ void softmax_rows(const PrefixArgs &a, uint8_t *smem,
       tc_fence_after();
       uint32_t z[64];
       tmem_ld64(col, z);
-      float mx = kNegInf;
       if (per_token) {
 #pragma unroll
         for (int j = 0; j < 64; j += 4) {
@@ -715,9 +714,11 @@ __device__ __forceinline__ void softmax_rows(const PrefixArgs &a, uint8_t *smem,
         for (int j = 0; j < 64; ++j)
           if (j >= valid) z[j] = 0xff800000u;
       }
+      float part[2] = {kNegInf, kNegInf};
 #pragma unroll
-      for (int j = 0; j < 64; j += 2)  // three at a time
-        mx = fmaxf(fmaxf(mx, __uint_as_float(z[j])), __uint_as_float(z[j + 1]));
+      for (int j = 0; j < 64; j += 2)  // three operands at a time
+        part[j >> 1 & 1] = fmaxf(fmaxf(part[j >> 1 & 1], __uint_as_float(z[j])), __uint_as_float(z[j + 1]));
+      float mx = fmaxf(part[0], part[1]);
       mx = mx == kNegInf ? kNegInf : mx * mult;
       // move the reference
       const bool grow = mx > m + C::kGrow || first;
