@@ -43,6 +43,20 @@ struct PrefixRow {
   int slot0, n, row, sh;
 };
 
+// One piece of work; n_rows 0 ends the work.
+struct PItem {
+  int first, lead, row0, n_rows, h, p0, p1;
+  long long slot;
+  int split;  // at most 128 rows: each half takes 64 tokens of a tile
+};
+static_assert(sizeof(PItem) % 8 == 0, "tile slots follow it in shared memory");
+
+// A range's first piece, and where the walk goes on from there.
+struct PRange {
+  PItem item;
+  long long u, u1;
+};
+
 struct PrefixArgs {
   DecodeArgs d;  // the decode call: cache, q, lengths, tables, workspace of the own pages' pieces, out, status
   int G;         // query heads per KV head
@@ -60,6 +74,7 @@ struct PrefixArgs {
   PrefixGroup *groups;  // [n_groups]
   PrefixRow *rows;      // [B][Hq], written beside the products
   PrefixHdr *hdr;
+  PRange *ranges;  // [kMaxRanges]
   float2 *ml;   // [slot][kRows]
   float *o;     // [slot][kRows][D]
   int *aborts;  // [kMaxRanges]
@@ -90,6 +105,51 @@ __device__ __forceinline__ HeadLine head_line(int n, int G, int pages, int c0) {
 }
 __device__ __forceinline__ int page_cost(const HeadLine &l, int blk) {
   return blk == l.blocks - 1 && l.last_rows <= kRows / 2 ? kCostHalf : kCostFull;
+}
+// Pages of that cost that begin before unit x of an item's pages.
+__device__ __forceinline__ int pages_before(long long x, int cost) {
+  if (x <= 0) return 0;
+  const unsigned long long y = (unsigned long long)x + (unsigned)(cost - 1);
+  return (int)(cost == kCostHalf ? y / kCostHalf : y / kCostFull);
+}
+
+// The pieces of range k from unit u on.
+struct PWalk {
+  long long u, u1;
+  int k;
+};
+
+// The next piece with pages.
+__device__ __forceinline__ bool walk_next(const PrefixArgs &a, const PrefixGroup *groups, PWalk &w, PItem &it) {
+  while (w.u < w.u1) {
+    int lo = 0, hi = a.n_groups - 1;  // the last group that starts at or before u
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (groups[mid].unit0 <= w.u) lo = mid;
+      else hi = mid - 1;
+    }
+    const PrefixGroup g = groups[lo];
+    const HeadLine line = head_line(g.n, a.G, g.pages, a.c0);
+    const long long rel = w.u - g.unit0;
+    it.h = (int)div_floor(rel, line.head);
+    const long long in_head = rel - it.h * line.head;
+    const int blk = line.blocks == 1 ? 0 : (int)min((long long)(line.blocks - 1), div_floor(in_head, line.full));
+    const long long off = in_head - blk * line.full, seg = blk < line.blocks - 1 ? line.full : line.last;
+    const long long end = min(seg, off + (w.u1 - w.u));
+    const int cost = page_cost(line, blk);
+    it.p0 = pages_before(off - a.c0, cost);
+    it.p1 = pages_before(end - a.c0, cost);
+    w.u += end - off;
+    if (it.p1 <= it.p0) continue;
+    it.first = g.first;
+    it.lead = g.lead;
+    it.row0 = blk * kRows;
+    it.n_rows = blk < line.blocks - 1 ? kRows : line.last_rows;
+    it.slot = (long long)w.k + g.item0 + it.h * line.blocks + blk;
+    it.split = cost == kCostHalf;
+    return true;
+  }
+  return false;
 }
 
 }  // namespace

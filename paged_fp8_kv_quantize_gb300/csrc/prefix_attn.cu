@@ -27,6 +27,7 @@ namespace {
 // ---------------------------------------------------------------- plan
 
 constexpr int kPlanThreads = 256;
+constexpr int kPlanGroups = 64;  // groups whose segments block B keeps in shared memory
 
 // Sum over the block (kPlanThreads threads); every thread gets it.
 __device__ __forceinline__ int block_sum(int v, int *s_sum) {
@@ -45,6 +46,8 @@ __device__ __forceinline__ int block_sum(int v, int *s_sum) {
 __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const PrefixArgs a) {
   extern __shared__ int s_count[];  // block B: requests of each group, then the first of each
   __shared__ int s_sum[kPlanThreads / 32];
+  __shared__ PrefixGroup s_groups[kPlanGroups];
+  __shared__ PrefixHdr s_hdr;
   pdl_wait();
   pdl_launch_dependents();
   const int t = threadIdx.x, B = a.d.B, MP = a.d.MP, S = a.d.S;
@@ -85,16 +88,30 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const PrefixA
             xu += yu;
           }
         }
-        if (g < a.n_groups) a.groups[g] = PrefixGroup{first + xn - n, n, s_lead[g], 0, pages, item + xi - items, unit + xu - units};
+        const PrefixGroup pg{first + xn - n, n, g < a.n_groups ? s_lead[g] : 0, 0, pages, item + xi - items, unit + xu - units};
+        if (g < kPlanGroups) s_groups[g] = pg;
+        if (g < a.n_groups) a.groups[g] = pg;
         first += __shfl_sync(0xffffffffu, xn, 31);
         item += __shfl_sync(0xffffffffu, xi, 31);
         unit += __shfl_sync(0xffffffffu, xu, 31);
       }
       if (t == 0) {
         const long long r = unit / a.min_units;
-        a.hdr->T = unit;
-        a.hdr->R = unit == 0 ? 0 : r < 1 ? 1 : (int)(r < a.ctas ? r : a.ctas);
+        s_hdr = PrefixHdr{unit, unit == 0 ? 0 : r < 1 ? 1 : (int)(r < a.ctas ? r : a.ctas), 0};
+        *a.hdr = s_hdr;
       }
+    }
+    __syncthreads();
+    // the ranges' first pieces, a thread each
+    const PrefixHdr hdr = s_hdr;
+    for (int k = t; k < hdr.R; k += kPlanThreads) {
+      PRange r;
+      PWalk w{range_start(hdr, k), range_start(hdr, k + 1), k};
+      r.item = PItem{};
+      walk_next(a, a.n_groups <= kPlanGroups ? s_groups : a.groups, w, r.item);
+      r.u = w.u;
+      r.u1 = w.u1;
+      a.ranges[k] = r;
     }
     return;
   }
@@ -273,7 +290,7 @@ __global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(const PrefixA
 size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 
 struct PrefixLayout {
-  size_t own_len, skip, pre_st, check_st, rank, members, groups, rows, hdr, ml, o, aborts, total;
+  size_t own_len, skip, pre_st, check_st, rank, members, groups, rows, hdr, ranges, ml, o, aborts, total;
 };
 
 // Slots: pieces of the work line, at most one per range and one per item more.
@@ -292,7 +309,8 @@ PrefixLayout prefix_layout(size_t first, int batch, int q_heads, int kv_heads, i
   w.groups = w.members + up256(4 * B);
   w.rows = w.groups + up256(sizeof(PrefixGroup) * (size_t)n_groups);
   w.hdr = w.rows + (n_groups ? up256(sizeof(PrefixRow) * B * (size_t)q_heads) : 0);
-  w.aborts = w.hdr + up256(sizeof(PrefixHdr));
+  w.ranges = w.hdr + up256(sizeof(PrefixHdr));
+  w.aborts = w.ranges + up256(sizeof(PRange) * kMaxRanges);
   w.ml = w.aborts + up256(4 * (size_t)kMaxRanges);
   w.o = w.ml + up256(sizeof(float2) * slots);
   w.total = w.o + up256(sizeof(float) * slots * dim);
@@ -368,6 +386,7 @@ int launch_prefix_decode(const DecodeArgs &d, size_t ws_first, uint8_t *ws, cons
   a.groups = reinterpret_cast<PrefixGroup *>(ws + L.groups);
   a.rows = reinterpret_cast<PrefixRow *>(ws + L.rows);
   a.hdr = reinterpret_cast<PrefixHdr *>(ws + L.hdr);
+  a.ranges = reinterpret_cast<PRange *>(ws + L.ranges);
   a.aborts = reinterpret_cast<int *>(ws + L.aborts);
   a.ml = reinterpret_cast<float2 *>(ws + L.ml);
   a.o = reinterpret_cast<float *>(ws + L.o);

@@ -61,14 +61,6 @@ static_assert(kRegsSoftmax >= 128 && kRegsLoader <= 128 && kRegsRest <= 128 &&
                   2 * kRegsSoftmax + kRegsLoader + kRegsRest <= 4 * 128,
               "an increase goes up and a decrease down, and all of them fit what the block was launched with");
 
-// One piece of work, announced by the planner; n_rows 0 ends the work.
-struct PItem {
-  int first, lead, row0, n_rows, h, p0, p1;
-  long long slot;
-  int split;  // at most 128 rows: each half takes 64 tokens of a tile
-};
-static_assert(sizeof(PItem) % 8 == 0, "tile slots follow");
-
 // One tile, announced by the planner: the pool row of each 16 tokens' first
 // one (they lie in one page), or -1 for tokens past the end or a page id
 // outside the pool.
@@ -110,43 +102,6 @@ struct PCfg {
   static constexpr uint32_t kIdPV = umma_idesc_f16(128, kD, !kFp8, 0, 1);
   static_assert(kTotal <= 232448, "shared memory plan exceeds one SM");
 };
-
-struct PWalk {
-  long long u, u1;
-  int k, group;  // range; a group at or before the one that holds u, by 32
-};
-
-// The next piece with pages; whole warp, the same in every lane.
-__device__ __forceinline__ bool walk_next(const PrefixArgs &a, PWalk &w, PItem &it) {
-  while (w.u < w.u1) {
-    // the last group that starts at or before u, 32 at a time
-    for (; w.group + 32 < a.n_groups && a.groups[w.group + 32].unit0 <= w.u; w.group += 32) {
-    }
-    const int lane = threadIdx.x & 31, gl = w.group + lane;
-    const unsigned before = __ballot_sync(0xffffffffu, gl < a.n_groups && a.groups[gl].unit0 <= w.u);
-    const PrefixGroup g = a.groups[w.group + __popc(before) - 1];
-    const HeadLine line = head_line(g.n, a.G, g.pages, a.c0);
-    const long long rel = w.u - g.unit0;
-    it.h = (int)div_floor(rel, line.head);
-    const long long in_head = rel - it.h * line.head;
-    const int blk = (int)min((long long)(line.blocks - 1), div_floor(in_head, line.full));
-    const long long off = in_head - blk * line.full, seg = blk < line.blocks - 1 ? line.full : line.last;
-    const long long end = min(seg, off + (w.u1 - w.u));
-    const int cost = page_cost(line, blk);
-    it.p0 = (int)div_floor(max(0LL, off - a.c0) + cost - 1, cost);
-    it.p1 = (int)div_floor(max(0LL, end - a.c0) + cost - 1, cost);
-    w.u += end - off;
-    if (it.p1 <= it.p0) continue;
-    it.first = g.first;
-    it.lead = g.lead;
-    it.row0 = blk * kRows;
-    it.n_rows = blk < line.blocks - 1 ? kRows : line.last_rows;
-    it.slot = (long long)w.k + g.item0 + it.h * line.blocks + blk;
-    it.split = cost == kCostHalf;
-    return true;
-  }
-  return false;
-}
 
 constexpr int kMaxSlots = 4;
 struct PBars {
@@ -232,12 +187,21 @@ __device__ __forceinline__ void plan_tiles(const PrefixArgs &a, uint8_t *smem, c
   const bool per_token = kFp8 && a.d.scale_mode == PFKV_SCALE_PER_TOKEN;
   const uint64_t policy = l2_evict_first_policy();
   constexpr int kGroups = kTok / 16, kAtOnce = 32 / kGroups;  // 16-token groups of a tile; tiles per look-up
-  PWalk w{range_start(hdr, blockIdx.x), range_start(hdr, blockIdx.x + 1), (int)blockIdx.x, 0};
+  // the range's first piece comes from the plan: working it out here, in code that runs once and so out of a cold
+  // instruction cache, took 3.4 us
+  PItem first;
+  PWalk w;
+  {
+    const PRange r = a.ranges[blockIdx.x];
+    first = r.item;
+    w = PWalk{r.u, r.u1, (int)blockIdx.x};
+  }
   uint32_t n = 0;
   bool ok = true;
   for (uint32_t i = 0; ok; ++i) {
     PItem it{};
-    const bool have = walk_next(a, w, it);
+    if (i == 0) it = first;
+    const bool have = i == 0 ? it.n_rows != 0 : walk_next(a, a.groups, w, it);
     if (!mbar_wait_warp(&B.item_empty[i % kItemSlots], ((i / kItemSlots) & 1u) ^ 1u, abort)) break;
     if (lane == 0) {
       items[i % kItemSlots] = it;
