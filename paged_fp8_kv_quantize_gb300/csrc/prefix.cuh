@@ -88,7 +88,7 @@ __device__ __forceinline__ int range_of(const PrefixHdr &h, long long u) {
 }
 
 // A group's items of one KV head on the line.
-constexpr int kCostHalf = 4, kCostFull = 7;  // a page's cost; measured 1.2 and 2.1 us per 128 tokens (FP8, D 128)
+constexpr int kCostHalf = 4, kCostFull = 7;  // a page's cost: about 1.1 us and 1.8 us per 128 tokens (FP8, D 128)
 struct HeadLine {
   int blocks, last_rows;       // row blocks, rows of the last one
   long long full, last, head;  // units of a full block, of the last one, of all

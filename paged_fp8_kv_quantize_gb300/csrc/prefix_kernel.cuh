@@ -666,11 +666,15 @@ __device__ __forceinline__ void softmax_rows(const PrefixArgs &a, uint8_t *smem,
       if (per_token) {
 #pragma unroll
         for (int j = 0; j < 64; j += 4) {
-          const float4 k4 = *reinterpret_cast<const float4 *>(sc + j);
-          z[j] = __float_as_uint(__uint_as_float(z[j]) * k4.x);
-          z[j + 1] = __float_as_uint(__uint_as_float(z[j + 1]) * k4.y);
-          z[j + 2] = __float_as_uint(__uint_as_float(z[j + 2]) * k4.z);
-          z[j + 3] = __float_as_uint(__uint_as_float(z[j + 3]) * k4.w);
+          const ulonglong2 k4 = *reinterpret_cast<const ulonglong2 *>(sc + j);
+          const uint64_t s[2] = {k4.x, k4.y};
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            float lo, hi;
+            f32x2_split(mul_f32x2(f32x2(__uint_as_float(z[j + 2 * q]), __uint_as_float(z[j + 2 * q + 1])), s[q]), lo, hi);
+            z[j + 2 * q] = __float_as_uint(lo);
+            z[j + 2 * q + 1] = __float_as_uint(hi);
+          }
         }
       }
       if (valid < 64) {
@@ -723,7 +727,7 @@ __device__ __forceinline__ void softmax_rows(const PrefixArgs &a, uint8_t *smem,
             p1 = fast_exp2(p1);
             p = f32x2(p0, p1);
             sum = add_f32x2(sum, p);
-            if (per_token) p = mul_f32x2(p, *reinterpret_cast<const uint64_t *>(sc + kTok + j));
+            if (per_token) p = mul_f32x2(p, reinterpret_cast<const uint64_t *>(sc + kTok)[j / 2]);
           }
           f32x2_split(p, p0, p1);
           pk[j / 2] = kFp8 ? pack_f16x2(p0, p1) : pack_bf16x2(p0, p1);
