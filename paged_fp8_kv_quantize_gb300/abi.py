@@ -372,7 +372,7 @@ def paged_decode_attention_prefix(cache, q, seq_lens, block_table, block_tags, p
         _arg(q, "q", B * Hq * D, dev, bf16), Hq, _arg(seq_lens, "seq_lens", B, dev),
         _arg(block_table, "block_table", B * MP, dev), _arg(block_tags, "block_tags", B * MP, dev), B, MP,
         _arg(prefix_group, "prefix_group", B, dev), _arg(prefix_pages, "prefix_pages", n_groups, dev), n_groups,
-        softmax_scale, flags, max_splits, _arg(workspace, "workspace", workspace.numel(), dev, torch.uint8),
+        float(softmax_scale), int(flags), int(max_splits), _arg(workspace, "workspace", workspace.numel(), dev, torch.uint8),
         workspace.numel(), _arg(out, "out", B * Hq * D, dev, out.dtype), kind, _arg(status, "status", B, dev),
         _raw_stream(stream, dev))
     _check("pfkv_paged_decode_attention_prefix", rc)

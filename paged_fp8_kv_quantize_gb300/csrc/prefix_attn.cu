@@ -317,6 +317,20 @@ PrefixLayout prefix_layout(size_t first, int batch, int q_heads, int kv_heads, i
   return w;
 }
 
+// A BF16 pool in boxes of 16 tokens x 64 values, as operand tiles hold them.
+int make_tile_map(CUtensorMap *map, const void *pool, const DecodeArgs &d) {
+  EncodeTiledFn enc = encode_tiled_fn();
+  if (!enc) return cuda_fail(cudaErrorNotSupported, "cuTensorMapEncodeTiled entry point");
+  const cuuint64_t row = 2ull * d.D;
+  const cuuint64_t dims[4] = {(cuuint64_t)d.D, (cuuint64_t)d.S, (cuuint64_t)d.cache.num_kv_heads, (cuuint64_t)d.P};
+  const cuuint64_t strides[3] = {row, row * d.S, row * d.S * d.cache.num_kv_heads};
+  const cuuint32_t box[4] = {64, 16, 1, 1}, estr[4] = {1, 1, 1, 1};
+  const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(pool), dims, strides, box, estr,
+                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? PFKV_OK : cuda_fail(cudaErrorInvalidValue, "cuTensorMapEncodeTiled");
+}
+
 template <bool kFp8, int kD, int kTerms>
 int run_prefix(PrefixArgs a, cudaStream_t s) {
   using C = PCfg<kFp8, kD, kTerms>;
@@ -338,7 +352,14 @@ int run_prefix(PrefixArgs a, cudaStream_t s) {
                    "prefix plan launch");
   if (rc) return rc;
   if (a.ctas > 0) {
-    rc = cuda_ok(launch_dependent(prefix_kernel<kFp8, kD, kTerms>, dim3(a.ctas), kPThreads, C::kTotal, s, a),
+    CUtensorMap map_k{}, map_v{};
+    if (!kFp8) {
+      rc = make_tile_map(&map_k, a.d.k_pool, a.d);
+      if (!rc) rc = make_tile_map(&map_v, a.d.v_pool, a.d);
+      if (rc) return rc;
+    }
+    rc = cuda_ok(launch_dependent(prefix_kernel<kFp8, kD, kTerms>, dim3(a.ctas), kPThreads, C::kTotal, s, map_k, map_v,
+                                  a),
                  "prefix kernel launch");
     if (rc) return rc;
   }

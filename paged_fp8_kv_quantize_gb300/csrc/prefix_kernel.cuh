@@ -19,15 +19,16 @@
 // follows when it can.  One CTA per SM:
 //   warps 0-3, 4-7  softmax of row half 0 and 1: a thread owns a row, so that
 //                   maxima and sums need no exchange; P overwrites S.
-//   warps 8-11      operands, in a ring of K and V tiles of 128 tokens in the
-//                   128-byte-swizzled layout.  FP8: e4m3 -> f16 from staged
-//                   codes, once per CTA.  BF16: asynchronous copies from the
-//                   pool, two tiles ahead.
+//   warps 8-11      FP8: operands e4m3 -> f16 from staged codes, once per CTA,
+//                   into a ring of K and V tiles of 128 tokens in the 128-byte-
+//                   swizzled layout.  (BF16: the planner's tensor copies land
+//                   in that ring by themselves.)
 //   warps 12, 14    issue the MMAs of half 0 and 1.
 //   warp 13         planner: works out the CTA's items and where each tile's
 //                   rows lie (bounds-checked page ids), so that nobody else
-//                   waits for a table entry; FP8: bulk-copies the codes into
-//                   a staging ring of three tiles (48 KB in flight).
+//                   waits for a table entry, and issues the copies: FP8 codes
+//                   into a staging ring of three tiles (48 KB in flight), BF16
+//                   tiles into the operand ring (64 KB and more).
 //   warp 15         works out where the join finds each row's pieces and
 //                   compares the requests' prefix pages, all CTAs together.
 // An item of more than 128 rows has 128 in each half, over the same tokens.
@@ -177,9 +178,26 @@ __device__ __forceinline__ bool stage_codes(const PrefixArgs &a, uint8_t *smem, 
   return true;
 }
 
+// BF16: tensor copies of tile i of the operand ring, 16 tokens x 64 values
+// each, lane l % 8 the tokens and l / 8 the values.  Tokens without a row get
+// the copy's fill value: a page past the pool's last reads as zeros.
+template <typename C, int kD>
+__device__ __forceinline__ bool copy_tile(const CUtensorMap &map, uint8_t *smem, const PBars &B, uint32_t i, int page,
+                                          int slot, int h, uint64_t policy, volatile int *abort) {
+  const int lane = threadIdx.x & 31;
+  const uint32_t s = i % C::kSlots;
+  if (!mbar_wait_warp(&B.empty[s], ((i / C::kSlots) & 1u) ^ 1u, abort)) return false;
+  if (lane == 0) mbar_arrive_expect_tx(&B.full[s], C::kTBytes);
+  __syncwarp();
+  if (lane < kD / 8)
+    tma_load_4d_stream(smem + C::kOffT + s * C::kTBytes + (lane >> 3) * C::kBlk + (lane & 7) * 16 * 128, &map,
+                       &B.full[s], (lane >> 3) * 64, slot, h, page, policy);
+  return true;
+}
+
 template <bool kFp8, int kD, int kTerms>
-__device__ __forceinline__ void plan_tiles(const PrefixArgs &a, uint8_t *smem, const PBars &B, const PrefixHdr &hdr,
-                                           volatile int *abort) {
+__device__ __forceinline__ void plan_tiles(const PrefixArgs &a, const CUtensorMap &map_k, const CUtensorMap &map_v,
+                                           uint8_t *smem, const PBars &B, volatile int *abort) {
   using C = PCfg<kFp8, kD, kTerms>;
   PItem *items = reinterpret_cast<PItem *>(smem + C::kOffItems);
   PTile *tiles = reinterpret_cast<PTile *>(smem + C::kOffItems + kItemSlots * sizeof(PItem));
@@ -220,6 +238,17 @@ __device__ __forceinline__ void plan_tiles(const PrefixArgs &a, uint8_t *smem, c
       const bool fine = p >= 0 && p < a.d.P;
       const uint32_t rows = __ballot_sync(0xffffffffu, fine);
       for (int k = 0; k < kAtOnce && t0 + k * kTok < n_tok; ++k, ++n) {
+        if constexpr (!kFp8) {
+          if (!have) return;
+          const int g = kGroups * k + (lane & 7);
+          const int page = __shfl_sync(0xffffffffu, fine ? p : a.d.P, g), slot = (t0 + 16 * g) % S;
+          // test hook: the first CTA never gets its first tile, and the other warps' bounded waits give up
+          if ((a.d.flags & PFKV_FLAG_TEST_WITHHOLD) && blockIdx.x == 0 && n == 0) return;
+          ok = copy_tile<C, kD>(map_k, smem, B, 2 * n, page, slot, it.h, policy, abort);
+          ok = ok && copy_tile<C, kD>(map_v, smem, B, 2 * n + 1, page, slot, it.h, policy, abort);
+          if (!ok) break;
+          continue;
+        }
         PTile &d = tiles[n % kTileSlots];
         ok = mbar_wait_warp(&B.tile_empty[n % kTileSlots], ((n / kTileSlots) & 1u) ^ 1u, abort);
         if (!ok) break;
@@ -240,14 +269,15 @@ __device__ __forceinline__ void plan_tiles(const PrefixArgs &a, uint8_t *smem, c
     }
     if (!have) return;
   }
-  // a wait gave up: copies in flight land before the block may exit
-  if constexpr (kFp8) {
-    const uint32_t issued = 2 * n + 2;  // at most
-    for (uint32_t i = issued > C::kStage + 2 ? issued - C::kStage - 2 : 0; i < issued; ++i) {
-      const uint64_t t0 = global_timer_ns();
-      while (!mbar_try_wait(&B.code_full[i % C::kStage], (i / C::kStage) & 1u))
-        if (global_timer_ns() - t0 > kWaitLimitNs / 8) break;
-    }
+  // a wait gave up: copies in flight land before the block may exit (waits of copies that were never issued, or that
+  // a later one has overtaken, run out)
+  constexpr uint32_t kRing = kFp8 ? C::kStage : C::kSlots;
+  uint64_t *landed = kFp8 ? B.code_full : B.full;
+  const uint32_t issued = 2 * n + 2;  // at most
+  for (uint32_t i = issued > kRing + 2 ? issued - kRing - 2 : 0; i < issued; ++i) {
+    const uint64_t t0 = global_timer_ns();
+    while (!mbar_try_wait(&landed[i % kRing], (i / kRing) & 1u))
+      if (global_timer_ns() - t0 > kWaitLimitNs / 8) break;
   }
 }
 
@@ -301,7 +331,7 @@ __device__ __forceinline__ void find_pieces(const PrefixArgs &a, const PrefixHdr
   }
 }
 
-// ---------------------------------------------------------------- loaders (warps 8-11)
+// ---------------------------------------------------------------- operands of FP8 caches (warps 8-11)
 
 // Per-token scales of tile n, from beside its staged K codes: K scales as they
 // are, V scales relative to a running reference vref, which moves when a
@@ -392,63 +422,6 @@ __device__ __forceinline__ void loader_fp8(const PrefixArgs &a, uint8_t *smem, c
     }
     if (lane == 0) mbar_arrive(&B.tile_empty[n % kTileSlots]);
   }
-}
-
-// BF16: copies straight into the operand layout, two tiles in flight.
-template <bool kFp8, int kD, int kTerms>
-__device__ __forceinline__ void loader_bf16(const PrefixArgs &a, uint8_t *smem, const PBars &B, volatile int *abort) {
-  using C = PCfg<kFp8, kD, kTerms>;
-  constexpr int kLanes = kD / 8, kRowsIt = 128 / kLanes, kIt = kTok / kRowsIt;
-  const PTile *tiles = reinterpret_cast<const PTile *>(smem + C::kOffItems + kItemSlots * sizeof(PItem));
-  const int t = threadIdx.x - 8 * 32, lane = t & 31, c = t % kLanes, r_it = t / kLanes;
-  const uint32_t s_ring = smem_addr(smem + C::kOffT);
-  const bool withhold = (a.d.flags & PFKV_FLAG_TEST_WITHHOLD) && blockIdx.x == 0;
-  uint32_t n = 0;  // copies issued (K and V counted apart); copy n - 2 is handed over when copy n is issued
-  auto hand_over = [&](uint32_t i) {
-    fence_async_smem();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&B.full[i % C::kSlots]);
-  };
-  for (uint32_t m = 0;; ++m) {
-    if (!mbar_wait_warp(&B.tile_full[m % kTileSlots], (m / kTileSlots) & 1u, abort)) break;
-    const PTile &d = tiles[m % kTileSlots];
-    if (d.kind == 0) {
-      cp_async_wait<0>();
-      if (n >= 2 && !(withhold && n == 2)) {
-        hand_over(n - 2);
-        hand_over(n - 1);
-      }
-      return;
-    }
-#pragma unroll
-    for (int part = 0; part < 2; ++part, ++n) {
-      if (!mbar_wait_warp(&B.empty[n % C::kSlots], ((n / C::kSlots) & 1u) ^ 1u, abort)) {
-        cp_async_wait<0>();
-        return;
-      }
-      const uint32_t base = s_ring + (n % C::kSlots) * C::kTBytes;
-      const uint8_t *pool = static_cast<const uint8_t *>(part ? a.d.v_pool : a.d.k_pool);
-#pragma unroll
-      for (int i = 0; i < kIt; ++i) {
-        const int r = i * kRowsIt + r_it;
-        const long long row = d.row[r >> 4];
-        cp_async16(base + (c >> 3) * C::kBlk + r * 128 + (((c & 7) ^ (r & 7)) << 4),
-                   pool + (row >= 0 ? row + (r & 15) : 0) * (2 * kD) + 16 * c, row >= 0);
-      }
-      cp_async_commit();
-      if (n >= 2) {
-        cp_async_wait<2>();
-        if (withhold && n == 2) {  // test hook, as in the FP8 loader
-          cp_async_wait<0>();
-          return;
-        }
-        hand_over(n - 2);
-      }
-    }
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&B.tile_empty[m % kTileSlots]);
-  }
-  cp_async_wait<0>();
 }
 
 // ---------------------------------------------------------------- MMA issuers (warps 12 and 14)
@@ -789,7 +762,9 @@ __device__ __forceinline__ void softmax_rows(const PrefixArgs &a, uint8_t *smem,
 }
 
 template <bool kFp8, int kD, int kTerms>
-__global__ void __launch_bounds__(kPThreads, 1) prefix_kernel(const PrefixArgs a) {
+__global__ void __launch_bounds__(kPThreads, 1)
+    prefix_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
+                  const PrefixArgs a) {
   using C = PCfg<kFp8, kD, kTerms>;
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint32_t s_tmem;
@@ -799,7 +774,7 @@ __global__ void __launch_bounds__(kPThreads, 1) prefix_kernel(const PrefixArgs a
   const int warp = threadIdx.x >> 5;
   if (threadIdx.x == 0) {
     for (int i = 0; i < kMaxSlots; ++i) {
-      mbar_init(&B.full[i], 4);
+      mbar_init(&B.full[i], kFp8 ? 4 : 1);
       mbar_init(&B.empty[i], 2);  // both halves
       mbar_init(&B.code_full[i], 1);
       mbar_init(&B.code_empty[i], 4);
@@ -842,7 +817,6 @@ __global__ void __launch_bounds__(kPThreads, 1) prefix_kernel(const PrefixArgs a
     } else if (warp < 12) {
       regs_dec<kRegsLoader>();
       if constexpr (kFp8) loader_fp8<kFp8, kD, kTerms>(a, smem, B, abort);
-      else loader_bf16<kFp8, kD, kTerms>(a, smem, B, abort);
     } else {
       regs_dec<kRegsRest>();
       if (warp == 12) {
@@ -850,7 +824,7 @@ __global__ void __launch_bounds__(kPThreads, 1) prefix_kernel(const PrefixArgs a
       } else if (warp == 14) {
         issue_half<kFp8, kD, kTerms>(a, smem, B, tmem, 1, abort);
       } else if (warp == 13) {
-        plan_tiles<kFp8, kD, kTerms>(a, smem, B, hdr, abort);
+        plan_tiles<kFp8, kD, kTerms>(a, map_k, map_v, smem, B, abort);
       }
     }
   }

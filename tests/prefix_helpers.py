@@ -92,7 +92,7 @@ class PrefixCase:
 
     def tolerance(self, out, mag, out_dtype):
         """A score z = tau log2(e) q.k is a sum of D exact products in fp32, off
-        by at most (D + 4) 2^-24 sum |q k|; a weight 2^(z - m) then by the
+        by at most (D + 4) 2^-24 |tau| log2(e) sum |q k|; a weight 2^(z - m) then by the
         factor e^(2 dz ln 2), 2^-21 from the exponential and its scales, and
         what its 16-bit terms drop (FP8: 2^-22 or, for a bf16 output, 2^-11;
         BF16: 2^-24 or 2^-16); sums of L weights by L 2^-24, in numerator and
@@ -100,7 +100,7 @@ class PrefixCase:
         rounding, half a step."""
         q = np.abs(synth.bf16_to_f32(self.q).astype(np.float64))
         kmax = np.abs(self.values("k")).max(axis=(0, 2))  # [H][D]
-        z = np.einsum("bhd,hd->bh", q, np.repeat(kmax, self.Hq // self.H, axis=0)) * self.tau * math.log2(math.e)
+        z = np.einsum("bhd,hd->bh", q, np.repeat(kmax, self.Hq // self.H, axis=0)) * abs(self.tau) * math.log2(math.e)
         dz = (self.D + 4) * 2.0 ** -24 * z
         fp32 = out_dtype == torch.float32
         drop = (2.0 ** -24 if fp32 else 2.0 ** -16) if self.cache_kind == BF16 else (2.0 ** -22 if fp32 else 2.0 ** -11)

@@ -234,6 +234,26 @@ def test_on_a_side_stream_beside_another_call():
         assert all(torch.equal(x, want[i]) for x in got[i])
 
 
+@pytest.mark.parametrize("cache", [FP8, FP8_TOKEN, BF16])
+@pytest.mark.parametrize("tau", [0.0, -0.2])
+def test_scales_that_are_not_positive(cache, tau):
+    """Zero: every token weighs the same.  Negative: the smallest product is the largest score."""
+    c = PrefixCase(18, [0, 0, -1, 0], [12], [1, 9, 21, 15], q_heads=8, kv_heads=2, dim=64, page=16, cache=cache)
+    c.tau = tau
+    c.assert_matches()
+
+
+@pytest.mark.parametrize("cache", [FP8, BF16])
+@pytest.mark.parametrize("pages", [40, 3])
+def test_withheld_tile_times_out_and_context_stays_usable(cache, pages):
+    """The test hook makes a CTA's first tile never arrive: the bounded waits
+    give up, every request says so, and the next call is right."""
+    c = PrefixCase(19, [0] * 9 + [-1], [pages], [30] * 10, q_heads=32, kv_heads=2, dim=128, page=16, cache=cache)
+    _, st = c.call(flags=abi.FLAG_TEST_WITHHOLD)
+    assert (st & abi.ST_TIMEOUT).all(), st
+    c.assert_matches()
+
+
 def test_fork_decode_release_together():
     """One prompt forked into samples that decode a few steps each, reading the
     prompt's pages once, and are given back: outputs against the oracle, and
@@ -312,5 +332,10 @@ def test_wrong_arguments_are_refused():
         c.call(workspace=torch.empty(512, dtype=torch.uint8, device="cuda"))
     with pytest.raises(abi.PfkvError):
         c.call(k_new=torch.zeros(2, 2, 64, dtype=torch.bfloat16, device="cuda"))
+    for tau in (float("nan"), float("inf")):
+        with pytest.raises(abi.PfkvError):
+            c.tau = tau
+            c.call()
+    c.tau = 0.1
     with pytest.raises(abi.PfkvError):
         c.call(block_tags=None, flags=abi.FLAG_TAG_CHECK)
