@@ -36,14 +36,12 @@
 // tokens of each tile and half 1 the others; each half then leaves a partial
 // result of its own.
 //
-// The running maximum m of a row is a reference that moves only when a unit
-// exceeds it by far (2^14 for f16 weights, which then still fit; 2^60 for
-// bf16), which after the first unit hardly happens; O is then rescaled in
-// tensor memory by the row's own softmax warp, after the products it has handed
-// over and before the next.  (With 2^8 a third of the units of heavy-tailed
-// scores, one key element in a hundred 20 times as large, moved some row.)
-// f16 weights below 2^-14 of the reference are subnormal: off by at most 2^-25
-// of it, alone or (second term) together.
+// The running maximum m of a row is a reference that moves only when a weight
+// would pass 2^14 (f16, where it still fits; 2^60 for bf16), which after the
+// first units hardly happens; O is then rescaled in tensor memory by the row's
+// own softmax warp, after the products it has handed over and before the next.
+// f16 weights below 2^-14 are subnormal: off by at most 2^-25, alone or (second
+// term) together.
 #pragma once
 
 #include "prefix.cuh"
@@ -87,12 +85,16 @@ struct PCfg {
   __host__ __device__ static constexpr uint32_t col_x(int t, int b) { return 128 * kBufs + (uint32_t)(t * kBufs + b) * 32; }
   __host__ __device__ static constexpr uint32_t col_o(int t) { return 512 - (uint32_t)(2 - t) * kD; }
   static_assert((kTerms == 3 ? 192 : 128) * kBufs + 2 * kD <= 512, "tensor memory plan");
-  // A row's reference is set kHead above its maximum (log2) and moves when a
-  // score exceeds it by kGrow.  f16: weights up to 2^14, times V scales of at
-  // most twice their reference, stay below 65504; bf16 has the range of fp32.
-  // Headroom saves moves and costs small weights bits (f16 steps are 2^-24 of
-  // the reference at least), which one term, of a bf16 output, can spare.
-  static constexpr float kHead = kFp8 && kTerms == 1 ? 4.f : 0.f, kGrow = kFp8 ? 14.f : 60.f;
+  // The maximum's weight is 2^kLead when a row's reference is set, and the
+  // reference moves when a weight would pass 2^kGrow.  f16: weights up to
+  // 2^14, times V scales of at most twice their reference, stay below 65504,
+  // and steps are 2^-24 at least, so a weight is off by 2^-25-kLead of the
+  // largest; bf16 has the range of fp32.  A lead costs moves: 1.76 -> 1.82 us
+  // per tile from 2^-4 to 2^0 with one term, 2.42 -> 2.64 from 2^0 to 2^10 with
+  // two.  Under a first token that takes 2^13 times a later one's weight (1024
+  // tokens), the smallest lead put outputs off by 2e-2 and 5e-4 of sum p |v|;
+  // these leave 2^-8, a bf16 output's rounding, and 3e-6.
+  static constexpr float kLead = kFp8 && kTerms == 2 ? 10.f : 0.f, kGrow = kFp8 ? 14.f : 60.f;
   static constexpr uint32_t kOffQ = 0, kOffT = 2 * kQBytes, kOffCode = kOffT + kSlots * kTBytes;
   static constexpr uint32_t kOffCodeScale = kOffCode + kStage * kCodeBytes;  // K and V scales beside the codes of K
   static constexpr uint32_t kOffScale = kOffCodeScale + kStage * 2 * kTok * 4;
@@ -664,7 +666,7 @@ __device__ __forceinline__ void softmax_rows(const PrefixArgs &a, uint8_t *smem,
       // move the reference
       const bool grow = mx > m + C::kGrow || first;
       if (__any_sync(0xffffffffu, grow || moved != 1.f)) {
-        const float mn = grow ? mx + C::kHead : m;
+        const float mn = grow ? mx - C::kLead : m;
         const float al = first ? 0.f : fast_exp2(m - mn);
         l *= al;
         if (!first) {

@@ -4,6 +4,7 @@ import numpy as np
 import pytest
 import torch
 
+import oracle
 from gpu_helpers import dev_bf16, dev_i32
 from paged_fp8_kv_quantize_gb300 import abi, synth
 from prefix_helpers import BF16, FP8, FP8_TOKEN, PrefixCase
@@ -234,6 +235,35 @@ def test_on_a_side_stream_beside_another_call():
         assert all(torch.equal(x, want[i]) for x in got[i])
 
 
+@pytest.mark.parametrize("out", list(OUT))
+@pytest.mark.parametrize("cache", [FP8, FP8_TOKEN, BF16])
+def test_first_token_that_outweighs_the_others(cache, out):
+    """Small weights keep their bits beside a large one: weights in f16 are off
+    by 2^-25 of the largest (one term; two: 2^-35, the largest at 2^10) where
+    they are subnormal, times V scales up to the largest, and the sum of the
+    weights is at least the largest."""
+    c = PrefixCase(20, [0] * 6 + [1] * 5, [64, 9], [5 * i + 1 for i in range(11)], q_heads=16, kv_heads=2, dim=64,
+                   page=16, cache=cache)
+    base = c.rng.standard_normal(64).astype(np.float32)
+    c.q = synth.bf16_bits((1.5 * base + 0.3 * c.rng.standard_normal((11, 16, 64))).astype(np.float32))
+    for p in (c.table[0, 0], c.table[6, 0]):
+        rows = c.ref.k_pool.reshape(c.P, 2, 16, 64)[p, :, 0]
+        rows[:] = synth.bf16_bits(base) if cache == BF16 else oracle.e4m3_encode(64 * base)
+        if cache == FP8_TOKEN:
+            c.ref.k_scale.reshape(c.P, 2, 16)[p, :, 0] = 1 / 64
+            c.ref.v_scale.reshape(c.P, 2, 16)[p, :, 0] = 2.0 ** -12
+    got, st = c.call(OUT[out])
+    want, _, mag = c.want()
+    tol = c.tolerance(want, mag, OUT[out])
+    if cache != BF16:
+        if cache == FP8_TOKEN:
+            c.ref.v_scale[:] = c.ref.v_scale.max()
+        c.tau = 0.0  # sum |v| is the mean of |v| under equal weights, times the length
+        extra = c.want()[2] * c.lens[:, None, None] * 2.0 ** (-35 if out == "fp32" else -25)
+        tol = tol + extra * (1 + 2.0 ** -8)
+    assert not st.any() and (np.abs(got.float().cpu().numpy() - want) <= tol).all()
+
+
 @pytest.mark.parametrize("cache", [FP8, FP8_TOKEN, BF16])
 @pytest.mark.parametrize("tau", [0.0, -0.2])
 def test_scales_that_are_not_positive(cache, tau):
@@ -281,8 +311,6 @@ def test_fork_decode_release_together():
                     dev_i32(np.full(B - 1, n0, np.int32)), table, tags, flags=abi.FLAG_TAG_CHECK)
     assert not st.any()
     group, shared = torch.zeros(B, dtype=torch.int32, device="cuda"), dev_i32(np.array([n0 // S]))
-    import oracle
-    import prefix_helpers
     c = PrefixCase(31, [0] * B, [n0 // S], [n0 % S] * B, q_heads=Hq, kv_heads=H, dim=D, page=S)
     c.P, c.gpu = P, cache
     for step in range(20):
