@@ -291,19 +291,22 @@ int pfkv_paged_decode_step(const pfkv_cache *cache, const void *k_new, const voi
  *                  n_groups, max_splits) bytes, 256-byte aligned
  *   status[b]    : that of paged_decode_attention, and
  *     BAD_GROUP      prefix_group[b] outside [-1, n_groups), or its
- *                    prefix_pages outside [0, max_pages]
+ *                    prefix_pages outside [0, max_pages] or 2^31 - 4096
+ *                    tokens or more
  *     BAD_LEN        also a length below the prefix, or (with k_new) a new
  *                    token inside it
  *     PREFIX_DIFFERS an entry of the prefix is another page than the group's
- *                    first request (in batch order) has there
+ *                    first request (in batch order, of those whose length
+ *                    covers the prefix) has there
  *   As elsewhere, a request with a data fault gets zeros and does not touch
- *   the others of its group.
+ *   the others of its group; an unused row of the batch may keep its group
+ *   with a length of 0.
  * Slots past a request's length may hold anything here, NaN among it.
  * The other arguments are those of paged_decode_attention.  Supported: its
  * grouped-query shapes (head_dim 64 or 128, FP8 with either scale mode, or
- * BF16) with up to 4096 groups.  The latent stream is not
- * (PFKV_ERR_UNSUPPORTED): its decode is bound by its products, which sharing
- * does not lessen.  batch * num_q_heads may not reach 2^31 (PFKV_ERR_SHAPE).
+ * BF16) with up to 4096 groups of up to 65535 requests in all.  The latent
+ * stream is not (PFKV_ERR_UNSUPPORTED): its decode is bound by its products,
+ * which sharing does not lessen.
  */
 enum { PFKV_OUT_FP32 = 0, PFKV_OUT_BF16 = 1 };
 
@@ -430,17 +433,19 @@ int pfkv_page_copy(const pfkv_cache *cache, const int32_t *src_pages, const int3
  *               parent of any entry of the call
  *     NO_PAGES  the sound entries together need more fresh pages than are
  *               free: none of them is done, and nothing is taken
- * Fresh pages are taken in list order. */
+ * Fresh pages are taken in list order.  n may not exceed 65536
+ * (PFKV_ERR_SHAPE). */
 int pfkv_page_fork(void *state, uint32_t *page_tags, int32_t *page_refs, const pfkv_cache *cache,
                    const int32_t *parents, const int32_t *children, const int32_t *lens, int32_t n,
                    int32_t *block_table, uint32_t *block_tags, int32_t batch, int32_t max_pages, uint32_t flags,
                    uint32_t *fork_status, void *stream);
 
 /* page_release -- each listed page loses one holder; the page returns to the
- * free list with its last one.  A page may be listed once per holder.  Where
- * no page is shared this is pfkv_page_free.  page_status[i]: 0, PAGE_OOB, or
- * NOT_HELD (not handed out, or given back by all its holders earlier in the
- * list).  n must be below 2^30. */
+ * free list with its last one.  A page may be listed once per holder; one
+ * listed more often goes back at its first listing, and the others are
+ * NOT_HELD.  Where no page is shared this is pfkv_page_free.
+ * page_status[i]: 0, PAGE_OOB, or NOT_HELD (also: not handed out).  n must be
+ * below 2^30. */
 int pfkv_page_release(void *state, int32_t *page_refs, const int32_t *pages, int32_t n, uint32_t *page_status,
                       void *stream);
 

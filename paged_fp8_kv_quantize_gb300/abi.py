@@ -8,6 +8,7 @@ implementation behind it.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -188,8 +189,21 @@ def _arg(t, name, n, dev, dtype=torch.int32):
     return t.data_ptr()
 
 
-def _raw_stream(stream, dev):
-    return stream.cuda_stream if stream is not None else torch.cuda.current_stream(dev).cuda_stream
+def _on_stream(f):
+    """f with its stream (None: the current one) as the current stream: what it allocates belongs to that stream."""
+
+    @functools.wraps(f)
+    def run(*args, stream=None, **kw):
+        if stream is None:
+            return f(*args, **kw)
+        with torch.cuda.stream(stream):
+            return f(*args, **kw)
+
+    return run
+
+
+def _current_stream(dev):
+    return torch.cuda.current_stream(dev).cuda_stream
 
 
 class PagedCache:
@@ -232,8 +246,10 @@ class PagedCache:
                          _ptr(self.k_pool), _ptr(self.v_pool), _ptr(self.k_scale), _ptr(self.v_scale),
                          _ptr(self.page_tags))
 
-    def _ref(self):
+    def _ref(self, dev):
         """desc() by reference, its struct kept from call to call and the addresses filled in anew."""
+        if self.page_tags.get_device() != dev:
+            raise ValueError(f"the cache is on {self.page_tags.device}, not on the current device")
         d = self.__dict__.get("_desc")
         if d is None:
             d = self._desc = self.desc()
@@ -344,9 +360,10 @@ _OUT_DTYPES = {torch.float32: 0, torch.bfloat16: 1}  # PFKV_OUT_*
 _prefix = lib.pfkv_paged_decode_attention_prefix
 
 
+@_on_stream
 def paged_decode_attention_prefix(cache, q, seq_lens, block_table, block_tags, prefix_group, prefix_pages,
                                   softmax_scale, flags=0, max_splits=64, k_new=None, v_new=None, workspace=None,
-                                  out=None, out_dtype=torch.float32, status=None, stream=None):
+                                  out=None, out_dtype=torch.float32, status=None):
     """Decode attention of a batch whose groups share prefixes, each shared page read once
     (pfkv_paged_decode_attention_prefix).  With k_new / v_new the new tokens are appended first."""
     B, Hq, D = q.shape
@@ -368,13 +385,13 @@ def paged_decode_attention_prefix(cache, q, seq_lens, block_table, block_tags, p
         status = seq_lens.new_empty(B)
     bf16, rows, dev = torch.bfloat16, B * cache.H * cache.D, torch.cuda.current_device()
     rc = _prefix(
-        cache._ref(), _arg(k_new, "k_new", rows, dev, bf16), _arg(v_new, "v_new", rows, dev, bf16),
+        cache._ref(dev), _arg(k_new, "k_new", rows, dev, bf16), _arg(v_new, "v_new", rows, dev, bf16),
         _arg(q, "q", B * Hq * D, dev, bf16), Hq, _arg(seq_lens, "seq_lens", B, dev),
         _arg(block_table, "block_table", B * MP, dev), _arg(block_tags, "block_tags", B * MP, dev), B, MP,
         _arg(prefix_group, "prefix_group", B, dev), _arg(prefix_pages, "prefix_pages", n_groups, dev), n_groups,
         float(softmax_scale), int(flags), int(max_splits), _arg(workspace, "workspace", workspace.numel(), dev, torch.uint8),
         workspace.numel(), _arg(out, "out", B * Hq * D, dev, out.dtype), kind, _arg(status, "status", B, dev),
-        _raw_stream(stream, dev))
+        _current_stream(dev))
     _check("pfkv_paged_decode_attention_prefix", rc)
     return out, status
 
@@ -430,14 +447,15 @@ _page_copy, _page_fork = lib.pfkv_page_copy, lib.pfkv_page_fork
 _page_release, _page_compact = lib.pfkv_page_release, lib.pfkv_page_compact
 
 
-def page_copy(cache: PagedCache, src_pages, dst_pages, slots=None, page_status=None, stream=None):
+@_on_stream
+def page_copy(cache: PagedCache, src_pages, dst_pages, slots=None, page_status=None):
     """Copy pages src_pages[i] to dst_pages[i] of the same cache, the first slots[i] slots of each (None: all)."""
     n, dev = src_pages.numel(), torch.cuda.current_device()
     if page_status is None:
         page_status = src_pages.new_empty(n)
-    rc = _page_copy(cache._ref(), _arg(src_pages, "src_pages", n, dev), _arg(dst_pages, "dst_pages", n, dev),
+    rc = _page_copy(cache._ref(dev), _arg(src_pages, "src_pages", n, dev), _arg(dst_pages, "dst_pages", n, dev),
                     _arg(slots, "slots", n, dev), n, _arg(page_status, "page_status", n, dev),
-                    _raw_stream(stream, dev))
+                    _current_stream(dev))
     _check("pfkv_page_copy", rc)
     return page_status
 
@@ -495,8 +513,8 @@ class PageAllocator:
         _check("pfkv_page_realloc", rc)
         return tags, st
 
-    def fork(self, cache, parents, children, lens, block_table, block_tags=None, flags=0, fork_status=None,
-             stream=None):
+    @_on_stream
+    def fork(self, cache, parents, children, lens, block_table, block_tags=None, flags=0, fork_status=None):
         """Rows children[i] of block_table (and block_tags) get the first lens[i] tokens of rows parents[i]: full
         pages shared, the partly filled last one copied into a fresh page (pfkv_page_fork).  -> fork_status [n]"""
         n, dev = parents.numel(), torch.cuda.current_device()
@@ -505,25 +523,27 @@ class PageAllocator:
             fork_status = parents.new_empty(n)
         rc = _page_fork(
             self.state.data_ptr(), _arg(cache.page_tags, "page_tags", cache.P, dev),
-            _arg(self.refs, "refs", self.num_pages, dev), cache._ref(), _arg(parents, "parents", n, dev),
+            _arg(self.refs, "refs", self.num_pages, dev), cache._ref(dev), _arg(parents, "parents", n, dev),
             _arg(children, "children", n, dev), _arg(lens, "lens", n, dev), n,
-            _arg(block_table, "block_table", B * MP, dev), _arg(block_tags, "block_tags", B * MP, dev), B, MP, flags,
-            _arg(fork_status, "fork_status", n, dev), _raw_stream(stream, dev))
+            _arg(block_table, "block_table", B * MP, dev), _arg(block_tags, "block_tags", B * MP, dev), B, MP, int(flags),
+            _arg(fork_status, "fork_status", n, dev), _current_stream(dev))
         _check("pfkv_page_fork", rc)
         return fork_status
 
-    def release(self, pages, page_status=None, stream=None):
+    @_on_stream
+    def release(self, pages, page_status=None):
         """Take one holder off each listed page; a page returns to the free list with its last (pfkv_page_release)."""
         n, dev = pages.numel(), torch.cuda.current_device()
         if page_status is None:
             page_status = pages.new_empty(n)
         rc = _page_release(self.state.data_ptr(), _arg(self.refs, "refs", self.num_pages, dev),
                            _arg(pages, "pages", n, dev), n, _arg(page_status, "page_status", n, dev),
-                           _raw_stream(stream, dev))
+                           _current_stream(dev))
         _check("pfkv_page_release", rc)
         return page_status
 
-    def compact(self, cache, block_table, block_tags=None, used=None, max_moves=None, stream=None):
+    @_on_stream
+    def compact(self, cache, block_table, block_tags=None, used=None, max_moves=None):
         """Move the highest held pages into the lowest free ones and rename them in block_table (and block_tags),
         the first used[b] entries of each row (pfkv_page_compact).
         -> (moved_src, moved_dst, n_moved [1]) on the device; the lists are filled up to n_moved."""
@@ -533,10 +553,10 @@ class PageAllocator:
         src, dst, n_moved = block_table.new_empty(max(m, 0)), block_table.new_empty(max(m, 0)), block_table.new_empty(1)
         rc = _page_compact(
             self.state.data_ptr(), _arg(cache.page_tags, "page_tags", cache.P, dev),
-            _arg(self.refs, "refs", self.num_pages, dev), cache._ref(),
+            _arg(self.refs, "refs", self.num_pages, dev), cache._ref(dev),
             _arg(block_table, "block_table", B * MP, dev), _arg(block_tags, "block_tags", B * MP, dev),
             _arg(used, "used", B, dev), B, MP, m, src.data_ptr() or None, dst.data_ptr() or None, n_moved.data_ptr(),
-            _raw_stream(stream, dev))
+            _current_stream(dev))
         _check("pfkv_page_compact", rc)
         return src, dst, n_moved
 

@@ -63,7 +63,9 @@ static bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 
 // any model's; they bound the workspace arithmetic).
 constexpr int kMaxQHeads = 65536;
 constexpr int kMaxHeadDim = 4096;
-constexpr int kMaxPrefixGroups = 4096;  // one shared-memory counter each in the plan
+// the shared-prefix plan: a pair of shared-memory words per group, one of them two 16-bit counts of requests
+constexpr int kMaxPrefixGroups = 4096, kMaxPrefixBatch = 65535;
+constexpr int kMaxForks = 65536;  // every fork is compared with every other
 
 static bool is_latent(const pfkv_cache *c) {
   return c->kv_shared && c->num_kv_heads == 1 && c->head_dim == 576 && c->v_head_dim == 512;
@@ -124,9 +126,8 @@ static int decode_common(int want_dtype, const pfkv_cache *c, const void *q, int
   if (!isfinite(softmax_scale)) return PFKV_ERR_SHAPE;
   if (prefix) {
     if (prefix->out_dtype != PFKV_OUT_FP32 && prefix->out_dtype != PFKV_OUT_BF16) return PFKV_ERR_DTYPE;
-    // the join has a block per (request, query head)
-    if (prefix->n_groups < 0 || (int64_t)batch * Hq > 0x7fffffff) return PFKV_ERR_SHAPE;
-    if (prefix->n_groups > kMaxPrefixGroups || c->kv_shared) return PFKV_ERR_UNSUPPORTED;
+    if (prefix->n_groups < 0 || (int64_t)batch * Hq > 0x7fffffff) return PFKV_ERR_SHAPE;  // rows are counted in int
+    if (prefix->n_groups > kMaxPrefixGroups || batch > kMaxPrefixBatch || c->kv_shared) return PFKV_ERR_UNSUPPORTED;
   }
   if (batch == 0) return PFKV_OK;
   if (prefix && (!prefix->group_of || (prefix->n_groups > 0 && !prefix->group_pages))) return PFKV_ERR_NULL;
@@ -280,7 +281,7 @@ size_t pfkv_prefix_workspace_bytes(const pfkv_cache *cache, int32_t batch, int32
                                    int32_t max_splits) {
   const size_t n = pfkv_decode_workspace_bytes(cache, batch, num_q_heads, max_splits);
   if (n == 0 || n == SIZE_MAX || n_groups < 0) return n == SIZE_MAX ? n : 0;
-  if (n_groups > kMaxPrefixGroups || cache->num_kv_heads < 1 || num_q_heads % cache->num_kv_heads ||
+  if (n_groups > kMaxPrefixGroups || batch > kMaxPrefixBatch || cache->num_kv_heads < 1 || num_q_heads % cache->num_kv_heads ||
       cache->head_dim < 1 || cache->head_dim > kMaxHeadDim)
     return SIZE_MAX;
   return prefix_ws_bytes(n, batch, num_q_heads, cache->num_kv_heads, cache->head_dim, n_groups);
@@ -378,7 +379,7 @@ int pfkv_page_fork(void *state, uint32_t *page_tags, int32_t *page_refs, const p
   int rc = check_cache(cache);
   if (rc) return rc;
   if (!state || !page_tags || !page_refs) return PFKV_ERR_NULL;
-  if (n < 0 || batch < 0 || max_pages < 1 || (uint64_t)batch * (uint64_t)max_pages > (1ull << 40))
+  if (n < 0 || n > kMaxForks || batch < 0 || max_pages < 1 || (uint64_t)batch * (uint64_t)max_pages > (1ull << 40))
     return PFKV_ERR_SHAPE;
   if (!aligned256(state)) return PFKV_ERR_ALIGN;
   if (n == 0) return PFKV_OK;

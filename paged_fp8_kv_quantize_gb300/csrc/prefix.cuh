@@ -24,7 +24,7 @@ constexpr int kMaxRanges = 256;  // CTAs of the prefix kernel at most
 constexpr int kRows = 256;       // query rows of an item
 
 struct PrefixGroup {
-  int first, n;      // its requests: members[first .. first + n)
+  int first, n;      // its requests: members[first .. first + n), those whose length covers the prefix
   int lead, pad;     // the first of them
   int pages, item0;  // prefix pages, number of its first item
   long long unit0;   // its first unit on the line
@@ -32,8 +32,8 @@ struct PrefixGroup {
 
 struct PrefixHdr {
   long long T;
-  int R;  // ranges; 0 when no group has a prefix
-  int pad;
+  int R;          // ranges; 0 when no group has a prefix
+  int max_pages;  // pages of the longest prefix
 };
 
 // Where the join finds a row's pieces of the prefix: n of them, piece i in row

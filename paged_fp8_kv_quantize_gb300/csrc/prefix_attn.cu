@@ -29,6 +29,9 @@ namespace {
 constexpr int kPlanThreads = 256;
 constexpr int kPlanGroups = 64;  // groups whose segments block B keeps in shared memory
 
+// Tokens of a prefix stay below this, so that a tile past the end still counts in int.
+constexpr long long kMaxPrefixTokens = (1LL << 31) - 4096;
+
 // Sum over the block (kPlanThreads threads); every thread gets it.
 __device__ __forceinline__ int block_sum(int v, int *s_sum) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -44,7 +47,9 @@ __device__ __forceinline__ int block_sum(int v, int *s_sum) {
 
 // Block b < B: request b.  Block B: the groups' segments of the work line.
 __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const PrefixArgs a) {
-  extern __shared__ int s_count[];  // block B: requests of each group, then the first of each
+  // block B: requests of each group (low half: all, high half: those whose length covers the prefix), then the
+  // first of the latter
+  extern __shared__ uint32_t s_count[];
   __shared__ int s_sum[kPlanThreads / 32];
   __shared__ PrefixGroup s_groups[kPlanGroups];
   __shared__ PrefixHdr s_hdr;
@@ -52,31 +57,36 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const PrefixA
   pdl_launch_dependents();
   const int t = threadIdx.x, B = a.d.B, MP = a.d.MP, S = a.d.S;
   if ((int)blockIdx.x == B) {
-    int *s_lead = s_count + a.n_groups;
+    int *s_lead = reinterpret_cast<int *>(s_count + a.n_groups);
     for (int g = t; g < a.n_groups; g += kPlanThreads) {
-      s_count[g] = 0;
+      s_count[g] = 0u;
       s_lead[g] = B;
     }
     __syncthreads();
     for (int b = t; b < B; b += kPlanThreads) {
       const int g = a.group_of[b];
       if (g < 0 || g >= a.n_groups) continue;
-      atomicAdd(&s_count[g], 1);
-      atomicMin(&s_lead[g], b);
+      const long long L = a.d.seq_lens[b];
+      const bool fits = L >= 1 && L <= (long long)MP * S && L >= (long long)a.group_pages[g] * S;
+      atomicAdd(&s_count[g], fits ? 0x10001u : 1u);
+      if (fits) atomicMin(&s_lead[g], b);
     }
     __syncthreads();
     if (t < 32) {  // 32 groups at a time, their sums carried along
-      int first = 0, item = 0;
+      int first = 0, item = 0, longest = 0;
       long long unit = 0;
       for (int base = 0; base < a.n_groups; base += 32) {
         const int g = base + t;
-        const int n = g < a.n_groups ? s_count[g] : 0;
+        const uint32_t count = g < a.n_groups ? s_count[g] : 0u;
+        const int all = (int)(count & 0xffffu), n = (int)(count >> 16);
         int pages = g < a.n_groups ? a.group_pages[g] : 0;
-        if (pages < 0 || pages > MP || n == 0) pages = 0;  // a bad one is reported by its requests
+        // a bad one is reported by its requests
+        if (pages < 0 || pages > MP || (long long)pages * S >= kMaxPrefixTokens || n == 0) pages = 0;
+        longest = max(longest, pages);
         const HeadLine line = head_line(n, a.G, pages, a.c0);
         const int items = pages ? a.d.cache.num_kv_heads * line.blocks : 0;
         const long long units = pages ? a.d.cache.num_kv_heads * line.head : 0;
-        int xn = n, xi = items;
+        int xn = all, xi = items;
         long long xu = units;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -88,16 +98,17 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const PrefixA
             xu += yu;
           }
         }
-        const PrefixGroup pg{first + xn - n, n, g < a.n_groups ? s_lead[g] : 0, 0, pages, item + xi - items, unit + xu - units};
+        const PrefixGroup pg{first + xn - all, n, g < a.n_groups ? s_lead[g] : 0, 0, pages, item + xi - items, unit + xu - units};
         if (g < kPlanGroups) s_groups[g] = pg;
         if (g < a.n_groups) a.groups[g] = pg;
         first += __shfl_sync(0xffffffffu, xn, 31);
         item += __shfl_sync(0xffffffffu, xi, 31);
         unit += __shfl_sync(0xffffffffu, xu, 31);
       }
+      longest = __reduce_max_sync(0xffffffffu, longest);
       if (t == 0) {
         const long long r = unit / a.min_units;
-        s_hdr = PrefixHdr{unit, unit == 0 ? 0 : r < 1 ? 1 : (int)(r < a.ctas ? r : a.ctas), 0};
+        s_hdr = PrefixHdr{unit, unit == 0 ? 0 : r < 1 ? 1 : (int)(r < a.ctas ? r : a.ctas), longest};
         *a.hdr = s_hdr;
       }
     }
@@ -123,21 +134,21 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const PrefixA
   int pages = 0, rank = 0;
   if (g >= 0 && g < a.n_groups) {
     pages = a.group_pages[g];
-    if (pages < 0 || pages > MP) {
+    if (pages < 0 || pages > MP || (long long)pages * S >= kMaxPrefixTokens) {
       bits |= PFKV_ST_BAD_GROUP;
       pages = 0;
     }
+    if (!bits && (long long)L < (long long)pages * S) bits |= PFKV_ST_BAD_LEN;
     // its place among all members, and in its group
     int before = 0, mine = 0;
-    for (int k = t; k < B; k += kPlanThreads) {
-      const int gk = a.group_of[k];
+    for (int k = t; k < B && !bits; k += kPlanThreads) {
+      const int gk = a.group_of[k], Lk = a.d.seq_lens[k];
       before += gk >= 0 && gk < g;
-      mine += gk == g && k < b;
+      mine += gk == g && k < b && Lk >= 1 && (long long)Lk <= (long long)MP * S && (long long)Lk >= (long long)pages * S;
     }
     rank = block_sum(mine, s_sum);
     const int at = block_sum(before, s_sum) + rank;
-    if (t == 0) a.members[at] = b;
-    if (!bits && (long long)L < (long long)pages * S) bits |= PFKV_ST_BAD_LEN;
+    if (t == 0 && !bits) a.members[at] = b;
   }
   if (t == 0) {
     const long long own = (long long)L - (long long)pages * S;

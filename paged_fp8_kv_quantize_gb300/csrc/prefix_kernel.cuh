@@ -288,10 +288,10 @@ __device__ __forceinline__ void plan_tiles(const PrefixArgs &a, const CUtensorMa
 // Every member's first pages are the group's (those of its first request), lie
 // inside the pool and, under the tag check, have the tag of the member's
 // mapping.  (Request, 512 pages) at a time, over all CTAs.
-__device__ __forceinline__ void check_prefixes(const PrefixArgs &a) {
+__device__ __forceinline__ void check_prefixes(const PrefixArgs &a, const PrefixHdr &hdr) {
   constexpr int kChunk = 512;
   const int lane = threadIdx.x & 31;
-  const long long chunks = (a.d.MP + kChunk - 1) / kChunk;
+  const long long chunks = (hdr.max_pages + kChunk - 1) / kChunk;
   const bool tag_check = (a.d.flags & PFKV_FLAG_TAG_CHECK) != 0u;
   for (long long id = blockIdx.x; id < a.d.B * chunks; id += gridDim.x) {
     const int b = (int)(id / chunks), lo = (int)(id - b * chunks) * kChunk;
@@ -832,7 +832,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
   }
   if (warp == 15) {
     find_pieces(a, hdr);
-    check_prefixes(a);
+    check_prefixes(a, hdr);
   }
   __syncwarp();
   tc_fence_before();

@@ -156,21 +156,22 @@ __global__ void __launch_bounds__(kCopyThreads) fork_apply_kernel(const ForkArgs
 // ---------------------------------------------------------------- release
 //
 // The list is processed as if in order: a page with h holders may be listed
-// h times, the h-th time returns it to the free list (at that place of the
-// list), and any further one is NOT_HELD.  Three passes:
+// h times, and the h-th time returns it to the free list (at that place of the
+// list).  One listed more often, a caller's mistake, goes back where it is
+// listed first, and its other listings are NOT_HELD.  Three passes:
 //   count: how often each held page is listed (c), in its scratch word, as
 //          INT_MAX - c.
 //   sort:  a page with c < h stays held (kShared).  One with c = h is
 //          returned where it is listed last (kLast): the entries' largest
 //          index is found with atomicMin of -(index + 1) on the same word;
-//          c > h (kOver, a caller's mistake) marks it -(2^30 + index + 1).
+//          c > h (kOver) where it is listed first: atomicMin of
+//          index - (2^31 - 1), which lies below all of those.
 //   apply: kShared entries take one holder off; the others are walked by one
-//          block in list order, which pushes the returned pages.  An entry
-//          of a kOver page counts its earlier listings by reading the list.
+//          block in list order, which pushes the returned pages.
 // Classes stand in page_status between the passes.  Lists of up to
 // kReleaseOneBlock entries run all three in one block (one launch).
 enum { kShared = 0x10000u, kLast = 0x20000u, kOver = 0x40000u };
-constexpr int kOverBase = 1 << 30;
+constexpr int kOverBase = -INT_MAX;      // its entry i is marked kOverBase + i, below -(i + 1) as n < 2^30
 constexpr int kReleaseOneBlock = 4096;
 // Consecutive entries per thread of the ordered walk (64 rows of 1875 shared
 // pages given back: the apply kernel took 42 us with 4, 16 with 16).
@@ -204,14 +205,14 @@ __device__ __forceinline__ void release_sort(const ReleaseArgs &r, const AllocVi
   const int m = __ldcg(&v.mark[p]);
   bool over;
   if (m < 0) {  // another entry has marked the page
-    over = m < -kOverBase;
+    over = m < kOverBase / 2;
   } else {
     const int c = INT_MAX - m, h = holders(r, p);
     if (c < h) return;
     over = c > h;
   }
   r.status[i] = over ? kOver : kLast;
-  atomicMin(&v.mark[p], -(over ? kOverBase : 0) - (i + 1));
+  atomicMin(&v.mark[p], over ? kOverBase + i : -(i + 1));
 }
 
 __device__ __forceinline__ void release_shared(const ReleaseArgs &r, const AllocView &v, int i) {
@@ -245,17 +246,9 @@ __device__ __forceinline__ void release_push(const ReleaseArgs &r, const AllocVi
     for (int j = 0; j < kReleasePer; ++j) {
       if (!(st[j] & (kLast | kOver))) continue;
       const int i = (int)i0 + j, p = r.pages[i];
-      uint32_t fin = 0u;
-      if (st[j] == kLast) {
-        push |= (uint32_t)(__ldcg(&v.mark[p]) == -(i + 1)) << j;
-      } else {
-        const int h = holders(r, p);
-        int earlier = 0;
-        for (int k = 0; k < i && earlier < h; ++k) earlier += r.pages[k] == p;
-        push |= (uint32_t)(earlier == h - 1) << j;
-        if (earlier >= h) fin = PFKV_ST_NOT_HELD;
-      }
-      r.status[i] = fin;
+      const bool over = st[j] == kOver, back = __ldcg(&v.mark[p]) == (over ? kOverBase + i : -(i + 1));
+      push |= (uint32_t)back << j;
+      r.status[i] = over && !back ? PFKV_ST_NOT_HELD : 0u;
     }
     const int cnt = __popc(push);
     // exclusive scan of cnt over the block

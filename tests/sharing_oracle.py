@@ -3,6 +3,8 @@ plain Python over numpy arrays, one entry after another, as the header
 describes them.  Test infrastructure only."""
 from __future__ import annotations
 
+from collections import Counter
+
 import numpy as np
 
 STALE_TAG, PAGE_OOB, BAD_LEN, NO_PAGES, NOT_HELD, DUPLICATE, BAD_ROW = 1, 2, 4, 16, 32, 64, 128
@@ -84,16 +86,19 @@ class SharedPool:
 
     def release(self, pages):
         st = np.zeros(len(pages), dtype=np.uint32)
-        for i, p in enumerate(pages):
+        ids = [int(p) for p in pages]
+        over = {p for p, n in Counter(ids).items() if 0 <= p < self.P and n > self.refs[p] + 1}
+        for i, p in enumerate(ids):
             if not 0 <= p < self.P:
                 st[i] = PAGE_OOB
             elif not self.held[p]:
                 st[i] = NOT_HELD
-            elif self.refs[p] > 0:
+            elif self.refs[p] > 0 and p not in over:
                 self.refs[p] -= 1
-            else:
+            else:  # the last holder, or more listings than holders
+                self.refs[p] = 0
                 self.held[p] = False
-                self.stack.append(int(p))
+                self.stack.append(p)
         return st
 
     def compact(self, table, btags, used, max_moves):

@@ -134,6 +134,27 @@ def test_faults_stay_with_their_requests():
     assert st.cpu().numpy().view(np.uint32).tolist() == want.tolist()
 
 
+@pytest.mark.parametrize("members", [9, 40])
+def test_unused_rows_of_a_padded_batch(members):
+    """Rows without a request keep their group with a length of 0 or one that
+    ends inside the prefix: the group's pages are those of the first row that
+    has them, and the others take no part."""
+    c = PrefixCase(21, [0] * members + [1, 1], [20, 3], [7 * i + 1 for i in range(members + 2)], q_heads=16,
+                   kv_heads=2, dim=64, page=16)
+    unused = [0, 3, members - 1, members]
+    c.lens[unused] = [0, -1, 20 * 16 - 1, 0]
+    c.table[unused] = -1
+    got, st = c.call(flags=abi.FLAG_TAG_CHECK)
+    want = np.where(np.isin(np.arange(members + 2), unused), abi.ST_BAD_LEN, 0)
+    assert st.tolist() == want.tolist() and not got[unused].any()
+    out, _, mag = c.want()
+    used = np.flatnonzero(want == 0)
+    assert (np.abs(got.cpu().numpy() - out) <= c.tolerance(out, mag, torch.float32))[used].all()
+    c.lens[:] = 0  # a batch of nothing
+    got, st = c.call()
+    assert (st == abi.ST_BAD_LEN).all() and not got.any()
+
+
 def test_first_request_with_a_page_outside_the_pool():
     """The page is never fetched; the group's other requests have another page there."""
     c = PrefixCase(13, [0, 0, 0, -1], [3], [5, 6, 7, 8], q_heads=4, kv_heads=1, dim=64, page=16)
@@ -282,6 +303,20 @@ def test_withheld_tile_times_out_and_context_stays_usable(cache, pages):
     _, st = c.call(flags=abi.FLAG_TEST_WITHHOLD)
     assert (st & abi.ST_TIMEOUT).all(), st
     c.assert_matches()
+
+
+def test_stream_argument():
+    """What a call allocates for another stream belongs to that stream."""
+    c = PrefixCase(22, [0] * 12, [200], [5 * j + 1 for j in range(12)], q_heads=16, kv_heads=4, dim=128, page=16)
+    want = c.call()[0].clone()
+    args, side = c.args(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(8):
+        got.append(c.call(**args, stream=side)[0])
+        torch.empty(1 << 22, device="cuda").fill_(float("nan"))  # on the current stream, beside it
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, want) for x in got)
 
 
 def test_fork_decode_release_together():

@@ -213,9 +213,9 @@ def test_release_counts_holders():
     # four holders of a: two in this list, the page stays
     assert (p.release([a, c, a]) == 0).all()
     p.check("still held")
-    # c: two holders left, listed three times; b: four, listed four times
+    # c: two holders left, listed three times, so it goes back at once; b: four, listed four times
     st = p.release([c, b, b, c, c, b, b])
-    assert st.tolist() == [0, 0, 0, 0, 32, 0, 0]
+    assert st.tolist() == [0, 0, 0, 32, 32, 0, 0]
     p.check("given back in list order")
     assert p.alloc.free_list().cpu().tolist()[-2:] == [c, b]
     none = torch.empty(0, dtype=torch.int32, device="cuda")
@@ -249,6 +249,23 @@ def test_release_of_long_lists(n_rows, forks):
     # one page listed thousands of times
     p.release([again[0]] * 5000)
     p.check("never held")
+
+
+@pytest.mark.parametrize("repeat", [1, 900])
+def test_pages_listed_more_often_than_held(repeat):
+    """Short and long lists (one block, several): a page goes back at its first
+    listing, the rest of its listings are refused, and others are not touched."""
+    p = Pair("one_slot", 64, 6, 30, 8)
+    p.fill_row(0, 12)
+    p.fill_row(1, 5)
+    p.fork([0, 0, 1], [2, 3, 4], [12, 7, 5])  # three holders of seven pages, two of ten
+    a, b, c = p.table[0, 0], p.table[0, 9], p.table[1, 2]
+    pages = [b, a, c, a, b, a, 63, a, b, c, -1] + [a, 64, b] * repeat + [p.table[0, 1]]
+    st = p.release([int(x) for x in pages])
+    assert (st == 0).sum() == 5 and st[0] == st[1] == st[2] == st[9] == st[-1] == 0
+    p.check("released")
+    p.release([int(x) for x in pages] + [int(p.table[0, 1])] * 2 * repeat)
+    p.check("again")
 
 
 def test_release_without_sharing_is_free():

@@ -35,7 +35,7 @@ def test_refusals():
     assert call(n_groups=-1) == call(scale=float("inf")) == call(scale=float("nan")) == -2
     assert call(batch=1 << 20, mp=1 << 21) == -2
     assert call(batch=1 << 27, hq=32) == -2  # a join block per (request, head)
-    assert call(n_groups=4097) == -3
+    assert call(n_groups=4097) == call(batch=65536) == -3
     assert call(out_dtype=2) == call(out_dtype=-1) == -4
     assert call(desc(page_size=24)) == call(desc(page_size=272)) == -3
     lat = desc(num_kv_heads=1, head_dim=576, v_head_dim=512, kv_shared=1, scale_mode=1, page_size=64)
@@ -58,7 +58,7 @@ def test_workspace_bytes():
     assert rows - (256 + 8 * (64 * 4 // 256 + 1)) * 256 * 520 in range(64 * 1024)
     assert f(ctypes.byref(d), 64, 32, 5, 64) > one
     assert plain < f(ctypes.byref(d), 64, 32, 0, 64) < plain + 64 * 1024
-    for bad in ((64, 33, 1, 64), (64, 32, 4097, 64), (64, 32, 1, 300)):
+    for bad in ((64, 33, 1, 64), (64, 32, 4097, 64), (65536, 32, 1, 64), (64, 32, 1, 300)):
         assert f(ctypes.byref(d), *bad) == SIZE_MAX, bad
     assert f(None, 64, 32, 1, 64) == 0 and f(ctypes.byref(d), 64, 32, -1, 64) == 0
 

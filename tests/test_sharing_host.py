@@ -41,7 +41,7 @@ def test_fork_refusals():
     for k in ("state", "tags", "refs", "par", "chi", "lens", "table", "st"):
         assert call(**{k: None}) == -1, k
     assert call(btags=None, flags=abi.FLAG_TAG_CHECK) == -1
-    assert call(n=-1) == call(batch=-1) == call(mp=0) == call(batch=1 << 21, mp=1 << 20) == -2
+    assert call(n=-1) == call(n=65537) == call(batch=-1) == call(mp=0) == call(batch=1 << 21, mp=1 << 20) == -2
     assert call(state=272) == -6
     assert call(c=desc(page_size=0)) == -2
 
