@@ -753,7 +753,9 @@ __global__ void __launch_bounds__(Cfg<kFp8, kD, kG, kNCW>::kThreads, Cfg<kFp8, k
   // every request of the call as timed out (its output is not valid).
   __syncthreads();
   if (threadIdx.x == 0) a.cta_abort[blockIdx.x] = *abort_flag != 0;
-  if (kJoin && a.beside) pdl_wait();
+  // The kernel beside this one has to be over when this grid is: one block, the last to start, waits for it, and the
+  // others leave their SMs.
+  if (kJoin && a.beside && blockIdx.x == gridDim.x - 1) pdl_wait();
 }
 
 // ---------------------------------------------------------------- host side
