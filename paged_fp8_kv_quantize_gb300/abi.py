@@ -202,8 +202,7 @@ def _on_stream(f):
     return run
 
 
-def _current_stream(dev):
-    return torch.cuda.current_stream(dev).cuda_stream
+_current_stream = torch._C._cuda_getCurrentRawStream  # torch.cuda.current_stream(dev).cuda_stream without the object
 
 
 class PagedCache:
@@ -550,7 +549,7 @@ class PageAllocator:
         B, MP = block_table.shape
         room = self.num_pages // 2  # no pool needs more moves
         m, dev = room if max_moves is None else min(int(max_moves), room), torch.cuda.current_device()
-        src, dst, n_moved = block_table.new_empty(max(m, 0)), block_table.new_empty(max(m, 0)), block_table.new_empty(1)
+        src, dst, n_moved = block_table.new_empty(2 * max(m, 0) + 1).split((max(m, 0), max(m, 0), 1))
         rc = _page_compact(
             self.state.data_ptr(), _arg(cache.page_tags, "page_tags", cache.P, dev),
             _arg(self.refs, "refs", self.num_pages, dev), cache._ref(dev),

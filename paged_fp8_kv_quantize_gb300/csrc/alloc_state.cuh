@@ -15,7 +15,7 @@ constexpr int kAT = 1024;  // threads of the single-CTA kernels; also init's chu
 struct AllocHdr {
   int num_pages;
   int free_count;
-  int ticket;  // blocks of a fork's check that are done; zero between calls
+  int ticket;  // blocks of a fork's check or a compaction's count that are done; zero between calls
   int pad[61];
 };
 

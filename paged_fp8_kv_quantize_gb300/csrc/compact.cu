@@ -10,8 +10,9 @@
 //   a free page is move number F - f(q) - 1 as a destination (F free pages),
 //   and after m moves a page's place in the re-sorted free stack is q where
 //   fewer than m held pages lie above it, f(q) + m for the other free pages.
-// Three launches work this out (count per chunk, scan, plan; pools reach
-// millions of pages) and a fourth moves the data, which is all that costs:
+// Two launches work this out (count per chunk, whose last block to finish scans
+// the counts; plan: pools reach millions of pages) and a third moves the data,
+// which is all that costs:
 // it is bound by HBM, one read and one write of the moved pages.  In the same
 // launch the held flags and holder counts follow, and every live table entry
 // that names a moved page (found by a binary search of the sources, which
@@ -39,28 +40,31 @@ struct CompactArgs {
 
 // Chunk c covers q in [c * kAT, (c + 1) * kAT).
 __global__ void __launch_bounds__(kAT) compact_count_kernel(const CompactArgs a) {
-  AllocView v = view(a.state);
-  const int P = v.hdr->num_pages;
-  if (P != a.c.num_pages) return;
-  const long long q = (long long)blockIdx.x * kAT + threadIdx.x;
-  const int n = __syncthreads_count(q < P && !v.held[P - 1 - q]);
-  if (threadIdx.x == 0) v.counts[blockIdx.x] = n;
-}
-
-// Exclusive scan of the chunks' counts.
-__global__ void __launch_bounds__(kAT) compact_scan_kernel(const CompactArgs a, int n_chunks) {
+  __shared__ int s_last;
   __shared__ int s_warp[33];
-  pdl_wait();
   AllocView v = view(a.state);
-  if (v.hdr->num_pages != a.c.num_pages) {  // not this cache's allocator: nothing moves
-    if (threadIdx.x == 0) *a.n_moved = 0;
+  const int P = v.hdr->num_pages, n_chunks = gridDim.x;
+  if (P != a.c.num_pages) {  // not this cache's allocator: nothing moves
+    if (blockIdx.x == 0 && threadIdx.x == 0) *a.n_moved = 0;
     return;
   }
+  const long long q = (long long)blockIdx.x * kAT + threadIdx.x;
+  const int n = __syncthreads_count(q < P && !v.held[P - 1 - q]);
+  if (threadIdx.x == 0) {
+    v.counts[blockIdx.x] = n;
+    __threadfence();
+    s_last = atomicAdd(&v.hdr->ticket, 1) == n_chunks - 1;
+  }
+  __syncthreads();
+  if (!s_last) return;
+  __threadfence();
+  // the last block: exclusive scan of the chunks' counts
+  if (threadIdx.x == 0) v.hdr->ticket = 0;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int carry = 0;
   for (int base = 0; base < n_chunks; base += kAT) {
     const int c = base + (int)threadIdx.x;
-    const int cnt = c < n_chunks ? v.counts[c] : 0;
+    const int cnt = c < n_chunks ? __ldcg(&v.counts[c]) : 0;
     int incl = cnt;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -193,8 +197,6 @@ int launch_page_compact(void *state, uint32_t *page_tags, int *page_refs, const 
   const int n_chunks = (int)((c.num_pages + (long long)kAT - 1) / kAT);
   compact_count_kernel<<<n_chunks, kAT, 0, s>>>(a);
   int rc = cuda_ok(cudaGetLastError(), "compact launch (count)");
-  if (rc) return rc;
-  rc = cuda_ok(launch_dependent(compact_scan_kernel, dim3(1), kAT, 0, s, a, n_chunks), "compact launch (scan)");
   if (rc) return rc;
   rc = cuda_ok(launch_dependent(compact_plan_kernel, dim3(n_chunks), kAT, 0, s, a), "compact launch (plan)");
   if (rc) return rc;
