@@ -102,6 +102,8 @@ class SharedPool:
         return st
 
     def compact(self, table, btags, used, max_moves):
+        n_live = np.full(table.shape[0], table.shape[1]) if used is None else np.asarray(used)
+        live = np.arange(table.shape[1]) < n_live[:, None]
         moves = []
         while len(moves) < max_moves:
             h, f = np.flatnonzero(self.held), np.flatnonzero(~self.held)
@@ -113,12 +115,11 @@ class SharedPool:
             self.tags[d] = (int(self.tags[d]) + 1) & 0xFFFFFFFF
             for a in self.arrays:
                 a[d] = a[s]
-            for b in range(table.shape[0]):
-                for k in range(table.shape[1] if used is None else min(max(int(used[b]), 0), table.shape[1])):
-                    if table[b, k] == s and (btags is None or btags[b, k] == self.tags[s]):
-                        table[b, k] = -2 - d  # not a page of a later move
-                        if btags is not None:
-                            btags[b, k] = self.tags[d]
+            named = live & (table == s)
+            if btags is not None:
+                named &= btags == self.tags[s]
+                btags[named] = self.tags[d]
+            table[named] = -2 - d  # not a page of a later move
             moves.append((s, d))
         table[table <= -2] = -2 - table[table <= -2]
         self.stack = sorted(np.flatnonzero(~self.held).tolist(), reverse=True)
