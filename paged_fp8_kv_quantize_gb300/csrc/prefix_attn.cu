@@ -238,16 +238,17 @@ __global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(const PrefixA
   }
   for (int i = lane; i < n_own * a.d.st_groups; i += 32) st |= a.d.part_st[(size_t)c0 * a.d.st_groups + i];
   // the pieces' maxima, then their weights
-  float mx = kNegInf;
-  for (int i = lane; i < n; i += 32) {
-    const float2 ml = i < n_own ? a.d.part_ml[(size_t)(c0 + i) * a.d.Hq + hq] : a.ml[pre_row(i - n_own)];
-    mx = fmaxf(mx, ml.x);
-  }
+  auto ml_of = [&](int i) {
+    return i < n_own ? a.d.part_ml[(size_t)(c0 + i) * a.d.Hq + hq] : a.ml[pre_row(i - n_own)];
+  };
+  const float2 ml0 = lane < n ? ml_of(lane) : make_float2(kNegInf, 0.f);  // the first 32 stay in registers
+  float mx = ml0.x;
+  for (int i = lane + 32; i < n; i += 32) mx = fmaxf(mx, ml_of(i).x);
   for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
   st = __reduce_or_sync(0xffffffffu, st);
   float W = 0.f;
   for (int i = lane; i < n; i += 32) {
-    const float2 ml = i < n_own ? a.d.part_ml[(size_t)(c0 + i) * a.d.Hq + hq] : a.ml[pre_row(i - n_own)];
+    const float2 ml = i < 32 ? ml0 : ml_of(i);
     const float w = fast_exp2(ml.x - mx);
     W += w * ml.y;
     if (w0 == 0) sw[i] = w;
