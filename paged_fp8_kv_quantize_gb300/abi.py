@@ -381,7 +381,7 @@ def paged_decode_attention_prefix(cache, q, seq_lens, block_table, block_tags, p
     if kind is None:
         raise ValueError(f"out must be torch.float32 or torch.bfloat16, got {out.dtype}")
     if status is None:
-        status = seq_lens.new_empty(B)
+        status = torch.empty(B, dtype=torch.int32, device=q.device)
     bf16, rows, dev = torch.bfloat16, B * cache.H * cache.D, torch.cuda.current_device()
     rc = _prefix(
         cache._ref(dev), _arg(k_new, "k_new", rows, dev, bf16), _arg(v_new, "v_new", rows, dev, bf16),
@@ -451,7 +451,7 @@ def page_copy(cache: PagedCache, src_pages, dst_pages, slots=None, page_status=N
     """Copy pages src_pages[i] to dst_pages[i] of the same cache, the first slots[i] slots of each (None: all)."""
     n, dev = src_pages.numel(), torch.cuda.current_device()
     if page_status is None:
-        page_status = src_pages.new_empty(n)
+        page_status = torch.empty(n, dtype=torch.int32, device=src_pages.device)
     rc = _page_copy(cache._ref(dev), _arg(src_pages, "src_pages", n, dev), _arg(dst_pages, "dst_pages", n, dev),
                     _arg(slots, "slots", n, dev), n, _arg(page_status, "page_status", n, dev),
                     _current_stream(dev))
@@ -519,7 +519,7 @@ class PageAllocator:
         n, dev = parents.numel(), torch.cuda.current_device()
         B, MP = block_table.shape
         if fork_status is None:
-            fork_status = parents.new_empty(n)
+                fork_status = torch.empty(n, dtype=torch.int32, device=parents.device)
         rc = _page_fork(
             self.state.data_ptr(), _arg(cache.page_tags, "page_tags", cache.P, dev),
             _arg(self.refs, "refs", self.num_pages, dev), cache._ref(dev), _arg(parents, "parents", n, dev),
@@ -534,7 +534,7 @@ class PageAllocator:
         """Take one holder off each listed page; a page returns to the free list with its last (pfkv_page_release)."""
         n, dev = pages.numel(), torch.cuda.current_device()
         if page_status is None:
-            page_status = pages.new_empty(n)
+            page_status = torch.empty(n, dtype=torch.int32, device=pages.device)
         rc = _page_release(self.state.data_ptr(), _arg(self.refs, "refs", self.num_pages, dev),
                            _arg(pages, "pages", n, dev), n, _arg(page_status, "page_status", n, dev),
                            _current_stream(dev))
@@ -549,7 +549,7 @@ class PageAllocator:
         B, MP = block_table.shape
         room = self.num_pages // 2  # no pool needs more moves
         m, dev = room if max_moves is None else min(int(max_moves), room), torch.cuda.current_device()
-        src, dst, n_moved = block_table.new_empty(2 * max(m, 0) + 1).split((max(m, 0), max(m, 0), 1))
+        src, dst, n_moved = torch.empty(2 * max(m, 0) + 1, dtype=torch.int32, device=block_table.device).split((max(m, 0), max(m, 0), 1))
         rc = _page_compact(
             self.state.data_ptr(), _arg(cache.page_tags, "page_tags", cache.P, dev),
             _arg(self.refs, "refs", self.num_pages, dev), cache._ref(dev),
