@@ -158,15 +158,15 @@ __device__ __forceinline__ void regs_dec() {
 // and V; 1: V): lane g takes 16 tokens' codes, which are contiguous.
 template <typename C, int kD>
 __device__ __forceinline__ bool stage_codes(const PrefixArgs &a, uint8_t *smem, const PBars &B, const PTile &d,
-                                            uint32_t i, int part, bool per_token, bool live, uint64_t policy,
+                                            uint32_t rows, uint32_t i, int part, bool per_token, bool lead, uint64_t policy,
                                             volatile int *abort) {
   const int lane = threadIdx.x & 31;
   const uint32_t s = i % C::kStage;
   if (!mbar_wait_warp(&B.code_empty[s], ((i / C::kStage) & 1u) ^ 1u, abort)) return false;
   const uint32_t each = 16 * kD + (per_token && part == 0 ? 128 : 0);
-  if (lane == 0 && live) mbar_arrive_expect_tx(&B.code_full[s], each * (uint32_t)__popc(d.rows));
+  if (lead) mbar_arrive_expect_tx(&B.code_full[s], each * (uint32_t)__popc(rows));
   __syncwarp();
-  if (lane < 8 && (d.rows >> lane & 1u)) {
+  if (rows >> lane & 1u) {
     const long long row = d.row[lane];
     const uint8_t *pool = static_cast<const uint8_t *>(part ? a.d.v_pool : a.d.k_pool);
     bulk_load_stream(smem + C::kOffCode + s * C::kCodeBytes + lane * 16 * kD, pool + row * kD, 16 * kD,
@@ -185,11 +185,11 @@ __device__ __forceinline__ bool stage_codes(const PrefixArgs &a, uint8_t *smem, 
 // the copy's fill value: a page past the pool's last reads as zeros.
 template <typename C, int kD>
 __device__ __forceinline__ bool copy_tile(const CUtensorMap &map, uint8_t *smem, const PBars &B, uint32_t i, int page,
-                                          int slot, int h, bool live, uint64_t policy, volatile int *abort) {
+                                          int slot, int h, bool live, bool lead, uint64_t policy, volatile int *abort) {
   const int lane = threadIdx.x & 31;
   const uint32_t s = i % C::kSlots;
   if (!mbar_wait_warp(&B.empty[s], ((i / C::kSlots) & 1u) ^ 1u, abort)) return false;
-  if (lane == 0 && live) mbar_arrive_expect_tx(&B.full[s], C::kTBytes);
+  if (lead) mbar_arrive_expect_tx(&B.full[s], C::kTBytes);
   __syncwarp();
   if (lane < kD / 8 && live)
     tma_load_4d_stream(smem + C::kOffT + s * C::kTBytes + (lane >> 3) * C::kBlk + (lane & 7) * 16 * 128, &map,
@@ -214,22 +214,22 @@ __device__ __forceinline__ void plan_tiles(const PrefixArgs &a, const CUtensorMa
   PItem first{};
   PWalk w{};
   uint32_t n = 0;
-  bool ok = true, live = false;
+  bool ok = true, live = false, lead = false;  // lead: lane 0 of a live warp
   for (uint32_t i = 0; ok;) {
     PItem it{};
     if (i == 0) it = first;
     bool have = true;
     if (live) have = i == 0 ? it.n_rows != 0 : walk_next(a, a.groups, w, it);
     if (!mbar_wait_warp(&B.item_empty[i % kItemSlots], ((i / kItemSlots) & 1u) ^ 1u, abort)) break;
-    if (lane == 0 && live) {
+    if (lead) {
       items[i % kItemSlots] = it;
       mbar_arrive(&B.item_full[i % kItemSlots]);
     }
-    const int n_tok = !live || !have ? 1 : (it.p1 - it.p0) * S;
+    const int n_look = live && have ? (it.p1 - it.p0) * S : 0, n_tok = max(n_look, 1);
     const int *trow = have ? a.d.block_table + (size_t)it.lead * a.d.MP + it.p0 : nullptr;
     auto look_up = [&](int t0) -> int {
       const int tok = t0 + 16 * lane;
-      return have && live && tok < n_tok ? __ldg(trow + tok / S) : -1;
+      return tok < n_look ? __ldg(trow + tok / S) : -1;
     };
     int next = look_up(0);
     for (int t0 = 0; t0 < n_tok && ok; t0 += kAtOnce * kTok) {
@@ -244,8 +244,8 @@ __device__ __forceinline__ void plan_tiles(const PrefixArgs &a, const CUtensorMa
           const int page = __shfl_sync(0xffffffffu, fine ? p : a.d.P, g), slot = (t0 + 16 * g) % S;
           // test hook: the first CTA never gets its first tile, and the other warps' bounded waits give up
           if (live && (a.d.flags & PFKV_FLAG_TEST_WITHHOLD) && blockIdx.x == 0 && n == 0) return;
-          ok = copy_tile<C, kD>(map_k, smem, B, 2 * n, page, slot, it.h, live, policy, abort);
-          ok = ok && copy_tile<C, kD>(map_v, smem, B, 2 * n + 1, page, slot, it.h, live, policy, abort);
+          ok = copy_tile<C, kD>(map_k, smem, B, 2 * n, page, slot, it.h, live, lead, policy, abort);
+          ok = ok && copy_tile<C, kD>(map_v, smem, B, 2 * n + 1, page, slot, it.h, live, lead, policy, abort);
           if (!ok) break;
           continue;
         }
@@ -254,15 +254,16 @@ __device__ __forceinline__ void plan_tiles(const PrefixArgs &a, const CUtensorMa
         if (!ok) break;
         if (lane / kGroups == k)
           d.row[lane % kGroups] = fine ? ((long long)p * H + it.h) * S + (t0 + 16 * lane) % S : -1;
+        const uint32_t mine = rows >> (kGroups * k) & ((1u << kGroups) - 1u);
         if (lane == 0) {
           d.kind = !have ? 0 : t0 + k == 0 ? 2 : 1;
-          d.rows = rows >> (kGroups * k) & ((1u << kGroups) - 1u);
+          d.rows = mine;
         }
         __syncwarp();
-        if (lane == 0 && live) mbar_arrive(&B.tile_full[n % kTileSlots]);
+        if (lead) mbar_arrive(&B.tile_full[n % kTileSlots]);
         if constexpr (kFp8) {
           for (int part = 0; part < 2 && have && ok; ++part)
-            ok = stage_codes<C, kD>(a, smem, B, d, 2 * n + part, part, per_token, live, policy, abort);
+            ok = stage_codes<C, kD>(a, smem, B, d, mine, 2 * n + part, part, per_token, lead, policy, abort);
         }
         if (!ok) break;
       }
@@ -279,6 +280,7 @@ __device__ __forceinline__ void plan_tiles(const PrefixArgs &a, const CUtensorMa
     first = r.item;
     w = PWalk{r.u, r.u1, (int)blockIdx.x};
     live = true;
+    lead = lane == 0;
     n = 0;
   }
   // a wait gave up: copies in flight land before the block may exit (waits of copies that were never issued, or that
