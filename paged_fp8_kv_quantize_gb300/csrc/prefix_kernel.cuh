@@ -89,9 +89,9 @@ struct PCfg {
   // reference moves when a weight would pass 2^kGrow.  f16: weights up to
   // 2^14, times V scales of at most twice their reference, stay below 65504,
   // and steps are 2^-24 at least, so a weight is off by 2^-25-kLead of the
-  // largest; bf16 has the range of fp32.  A lead costs moves: 1.76 -> 1.82 us
-  // per tile from 2^-4 to 2^0 with one term, 2.42 -> 2.64 from 2^0 to 2^10 with
-  // two.  Under a first token that takes 2^13 times a later one's weight (1024
+  // largest; bf16 has the range of fp32.  A lead costs moves: 0.06 us a tile
+  // (of 1.8) from 2^-4 to 2^0 with one term, up to 0.2 (of 2.4) from 2^0 to 2^10
+  // with two.  Under a first token that takes 2^13 times a later one's weight (1024
   // tokens), the smallest lead put outputs off by 2e-2 and 5e-4 of sum p |v|;
   // these leave 2^-8, a bf16 output's rounding, and 3e-6.
   static constexpr float kLead = kFp8 && kTerms == 2 ? 10.f : 0.f, kGrow = kFp8 ? 14.f : 60.f;
