@@ -357,7 +357,7 @@ int pfkv_handoff_bf16_to_fp8(const pfkv_cache *src, const pfkv_cache *dst, const
  *   followed by per-page bookkeeping (a held flag and a scratch word).
  * A fresh state hands out pages in increasing id order; freed pages are
  * reused last-in first-out.  Calls on one state must be ordered (one stream,
- * or events): each call is one kernel that owns the state while it runs.
+ * or events): each call owns the state while it runs.
  * Lists are processed as if in order (first occurrence wins); results are
  * deterministic.
  */
@@ -395,7 +395,9 @@ int pfkv_page_realloc(void *state, uint32_t *page_tags, const int32_t *pages, in
  * pool whose pages are shared gives pages back with pfkv_page_release:
  * pfkv_page_free and pfkv_page_realloc take a page away from every holder at
  * once (their mappings then fail the tag check when the page is handed on)
- * and leave page_refs as it is.
+ * and leave page_refs as it is: the caller zeroes a shared page's entry.
+ * A page with several holders is read only: a request that goes back into
+ * one before it appends forks itself first (pfkv_page_fork copies the page).
  */
 
 /* page_copy -- copies pages of a cache to other pages of the same cache: the
