@@ -50,7 +50,6 @@ namespace pfkv {
 namespace {
 
 constexpr int kPThreads = 16 * 32;  // four warpgroups
-constexpr int kScaleSlots = 4;   // tiles whose per-token scales are kept
 constexpr int kItemSlots = 4;    // items announced ahead
 constexpr int kTileSlots = 8;    // tiles announced ahead
 // Registers a thread after the launch's 128: two softmax warpgroups, the
@@ -75,8 +74,13 @@ constexpr int kTok = 128;  // tokens per tile
 template <bool kFp8, int kD, int kTerms>
 struct PCfg {
   static constexpr int kBufs = kTerms == 3 && kD == 128 ? 1 : 2;  // score buffers per half (tensor memory bounds it)
-  static constexpr int kSlots = kFp8 && kD == 128 ? 3 : 4;        // operand ring: K, V, K, V, ...
-  static constexpr int kStage = kFp8 ? 3 : 0;                     // staged code tiles
+  // Rings as deep as shared memory allows.  (D 64 with 4 and 3 slots: two requests behind 65536 BF16 tokens 54.5 us
+  // against 51.2, 64 behind FP8 ones with per-token scales 231 against 223; other FP8 calls the same.)
+  static constexpr int kSlots = kD == 64 ? (kFp8 ? 6 : 8) : kFp8 ? 3 : 4;  // operand ring: K, V, K, V, ...
+  static constexpr int kStage = !kFp8 ? 0 : kD == 64 ? 8 : 3;     // staged code tiles
+  // Tiles whose per-token scales are kept: K's slot of tile n is free again when a product with the tile kSlots / 2
+  // before it is done, which the softmax of the tile two before that precedes.
+  static constexpr int kScaleSlots = kD == 64 ? 8 : 4;
   static constexpr uint32_t kBlk = 128 * 128;                     // 64 dims of a query half or of a tile
   static constexpr uint32_t kQBytes = kBlk * (kD / 64), kTBytes = kQBytes;
   static constexpr uint32_t kCodeBytes = kTok * kD;
@@ -98,15 +102,15 @@ struct PCfg {
   static constexpr uint32_t kOffQ = 0, kOffT = 2 * kQBytes, kOffCode = kOffT + kSlots * kTBytes;
   static constexpr uint32_t kOffCodeScale = kOffCode + kStage * kCodeBytes;  // K and V scales beside the codes of K
   static constexpr uint32_t kOffScale = kOffCodeScale + kStage * 2 * kTok * 4;
-  static constexpr uint32_t kOffBars = kOffScale + kScaleSlots * (2 * kTok * 4 + 16);
-  static constexpr uint32_t kOffItems = kOffBars + 8 * 64;
+  static constexpr uint32_t kOffBars = kOffScale + (kFp8 ? kScaleSlots : 0) * (2 * kTok * 4 + 16);
+  static constexpr uint32_t kOffItems = kOffBars + 8 * 96;
   static constexpr uint32_t kTotal = kOffItems + kItemSlots * sizeof(PItem) + kTileSlots * sizeof(PTile) + 1024;
   static constexpr uint32_t kIdQK = umma_idesc_f16(128, 64, !kFp8, 0, 0);
   static constexpr uint32_t kIdPV = umma_idesc_f16(128, kD, !kFp8, 0, 1);
   static_assert(kTotal <= 232448, "shared memory plan exceeds one SM");
 };
 
-constexpr int kMaxSlots = 4;
+constexpr int kMaxSlots = 8;
 struct PBars {
   uint64_t *full, *empty;              // operand ring
   uint64_t *code_full, *code_empty;    // staging ring
@@ -129,7 +133,7 @@ __device__ __forceinline__ PBars pbars_at(uint8_t *base) {
   r.s_full = b; b += 4;
   r.p_full = b; b += 4;
   r.pv_done = b; b += 4;
-  r.sc_full = b; b += kScaleSlots;
+  r.sc_full = b; b += kMaxSlots;
   r.item_full = b; b += kItemSlots;
   r.item_empty = b; b += kItemSlots;
   r.tile_full = b; b += kTileSlots;
@@ -355,7 +359,7 @@ __device__ __forceinline__ void find_pieces(const PrefixArgs &a, const PrefixHdr
 template <typename C>
 __device__ __forceinline__ void hand_scales(uint8_t *smem, const PBars &B, uint32_t n, uint32_t stage, uint32_t rows,
                                             float &vref, int t) {
-  float *dst = reinterpret_cast<float *>(smem + C::kOffScale) + (n % kScaleSlots) * (2 * kTok + 4);
+  float *dst = reinterpret_cast<float *>(smem + C::kOffScale) + (n % C::kScaleSlots) * (2 * kTok + 4);
   const float *src = reinterpret_cast<const float *>(smem + C::kOffCodeScale) + stage * 2 * kTok;
   const int lane = t & 31, warp = t >> 5;
   float mx = 0.f, mine = 0.f;
@@ -372,7 +376,7 @@ __device__ __forceinline__ void hand_scales(uint8_t *smem, const PBars &B, uint3
   dst[kTok + t] = vref > 0.f ? mine / vref : 0.f;
   if (t == 0) dst[2 * kTok] = vref;
   __syncwarp();
-  if (lane == 0) mbar_arrive(&B.sc_full[n % kScaleSlots]);
+  if (lane == 0) mbar_arrive(&B.sc_full[n % C::kScaleSlots]);
 }
 
 // FP8: staged codes to f16 operands.  A thread takes 16 codes of a row at a
@@ -638,11 +642,11 @@ __device__ __forceinline__ void softmax_rows(const PrefixArgs &a, uint8_t *smem,
       const int valid = n_tok - tok;
       const uint32_t buf = u % C::kBufs, col = tq + C::col_s(t, 0) + 64 * buf, n = tile0 + (uint32_t)tok / kTok;
       const float *sc = reinterpret_cast<const float *>(smem + C::kOffScale) +
-                        (n % kScaleSlots) * (2 * kTok + 4) + (tok & 64);
+                        (n % C::kScaleSlots) * (2 * kTok + 4) + (tok & 64);
       if (!mbar_wait_warp(&B.s_full[2 * t + buf], (u / C::kBufs) & 1u, abort)) return;
       float moved = 1.f;
       if (per_token) {
-        if (!mbar_wait_warp(&B.sc_full[n % kScaleSlots], (n / kScaleSlots) & 1u, abort)) return;
+        if (!mbar_wait_warp(&B.sc_full[n % C::kScaleSlots], (n / C::kScaleSlots) & 1u, abort)) return;
         const float now = sc[2 * kTok - (tok & 64)];  // against the reference this half last used
         if (!first && now != vref) moved = vref / now;
         vref = now;
@@ -803,7 +807,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
       mbar_init(&B.p_full[i], 4);
       mbar_init(&B.pv_done[i], 1);
     }
-    for (int i = 0; i < kScaleSlots; ++i) mbar_init(&B.sc_full[i], 4);
+    for (int i = 0; i < kMaxSlots; ++i) mbar_init(&B.sc_full[i], 4);
     for (int i = 0; i < kItemSlots; ++i) {
       mbar_init(&B.item_full[i], 1);
       mbar_init(&B.item_empty[i], 10);  // eight softmax warps and the issuers
