@@ -27,7 +27,7 @@
 //   warp 13         planner: works out the CTA's items and where each tile's
 //                   rows lie (bounds-checked page ids), so that nobody else
 //                   waits for a table entry, and issues the copies: FP8 codes
-//                   into a staging ring of three tiles (48 KB in flight), BF16
+//                   into a staging ring (48 KB in flight and more), BF16
 //                   tiles into the operand ring (64 KB and more).
 //   warp 15         works out where the join finds each row's pieces and
 //                   compares the requests' prefix pages, all CTAs together.
