@@ -106,7 +106,7 @@ struct Piece {
 // take the 32-bit unsigned division; larger ones a bitwise long division.
 // No floating point: double precision is slow on this part (an earlier
 // reciprocal-estimate form in fp64 cost 0.3-0.6 us per call).
-__device__ __forceinline__ unsigned long long div_floor_wide(unsigned long long x, unsigned long long y) {
+__host__ __device__ __forceinline__ unsigned long long div_floor_wide(unsigned long long x, unsigned long long y) {
   unsigned long long q = 0, r = 0;
   for (int i = 63; i >= 0; --i) {
     r = (r << 1) | ((x >> i) & 1ull);
@@ -118,7 +118,7 @@ __device__ __forceinline__ unsigned long long div_floor_wide(unsigned long long 
   return q;
 }
 
-__device__ __noinline__ long long div_floor(long long x, long long y) {
+__host__ __device__ __noinline__ long long div_floor(long long x, long long y) {
   const unsigned long long ux = (unsigned long long)x, uy = (unsigned long long)y;
   if (((ux | uy) >> 32) == 0ull) return (long long)((uint32_t)ux / (uint32_t)uy);
   return (long long)div_floor_wide(ux, uy);

@@ -81,19 +81,33 @@ struct PrefixArgs {
 };
 
 // floor(k T / R): first unit of range k.
-__device__ __forceinline__ long long range_start(const PrefixHdr &h, long long k) { return div_floor(k * h.T, h.R); }
+__host__ __device__ __forceinline__ long long range_start(const PrefixHdr &h, long long k) { return div_floor(k * h.T, h.R); }
 // The range that holds unit u.
-__device__ __forceinline__ int range_of(const PrefixHdr &h, long long u) {
+__host__ __device__ __forceinline__ int range_of(const PrefixHdr &h, long long u) {
   return (int)div_floor((u + 1) * h.R - 1, h.T);
 }
 
-// A group's items of one KV head on the line.
 constexpr int kCostHalf = 4, kCostFull = 7;  // a page's cost: about 1.1 us and 1.8 us per 128 tokens (FP8, D 128)
+
+// Units of an item's set-up and read-out, about what 512 tokens of a small
+// block cost, and units that a range holds at least: 256 such tokens, and one
+// page of any block.  With less than a page a range between an item's first
+// and last one may hold no page's beginning; nobody then writes the slot that
+// row_pieces counts there.
+struct LineUnits {
+  int c0, min_units;
+};
+inline LineUnits line_units(int S) {
+  const int units = kCostHalf * ((256 + S - 1) / S);
+  return {kCostHalf * ((512 + S - 1) / S), units > kCostFull ? units : kCostFull};
+}
+
+// A group's items of one KV head on the line.
 struct HeadLine {
   int blocks, last_rows;       // row blocks, rows of the last one
   long long full, last, head;  // units of a full block, of the last one, of all
 };
-__device__ __forceinline__ HeadLine head_line(int n, int G, int pages, int c0) {
+__host__ __device__ __forceinline__ HeadLine head_line(int n, int G, int pages, int c0) {
   HeadLine l;
   const long long rows = (long long)n * G;
   l.blocks = (int)((rows + kRows - 1) / kRows);
@@ -103,14 +117,30 @@ __device__ __forceinline__ HeadLine head_line(int n, int G, int pages, int c0) {
   l.head = (l.blocks - 1) * l.full + l.last;
   return l;
 }
-__device__ __forceinline__ int page_cost(const HeadLine &l, int blk) {
+__host__ __device__ __forceinline__ int page_cost(const HeadLine &l, int blk) {
   return blk == l.blocks - 1 && l.last_rows <= kRows / 2 ? kCostHalf : kCostFull;
 }
 // Pages of that cost that begin before unit x of an item's pages.
-__device__ __forceinline__ int pages_before(long long x, int cost) {
+__host__ __device__ __forceinline__ int pages_before(long long x, int cost) {
   if (x <= 0) return 0;
   const unsigned long long y = (unsigned long long)x + (unsigned)(cost - 1);
   return (int)(cost == kCostHalf ? y / kCostHalf : y / kCostFull);
+}
+
+// The pieces of query head hq's row of the rank-th request of a group.
+__host__ __device__ __forceinline__ PrefixRow row_pieces(const PrefixHdr &hdr, const PrefixGroup &gr, int G, int c0,
+                                                         int rank, int hq) {
+  const HeadLine line = head_line(gr.n, G, gr.pages, c0);
+  const int h = hq / G, r = rank * G + hq % G, blk = r / kRows;
+  const int item = h * line.blocks + blk, cost = page_cost(line, blk);
+  const long long first = gr.unit0 + h * line.head + blk * line.full + c0;  // unit of its first page
+  const int k0 = range_of(hdr, first);
+  PrefixRow pr;
+  pr.sh = cost == kCostHalf;
+  pr.n = (range_of(hdr, first + (long long)cost * (gr.pages - 1)) - k0 + 1) << pr.sh;
+  pr.slot0 = k0 + gr.item0 + item;
+  pr.row = r - blk * kRows;
+  return pr;
 }
 
 // The pieces of range k from unit u on.
@@ -120,7 +150,7 @@ struct PWalk {
 };
 
 // The next piece with pages.
-__device__ __forceinline__ bool walk_next(const PrefixArgs &a, const PrefixGroup *groups, PWalk &w, PItem &it) {
+__host__ __device__ __forceinline__ bool walk_next(const PrefixArgs &a, const PrefixGroup *groups, PWalk &w, PItem &it) {
   while (w.u < w.u1) {
     int lo = 0, hi = a.n_groups - 1;  // the last group that starts at or before u
     while (lo < hi) {

@@ -356,9 +356,9 @@ int run_prefix(PrefixArgs a, cudaStream_t s) {
     if (dev < 64) attr_set.fetch_or(1ull << dev);
   }
   a.ctas = a.n_groups == 0 ? 0 : num_sms() < kMaxRanges ? num_sms() : kMaxRanges;
-  // an item's set-up and read-out cost about what 512 tokens of a small block do; a range holds 256 of them at least
-  a.c0 = kCostHalf * ((512 + a.d.S - 1) / a.d.S);
-  a.min_units = kCostHalf * ((256 + a.d.S - 1) / a.d.S);
+  const LineUnits units = line_units(a.d.S);
+  a.c0 = units.c0;
+  a.min_units = units.min_units;
   int rc = cuda_ok(launch_dependent(prefix_plan_kernel, dim3((unsigned)a.d.B + 1u), kPlanThreads,
                                     8 * (size_t)a.n_groups, s, a),
                    "prefix plan launch");

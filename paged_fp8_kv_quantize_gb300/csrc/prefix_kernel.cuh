@@ -333,18 +333,8 @@ __device__ __forceinline__ void find_pieces(const PrefixArgs &a, const PrefixHdr
   for (unsigned id = blockIdx.x * 32 + (threadIdx.x & 31); id < all; id += gridDim.x * 32) {
     const int b = (int)(id / (unsigned)a.d.Hq), hq = (int)(id - (unsigned)b * (unsigned)a.d.Hq);
     PrefixRow pr{0, 0, 0, 0};
-    if (!a.pre_st[b] && a.group_of[b] >= 0 && a.skip[b] > 0) {
-      const PrefixGroup gr = a.groups[a.group_of[b]];
-      const HeadLine line = head_line(gr.n, a.G, gr.pages, a.c0);
-      const int h = hq / a.G, r = a.rank[b] * a.G + hq % a.G, blk = r / kRows;
-      const int item = h * line.blocks + blk, cost = page_cost(line, blk);
-      const long long first = gr.unit0 + h * line.head + blk * line.full + a.c0;  // unit of its first page
-      const int k0 = range_of(hdr, first);
-      pr.sh = cost == kCostHalf;
-      pr.n = (range_of(hdr, first + (long long)cost * (gr.pages - 1)) - k0 + 1) << pr.sh;
-      pr.slot0 = k0 + gr.item0 + item;
-      pr.row = r - blk * kRows;
-    }
+    if (!a.pre_st[b] && a.group_of[b] >= 0 && a.skip[b] > 0)
+      pr = row_pieces(hdr, a.groups[a.group_of[b]], a.G, a.c0, a.rank[b], hq);
     a.rows[id] = pr;
   }
 }

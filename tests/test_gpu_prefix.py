@@ -40,6 +40,26 @@ def test_page_sizes(page, pages):
     c.assert_matches(flags=abi.FLAG_TAG_CHECK)
 
 
+@pytest.mark.parametrize("page", [16, 48, 112, 240, 256])
+@pytest.mark.parametrize("members", [3, 36, 75])
+@pytest.mark.parametrize("pages", [2, 9])
+def test_page_sizes_of_larger_groups(page, members, pages):
+    """12, 144 and 300 rows: both halves of an item on their own tokens, on the
+    same ones, and two items.  The workspace holds NaN, so that a partial
+    result that nobody wrote shows."""
+    c = PrefixCase(23, [0] * members, [pages], [1 + 37 * i % (2 * page) for i in range(members)], q_heads=8,
+                   kv_heads=2, dim=64, page=page)
+    ws = torch.full((abi.prefix_workspace_bytes(c.device(), members, 8, 1),), 0xFF, dtype=torch.uint8, device="cuda")
+    c.assert_matches(workspace=ws)
+
+
+def test_few_large_pages_of_many_heads():
+    """Ranges as short as they get, page 256: a group of 256 rows, eight KV heads."""
+    c = PrefixCase(24, [0] * 64, [9], [1 + 5 * i for i in range(64)], q_heads=32, kv_heads=8, dim=64, page=256)
+    ws = torch.full((abi.prefix_workspace_bytes(c.device(), 64, 32, 1),), 0xFF, dtype=torch.uint8, device="cuda")
+    c.assert_matches(workspace=ws)
+
+
 @pytest.mark.parametrize("members", [1, 2, 15, 16, 17, 31, 32, 33, 63, 64, 65, 130])
 def test_row_counts(members):
     """Rows on both sides of the row block's and the instruction's edges."""

@@ -1,11 +1,13 @@
 """CPU-only checks of the shared-prefix decode: refusals before any CUDA call,
 the workspace's size, and the work line restated."""
 import ctypes
+import os
+import subprocess
 
 import numpy as np
 import pytest
 
-from paged_fp8_kv_quantize_gb300 import abi
+from paged_fp8_kv_quantize_gb300 import abi, build
 
 SIZE_MAX = ctypes.c_size_t(-1).value
 
@@ -123,3 +125,42 @@ def test_work_line_covers_every_item_once(seed):
                 assert [x[2] for x in pieces] == list(range(k0, k1 + 1))
                 assert [x[3] for x in pieces] == [k + item0 + h * len(cost) + blk for k in range(k0, k1 + 1)]
     assert not seen and max(slots) < R + items
+
+
+@pytest.fixture(scope="module")
+def line_faults(tmp_path_factory):
+    """prefix_line.cu, built from the kernels' own headers for the host."""
+    here = os.path.dirname(os.path.abspath(__file__))
+    lib = str(tmp_path_factory.mktemp("prefix_line") / "prefix_line.so")
+    subprocess.run([build.nvcc(), *build.ARCH, *build.FLAGS, "-I", build.CSRC, "-shared", "-o", lib,
+                    os.path.join(here, "prefix_line.cu")], check=True)
+    f = ctypes.CDLL(lib).prefix_line_faults
+    f.restype = ctypes.c_longlong
+
+    def call(groups, H, G, S, ctas):
+        n, p = zip(*groups)
+        arr = ctypes.c_int * len(groups)
+        return f(arr(*n), arr(*p), len(groups), H, G, S, ctas)
+
+    return call
+
+
+@pytest.mark.parametrize("page", range(16, 257, 16))
+def test_every_row_finds_its_pieces_on_short_lines(line_faults, page):
+    """One group of few pages, rows on both sides of 128, 256 and 384: ranges
+    are then as short as they get, and each between an item's first and last
+    still has to hold a page's beginning."""
+    bad = [(members, G, H, pages, ctas)
+           for members, G in ((1, 1), (16, 8), (33, 4), (64, 4), (65, 4), (48, 8), (13, 33))
+           for H in (1, 8) for ctas in (148, 152) for pages in (*range(1, 61), 100, 160)
+           if line_faults([(members, pages)], H, G, page, ctas)]
+    assert not bad, (len(bad), bad[:8])
+
+
+def test_every_row_finds_its_pieces_on_mixed_lines(line_faults):
+    rng = np.random.default_rng(61)
+    for _ in range(400):
+        groups = [(int(rng.integers(0, 90)), int(rng.integers(0, 40))) for _ in range(int(rng.integers(1, 9)))]
+        args = (groups, int(rng.choice([1, 2, 8])), int(rng.integers(1, 17)), int(rng.choice(range(16, 257, 16))),
+                int(rng.choice([1, 7, 148, 152, 256])))
+        assert line_faults(*args) == 0, args
