@@ -163,6 +163,7 @@ __global__ void __launch_bounds__(Cfg<kFp8, kD, kG, kNCW>::kThreads, Cfg<kFp8, k
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const bool per_token = kFp8 && a.scale_mode == PFKV_SCALE_PER_TOKEN;
+  constexpr bool kRef = kFp8 && kJoin;
   const SmemPlan sp = smem_plan(a.S, C::kRowBytes, per_token, nst, kNCW, kG, kD);
   uint64_t *full = reinterpret_cast<uint64_t *>(smem + sp.bars_off);
   uint64_t *empty = full + nst;
@@ -465,6 +466,8 @@ __global__ void __launch_bounds__(Cfg<kFp8, kD, kG, kNCW>::kThreads, Cfg<kFp8, k
       }
 
       float m[2] = {kNegInf, kNegInf}, l[2] = {0.f, 0.f};
+      uint32_t vref = 16;  // biased exponent of the V scales' reference (kRef), and what takes a scale to it
+      float vfac = ldexpf(C::kPScale, 127 - 16);
       float o[C::kKsteps][C::kNP][4];
 #pragma unroll
       for (int i = 0; i < C::kKsteps; ++i)
@@ -575,6 +578,38 @@ __global__ void __launch_bounds__(Cfg<kFp8, kD, kG, kNCW>::kThreads, Cfg<kFp8, k
               o[i][nt][0] *= apv0; o[i][nt][1] *= apv1; o[i][nt][2] *= apv0; o[i][nt][3] *= apv1;
             }
         }
+        // ---- per-token V scales, relative to a power of two not below any of them so far, so that weights times
+        // scales stay inside f16 at any magnitude of V; O is rescaled where it moves
+        float vs[2][2] = {{C::kPScale, C::kPScale}, {C::kPScale, C::kPScale}};
+        if (kRef && per_token) {
+          uint32_t e = 0;  // biased exponent of the largest
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            if (!live[t]) continue;
+            const uint32_t svs = smem_base + stg[t] * sp.stage_bytes + 2 * S * C::kRowBytes + 4 * S +
+                                 4 * ((tok_base[t] - (tok_base[t] / S) * S) + gid);
+            vs[t][0] = lds_f32(svs);
+            vs[t][1] = lds_f32(svs + 32);
+            e = max(e, max(__float_as_uint(vs[t][0]) >> 23 & 255u, __float_as_uint(vs[t][1]) >> 23 & 255u));
+          }
+          e = __reduce_max_sync(0xffffffffu, e);
+          if (e > vref) {
+            const uint32_t next = e + 3;  // room for scales that grow
+            const float f = ldexpf(1.f, (int)vref - (int)next);
+#pragma unroll
+            for (int i = 0; i < C::kKsteps; ++i)
+#pragma unroll
+              for (int j = 0; j < C::kNP; ++j)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) o[i][j][k] *= f;
+            vref = next;
+            vfac = ldexpf(C::kPScale, 127 - (int)vref);
+          }
+#pragma unroll
+          for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) vs[t][k] *= vfac;
+        }
         // ---- O^T += V^T P^T, one 16-token k-step per tile
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
@@ -589,7 +624,7 @@ __global__ void __launch_bounds__(Cfg<kFp8, kD, kG, kNCW>::kThreads, Cfg<kFp8, k
             for (int k = 0; k < 4; ++k) pv[k] = __shfl_sync(0xffffffffu, p[t][k], src_lane);
           }
           float vs0 = 1.f, vs1 = 1.f;
-          if (per_token) {
+          if (!kRef && per_token) {
             const uint32_t svs = smem_base + stg[t] * sp.stage_bytes + 2 * S * C::kRowBytes + 4 * S +
                                  4 * ((tok_base[t] - (tok_base[t] / S) * S) + gid);
             vs0 = lds_f32(svs);
@@ -603,7 +638,7 @@ __global__ void __launch_bounds__(Cfg<kFp8, kD, kG, kNCW>::kThreads, Cfg<kFp8, k
             for (int k = 0; k < 4; ++k) {
               const int e = k & 1;
               const int v = 8 * nt + 2 * tq + e;
-              const float pp = pv[k] * C::kPScale * ((k < 2) ? vs0 : vs1);
+              const float pp = kRef ? pv[k] * vs[t][k >> 1] : pv[k] * C::kPScale * ((k < 2) ? vs0 : vs1);
               const float hi = round16<kFp8>(pp);
               const bool lo_part = (kG == 1) ? (e == 1) : (v >= kG);
               val[k] = (v < 2 * kG) ? (lo_part ? pp - hi : hi) : 0.f;
@@ -650,6 +685,8 @@ __global__ void __launch_bounds__(Cfg<kFp8, kD, kG, kNCW>::kThreads, Cfg<kFp8, k
         }
       }
       // ---- per-warp state -> shared memory
+      // (the reference and the weights' scale taken out, each warp having its own)
+      const float wfac = kRef && per_token ? ldexpf(1.f / C::kPScale, (int)vref - 127) : 1.f;
 #pragma unroll
       for (int off = 4; off < 32; off <<= 1) {
         l[0] += __shfl_xor_sync(0xffffffffu, l[0], off);
@@ -683,8 +720,8 @@ __global__ void __launch_bounds__(Cfg<kFp8, kD, kG, kNCW>::kThreads, Cfg<kFp8, k
         for (int e = 0; e < 2; ++e) {
           const int hh = 2 * tq + e;
           if (hh < kG && !(kG == 1 && e == 1)) {
-            sm_o[(warp * kG + hh) * kD + d0] = hv[e];
-            sm_o[(warp * kG + hh) * kD + d0 + 1] = hv[2 + e];
+            sm_o[(warp * kG + hh) * kD + d0] = kRef ? hv[e] * wfac : hv[e];
+            sm_o[(warp * kG + hh) * kD + d0 + 1] = kRef ? hv[2 + e] * wfac : hv[2 + e];
           }
         }
       }
@@ -714,6 +751,7 @@ __global__ void __launch_bounds__(Cfg<kFp8, kD, kG, kNCW>::kThreads, Cfg<kFp8, k
       const uint32_t item_st = (uint32_t)sm_ctl[0];
       float ofac = 1.f;
       if constexpr (kFp8) ofac = (per_token ? 1.f : __ldg(&a.v_scale[hg.kv])) / C::kPScale;
+      if (kRef && per_token) ofac = 1.f;
       float *out_bg = a.out + ((size_t)d.b * a.Hq + hg.first) * kD;  // rows of this (request, head group)
       if (!kJoin && d.nb == 1) {
         // the item covers the whole request: finish it here

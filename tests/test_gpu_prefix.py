@@ -305,6 +305,36 @@ def test_first_token_that_outweighs_the_others(cache, out):
     assert not st.any() and (np.abs(got.float().cpu().numpy() - want) <= tol).all()
 
 
+def weight_floor(c, bits, own_max):
+    """What f16 weights may be off by where they are subnormal: 2^-bits of the
+    largest each, times the token's values, whose scale counts as 2^-18 of the
+    prefix's largest at least; own tokens 2^-36 of their largest scale.  Without the prompt's
+    scores (tau 0) the oracle's magnitude is the mean of |v|."""
+    tau, scale = c.tau, c.ref.v_scale.copy()
+    c.tau = 0.0
+    c.ref.v_scale[:] = np.maximum(scale, scale.max() * 2.0 ** -18)
+    floor = c.want()[2] * c.lens[:, None, None] * 2.0 ** -bits
+    own = c.lens - np.where(c.group >= 0, c.pages[c.group], 0) * c.S
+    c.tau, c.ref.v_scale[:] = tau, scale
+    return floor + own[:, None, None] * 448 * own_max * 2.0 ** -36
+
+
+@pytest.mark.parametrize("out", list(OUT))
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("power", [40, 14, -14, -60])
+def test_values_of_any_magnitude(power, dim, out):
+    """Per-token V scales up to 2^(power - 3): weights times scales stay inside
+    f16's range, in the prefix and in own pages."""
+    c = PrefixCase(25, [0] * 6 + [1] * 5 + [-1], [20, 9], [9 * i + 1 for i in range(12)], q_heads=16, kv_heads=2,
+                   dim=dim, page=16, cache=FP8_TOKEN)
+    c.ref.v_scale[:] = np.ldexp(c.ref.v_scale, power)
+    got, st = c.call(OUT[out])
+    want, _, mag = c.want()
+    tol = c.tolerance(want, mag, OUT[out]) + weight_floor(c, 35 if out == "fp32" else 25, c.ref.v_scale.max()) * (1 + 2.0 ** -8)
+    err = np.abs(got.float().cpu().numpy() - want)
+    assert not st.any() and (err <= tol).all(), (err / tol).max()
+
+
 @pytest.mark.parametrize("cache", [FP8, FP8_TOKEN, BF16])
 @pytest.mark.parametrize("tau", [0.0, -0.2])
 def test_scales_that_are_not_positive(cache, tau):
