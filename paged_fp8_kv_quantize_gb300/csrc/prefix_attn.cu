@@ -343,14 +343,14 @@ int make_tile_map(CUtensorMap *map, const void *pool, const DecodeArgs &d) {
   return r == CUDA_SUCCESS ? PFKV_OK : cuda_fail(cudaErrorInvalidValue, "cuTensorMapEncodeTiled");
 }
 
-template <bool kFp8, int kD, int kTerms>
+template <bool kFp8, int kD, int kTerms, bool kToken>
 int run_prefix(PrefixArgs a, cudaStream_t s) {
   using C = PCfg<kFp8, kD, kTerms>;
   int dev = 0;
   cudaGetDevice(&dev);
   static std::atomic<uint64_t> attr_set{0};  // devices whose shared-memory limit is raised
   if (dev >= 64 || !(attr_set.load() >> dev & 1)) {
-    const cudaError_t e = cudaFuncSetAttribute(prefix_kernel<kFp8, kD, kTerms>,
+    const cudaError_t e = cudaFuncSetAttribute(prefix_kernel<kFp8, kD, kTerms, kToken>,
                                                cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kTotal);
     if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(prefix kernel)");
     if (dev < 64) attr_set.fetch_or(1ull << dev);
@@ -370,7 +370,7 @@ int run_prefix(PrefixArgs a, cudaStream_t s) {
       if (!rc) rc = make_tile_map(&map_v, a.d.v_pool, a.d);
       if (rc) return rc;
     }
-    rc = cuda_ok(launch_dependent(prefix_kernel<kFp8, kD, kTerms>, dim3(a.ctas), kPThreads, C::kTotal, s, map_k, map_v,
+    rc = cuda_ok(launch_dependent(prefix_kernel<kFp8, kD, kTerms, kToken>, dim3(a.ctas), kPThreads, C::kTotal, s, map_k, map_v,
                                   a),
                  "prefix kernel launch");
     if (rc) return rc;
@@ -391,6 +391,18 @@ int run_prefix(PrefixArgs a, cudaStream_t s) {
                  "prefix join launch");
 }
 
+// How many 16-bit terms carry a probability.  FP8 caches (f16 products): one
+// holds 11 bits, below the rounding of a bf16 output; two hold 22.  BF16
+// caches (bf16 products) 8 bits a term: two for a bf16 output, three for fp32.
+template <int kD>
+int dispatch_prefix(const PrefixArgs &a, cudaStream_t s) {
+  if (a.d.dtype != PFKV_DTYPE_FP8_E4M3)
+    return a.out_bf16 ? run_prefix<false, kD, 2, false>(a, s) : run_prefix<false, kD, 3, false>(a, s);
+  if (a.d.scale_mode == PFKV_SCALE_PER_TOKEN)
+    return a.out_bf16 ? run_prefix<true, kD, 1, true>(a, s) : run_prefix<true, kD, 2, true>(a, s);
+  return a.out_bf16 ? run_prefix<true, kD, 1, false>(a, s) : run_prefix<true, kD, 2, false>(a, s);
+}
+
 }  // namespace
 
 size_t prefix_ws_bytes(size_t first, int batch, int q_heads, int kv_heads, int dim, int n_groups) {
@@ -406,9 +418,6 @@ int launch_prefix_decode(const DecodeArgs &d, size_t ws_first, uint8_t *ws, cons
   a.group_pages = group_pages;
   a.n_groups = n_groups;
   a.out_bf16 = out_bf16;
-  // How many 16-bit terms carry a probability.  FP8 caches (f16 products): one
-  // holds 11 bits, below the rounding of a bf16 output; two hold 22.  BF16
-  // caches (bf16 products) 8 bits a term: two for a bf16 output, three for fp32.
   const PrefixLayout L = prefix_layout(ws_first, d.B, d.Hq, d.cache.num_kv_heads, d.D, n_groups);
   a.own_len = reinterpret_cast<int *>(ws + L.own_len);
   a.skip = reinterpret_cast<int *>(ws + L.skip);
@@ -424,13 +433,7 @@ int launch_prefix_decode(const DecodeArgs &d, size_t ws_first, uint8_t *ws, cons
   a.ml = reinterpret_cast<float2 *>(ws + L.ml);
   a.o = reinterpret_cast<float *>(ws + L.o);
   a.d.skip = a.skip;
-  const bool fp8 = d.dtype == PFKV_DTYPE_FP8_E4M3;
-  if (d.D == 128) {
-    if (fp8) return out_bf16 ? run_prefix<true, 128, 1>(a, s) : run_prefix<true, 128, 2>(a, s);
-    return out_bf16 ? run_prefix<false, 128, 2>(a, s) : run_prefix<false, 128, 3>(a, s);
-  }
-  if (fp8) return out_bf16 ? run_prefix<true, 64, 1>(a, s) : run_prefix<true, 64, 2>(a, s);
-  return out_bf16 ? run_prefix<false, 64, 2>(a, s) : run_prefix<false, 64, 3>(a, s);
+  return d.D == 128 ? dispatch_prefix<128>(a, s) : dispatch_prefix<64>(a, s);
 }
 
 }  // namespace pfkv

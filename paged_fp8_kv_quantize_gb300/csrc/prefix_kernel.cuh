@@ -91,7 +91,7 @@ struct PCfg {
   static_assert((kTerms == 3 ? 192 : 128) * kBufs + 2 * kD <= 512, "tensor memory plan");
   // The maximum's weight is 2^kLead when a row's reference is set, and the
   // reference moves when a weight would pass 2^kGrow.  f16: weights up to
-  // 2^14, times V scales of at most twice their reference, stay below 65504,
+  // 2^14, times the rest of a V scale (below 2), stay below 65504,
   // and steps are 2^-24 at least, so a weight is off by 2^-25-kLead of the
   // largest; bf16 has the range of fp32.  A lead costs moves: 0.06 us a tile
   // (of 1.8) from 2^-4 to 2^0 with one term, up to 0.2 (of 2.4) from 2^0 to 2^10
@@ -160,14 +160,14 @@ __device__ __forceinline__ void regs_dec() {
 
 // Bulk copies of one staged tile (part 0: K, with the per-token scales of K
 // and V; 1: V): lane g takes 16 tokens' codes, which are contiguous.
-template <typename C, int kD>
+template <typename C, int kD, bool kToken>
 __device__ __forceinline__ bool stage_codes(const PrefixArgs &a, uint8_t *smem, const PBars &B, const PTile &d,
-                                            uint32_t rows, uint32_t i, int part, bool per_token, bool lead, uint64_t policy,
+                                            uint32_t rows, uint32_t i, int part, bool lead, uint64_t policy,
                                             volatile int *abort) {
   const int lane = threadIdx.x & 31;
   const uint32_t s = i % C::kStage;
   if (!mbar_wait_warp(&B.code_empty[s], ((i / C::kStage) & 1u) ^ 1u, abort)) return false;
-  const uint32_t each = 16 * kD + (per_token && part == 0 ? 128 : 0);
+  const uint32_t each = 16 * kD + (kToken && part == 0 ? 128 : 0);
   if (lead) mbar_arrive_expect_tx(&B.code_full[s], each * (uint32_t)__popc(rows));
   __syncwarp();
   if (rows >> lane & 1u) {
@@ -175,7 +175,7 @@ __device__ __forceinline__ bool stage_codes(const PrefixArgs &a, uint8_t *smem, 
     const uint8_t *pool = static_cast<const uint8_t *>(part ? a.d.v_pool : a.d.k_pool);
     bulk_load_stream(smem + C::kOffCode + s * C::kCodeBytes + lane * 16 * kD, pool + row * kD, 16 * kD,
                      &B.code_full[s], policy);
-    if (per_token && part == 0) {
+    if (kToken && part == 0) {
       float *dst = reinterpret_cast<float *>(smem + C::kOffCodeScale) + s * 2 * kTok + 16 * lane;
       bulk_load_stream(dst, a.d.k_scale + row, 64, &B.code_full[s], policy);
       bulk_load_stream(dst + kTok, a.d.v_scale + row, 64, &B.code_full[s], policy);
@@ -201,14 +201,13 @@ __device__ __forceinline__ bool copy_tile(const CUtensorMap &map, uint8_t *smem,
   return true;
 }
 
-template <bool kFp8, int kD, int kTerms>
+template <bool kFp8, int kD, int kTerms, bool kToken>
 __device__ __forceinline__ void plan_tiles(const PrefixArgs &a, const CUtensorMap &map_k, const CUtensorMap &map_v,
                                            uint8_t *smem, const PBars &B, volatile int *abort) {
   using C = PCfg<kFp8, kD, kTerms>;
   PItem *items = reinterpret_cast<PItem *>(smem + C::kOffItems);
   PTile *tiles = reinterpret_cast<PTile *>(smem + C::kOffItems + kItemSlots * sizeof(PItem));
   const int lane = threadIdx.x & 31, S = a.d.S, H = a.d.cache.num_kv_heads;
-  const bool per_token = kFp8 && a.d.scale_mode == PFKV_SCALE_PER_TOKEN;
   const uint64_t policy = l2_evict_first_policy();
   constexpr int kGroups = kTok / 16, kAtOnce = 32 / kGroups;  // 16-token groups of a tile; tiles per look-up
   // the range's first piece comes from the plan: working it out here, in code that runs once and so out of a cold
@@ -267,7 +266,7 @@ __device__ __forceinline__ void plan_tiles(const PrefixArgs &a, const CUtensorMa
         if (lead) mbar_arrive(&B.tile_full[n % kTileSlots]);
         if constexpr (kFp8) {
           for (int part = 0; part < 2 && have && ok; ++part)
-            ok = stage_codes<C, kD>(a, smem, B, d, mine, 2 * n + part, part, per_token, lead, policy, abort);
+            ok = stage_codes<C, kD, kToken>(a, smem, B, d, mine, 2 * n + part, part, lead, policy, abort);
         }
         if (!ok) break;
       }
@@ -341,37 +340,56 @@ __device__ __forceinline__ void find_pieces(const PrefixArgs &a, const PrefixHdr
 
 // ---------------------------------------------------------------- operands of FP8 caches (warps 8-11)
 
-// Per-token scales of tile n, from beside its staged K codes: K scales as they
-// are, V scales relative to a running reference vref, which moves when a
-// tile's largest scale exceeds twice it.  Every operand warp reads all of the
-// tile's V scales for their maximum, so that the warps need not meet, and
-// writes its own 32 tokens'.
+// Per-token scales of tile n, from beside its staged K codes.  K scales go to
+// the softmax as they are.  A V scale is parted: a weight times the whole scale
+// would leave f16's normal range wherever one token's scale is far above the
+// others' (the scale of an all-zero row is 1), so its power of two goes into
+// the token's V operand, as far as f16 holds every code exactly there
+// (2^-14 .. 2^7), and the weight takes the rest, [1, 2) for scales within 2^18 of
+// the largest:
+//   scale = rest 2^shift 2^(ref - 134),  shift = clamp(e - ref + 7),
+// with e a scale's biased exponent and ref a reference that starts 3 above the
+// largest e of a tile and moves when one exceeds it (O is then rescaled).
+// (A bf16 output behind an all-zero row, scale 1, among rows of 1e-3 at most
+// was off by 2.9e-2 of its norm with the whole scale on the weight.)
+// Every operand warp reads all of the tile's V scales for their maximum, so
+// that the warps need not meet, and writes its own 32 tokens'.  shifts: byte i
+// of lane r is shift + 15 of token 32 i + r.
+constexpr int kRefSpare = 3, kRefLeast = 8;  // the least reference keeps 2^(ref - 134) a normal number
 template <typename C>
 __device__ __forceinline__ void hand_scales(uint8_t *smem, const PBars &B, uint32_t n, uint32_t stage, uint32_t rows,
-                                            float &vref, int t) {
+                                            int &ref, uint32_t &shifts, int t) {
   float *dst = reinterpret_cast<float *>(smem + C::kOffScale) + (n % C::kScaleSlots) * (2 * kTok + 4);
   const float *src = reinterpret_cast<const float *>(smem + C::kOffCodeScale) + stage * 2 * kTok;
   const int lane = t & 31, warp = t >> 5;
-  float mx = 0.f, mine = 0.f;
+  int e[kTok / 32], most = 0;
+  float mine = 0.f;
 #pragma unroll
   for (int i = 0; i < kTok / 32; ++i) {
     const int r = 32 * i + lane;
     const float v = rows >> (r >> 4) & 1u ? src[kTok + r] : 0.f;
-    mx = fmaxf(mx, v);
+    e[i] = (int)(__float_as_uint(v) >> 23 & 255u);
+    most = max(most, e[i]);
     if (i == warp) mine = v;
   }
-  mx = warp_max_f32(mx);
-  if (mx > 2.f * vref) vref = mx;
+  most = __reduce_max_sync(0xffffffffu, most);
+  if (most > ref) ref = most + kRefSpare;
+  shifts = 0u;
+#pragma unroll
+  for (int i = 0; i < kTok / 32; ++i) shifts |= (uint32_t)min(max(e[i] - ref + 22, 1), 22) << (8 * i);
   dst[t] = rows >> (t >> 4) & 1u ? src[t] : 0.f;
-  dst[kTok + t] = vref > 0.f ? mine / vref : 0.f;
-  if (t == 0) dst[2 * kTok] = vref;
+  // by 2^(134 - ref - shift) as two factors, either of which is a normal number
+  const int by = 149 - ref - (int)(shifts >> (8 * warp) & 255u), half = by >> 1;
+  auto pow2 = [](int k) { return __uint_as_float((uint32_t)(k + 127) << 23); };
+  dst[kTok + t] = mine * pow2(half) * pow2(by - half);
+  if (t == 0) dst[2 * kTok] = pow2(ref - 134);
   __syncwarp();
   if (lane == 0) mbar_arrive(&B.sc_full[n % C::kScaleSlots]);
 }
 
 // FP8: staged codes to f16 operands.  A thread takes 16 codes of a row at a
 // time (8 lanes a row of 128, 4 of 64).
-template <bool kFp8, int kD, int kTerms>
+template <bool kFp8, int kD, int kTerms, bool kToken>
 __device__ __forceinline__ void loader_fp8(const PrefixArgs &a, uint8_t *smem, const PBars &B, volatile int *abort) {
   using C = PCfg<kFp8, kD, kTerms>;
   constexpr int kLanes = kD / 16;                  // lanes a row
@@ -383,16 +401,16 @@ __device__ __forceinline__ void loader_fp8(const PrefixArgs &a, uint8_t *smem, c
   // D 128: the second half of a row goes with the first half of its neighbour, so that eight lanes' stores, which
   // the swizzle places by row and 16-byte chunk, meet different banks
   const int r_it = (t / kLanes) ^ (kD == 128 ? c >> 2 : 0);
-  const bool per_token = a.d.scale_mode == PFKV_SCALE_PER_TOKEN;
   const uint32_t s_ring = smem_addr(smem + C::kOffT), s_code = smem_addr(smem + C::kOffCode) + r_it * kD + 16 * c;
   const bool withhold = (a.d.flags & PFKV_FLAG_TEST_WITHHOLD) && blockIdx.x == 0;
-  float vref = 0.f;
+  int ref = kRefLeast;
+  uint32_t shifts = 0u;
   for (uint32_t n = 0;; ++n) {
     if (!mbar_wait_warp(&B.tile_full[n % kTileSlots], (n / kTileSlots) & 1u, abort)) return;
     const int kind = tiles[n % kTileSlots].kind;
     const uint32_t rows = tiles[n % kTileSlots].rows;
     if (kind == 0) return;
-    if (kind == 2) vref = 0.f;
+    if (kind == 2) ref = kRefLeast;
 #pragma unroll 1
     for (int part = 0; part < 2; ++part) {
       const uint32_t i = 2 * n + part, st = i % C::kStage, slot = i % C::kSlots;
@@ -406,10 +424,13 @@ __device__ __forceinline__ void loader_fp8(const PrefixArgs &a, uint8_t *smem, c
         if (rows != 0xffu && !(rows >> (r >> 4) & 1u)) x[k] = make_uint4(0u, 0u, 0u, 0u);
       }
       if (!mbar_wait_warp(&B.empty[slot], ((i / C::kSlots) & 1u) ^ 1u, abort)) return;
-      if (per_token && part == 0) hand_scales<C>(smem, B, n, st, rows, vref, t);
+      if (kToken && part == 0) hand_scales<C>(smem, B, n, st, rows, ref, shifts, t);
       __syncwarp();
       if (lane == 0) mbar_arrive(&B.code_empty[st]);
       const uint32_t base = s_ring + slot * C::kTBytes;
+      // K as it is.  One code for both parts: a second copy of this loop cost more (instruction cache; document step
+      // with bf16 output 133 us against 128) than the products by 1.
+      const uint32_t by = part ? shifts : 0x0f0f0f0fu;
 #pragma unroll
       for (int k = 0; k < kIt; ++k) {
         const int r = k * kRowsIt + r_it;
@@ -418,6 +439,12 @@ __device__ __forceinline__ void loader_fp8(const PrefixArgs &a, uint8_t *smem, c
         e4m3x4_to_f16x4(x[k].y, lo.z, lo.w);
         e4m3x4_to_f16x4(x[k].z, hi.x, hi.y);
         e4m3x4_to_f16x4(x[k].w, hi.z, hi.w);
+        if constexpr (kToken) {
+          const uint32_t s4 = __shfl_sync(0xffffffffu, by, r & 31);
+          const uint32_t f = (s4 >> (8 * (k * kRowsIt / 32)) & 255u) * 0x04000400u;  // 2^shift, twice; exact products
+          lo.x = mul_f16x2(lo.x, f); lo.y = mul_f16x2(lo.y, f); lo.z = mul_f16x2(lo.z, f); lo.w = mul_f16x2(lo.w, f);
+          hi.x = mul_f16x2(hi.x, f); hi.y = mul_f16x2(hi.y, f); hi.z = mul_f16x2(hi.z, f); hi.w = mul_f16x2(hi.w, f);
+        }
         const uint32_t row = base + (c >> 2) * C::kBlk + r * 128;  // 16-byte chunks 2c and 2c + 1 of the row
         sts128(row + ((((2 * c) & 7) ^ (r & 7)) << 4), lo);
         sts128(row + ((((2 * c + 1) & 7) ^ (r & 7)) << 4), hi);
@@ -558,13 +585,12 @@ __device__ __forceinline__ void issue_half(const PrefixArgs &a, uint8_t *smem, c
 
 // ---------------------------------------------------------------- softmax (warps 0-7)
 
-template <bool kFp8, int kD, int kTerms>
+template <bool kFp8, int kD, int kTerms, bool kToken>
 __device__ __forceinline__ void softmax_rows(const PrefixArgs &a, uint8_t *smem, const PBars &B, uint32_t tmem,
                                              volatile int *abort) {
   using C = PCfg<kFp8, kD, kTerms>;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int t = warp >> 2, r = (warp & 3) * 32 + lane;  // half, row of it
-  const bool per_token = kFp8 && a.d.scale_mode == PFKV_SCALE_PER_TOKEN;
   const uint32_t tq = tmem + ((uint32_t)((warp & 3) * 32) << 16), col_o = tq + C::col_o(t);
   const int S = a.d.S;
   uint32_t tile0 = 0, u = 0;  // tiles before this item, this half's units so far
@@ -580,7 +606,7 @@ __device__ __forceinline__ void softmax_rows(const PrefixArgs &a, uint8_t *smem,
     // this thread's query row into the operand; f16: scaled by 2^e into [2^14, 2^15), exact; the sign of the
     // factor that turns products into scores goes with it, so that the largest product is the largest score
     float mult = a.d.sm_scale_log2;
-    if (kFp8 && !per_token) mult *= a.d.k_scale[it.h];
+    if (kFp8 && !kToken) mult *= a.d.k_scale[it.h];
     // (the half's last QK^T of the item before has read the operand)
     if (items > 0 && !mbar_wait_warp(&B.q_read[t], (items - 1) & 1u, abort)) return;
     {
@@ -635,7 +661,7 @@ __device__ __forceinline__ void softmax_rows(const PrefixArgs &a, uint8_t *smem,
                         (n % C::kScaleSlots) * (2 * kTok + 4) + (tok & 64);
       if (!mbar_wait_warp(&B.s_full[2 * t + buf], (u / C::kBufs) & 1u, abort)) return;
       float moved = 1.f;
-      if (per_token) {
+      if (kToken) {
         if (!mbar_wait_warp(&B.sc_full[n % C::kScaleSlots], (n / C::kScaleSlots) & 1u, abort)) return;
         const float now = sc[2 * kTok - (tok & 64)];  // against the reference this half last used
         if (!first && now != vref) moved = vref / now;
@@ -644,7 +670,7 @@ __device__ __forceinline__ void softmax_rows(const PrefixArgs &a, uint8_t *smem,
       tc_fence_after();
       uint32_t z[64];
       tmem_ld64(col, z);
-      if (per_token) {
+      if (kToken) {
 #pragma unroll
         for (int j = 0; j < 64; j += 4) {
           const ulonglong2 k4 = *reinterpret_cast<const ulonglong2 *>(sc + j);
@@ -708,7 +734,7 @@ __device__ __forceinline__ void softmax_rows(const PrefixArgs &a, uint8_t *smem,
             p1 = fast_exp2(p1);
             p = f32x2(p0, p1);
             sum = add_f32x2(sum, p);
-            if (per_token) p = mul_f32x2(p, reinterpret_cast<const uint64_t *>(sc + kTok)[j / 2]);
+            if (kToken) p = mul_f32x2(p, reinterpret_cast<const uint64_t *>(sc + kTok)[j / 2]);
           }
           f32x2_split(p, p0, p1);
           pk[j / 2] = kFp8 ? pack_f16x2(p0, p1) : pack_bf16x2(p0, p1);
@@ -743,7 +769,7 @@ __device__ __forceinline__ void softmax_rows(const PrefixArgs &a, uint8_t *smem,
       if (!mbar_wait_warp(&B.pv_done[2 * t + (u - 1) % C::kBufs], ((u - 1) / C::kBufs) & 1u, abort)) return;
       tc_fence_after();
     }
-    const float fac = !kFp8 ? 1.f : per_token ? vref : a.d.v_scale[it.h];
+    const float fac = !kFp8 ? 1.f : kToken ? vref : a.d.v_scale[it.h];
     const size_t at = (size_t)it.slot * kRows + t * (kRows / 2) + r;
 #pragma unroll 1
     for (int i = 0; i < kD / 32; ++i) {
@@ -769,7 +795,7 @@ __device__ __forceinline__ void softmax_rows(const PrefixArgs &a, uint8_t *smem,
   }
 }
 
-template <bool kFp8, int kD, int kTerms>
+template <bool kFp8, int kD, int kTerms, bool kToken>
 __global__ void __launch_bounds__(kPThreads, 1)
     prefix_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                   const PrefixArgs a) {
@@ -817,7 +843,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
   volatile int *abort = &s_abort;
   if (warp >= 12) regs_dec<kRegsRest>();
   if (warp == 13) {
-    plan_tiles<kFp8, kD, kTerms>(a, map_k, map_v, smem, B, abort);
+    plan_tiles<kFp8, kD, kTerms, kToken>(a, map_k, map_v, smem, B, abort);
   } else {
     pdl_wait();
     pdl_launch_dependents();
@@ -825,10 +851,10 @@ __global__ void __launch_bounds__(kPThreads, 1)
     if ((int)blockIdx.x < hdr.R) {
       if (warp < 8) {
         regs_inc<kRegsSoftmax>();
-        softmax_rows<kFp8, kD, kTerms>(a, smem, B, tmem, abort);
+        softmax_rows<kFp8, kD, kTerms, kToken>(a, smem, B, tmem, abort);
       } else if (warp < 12) {
         regs_dec<kRegsLoader>();
-        if constexpr (kFp8) loader_fp8<kFp8, kD, kTerms>(a, smem, B, abort);
+        if constexpr (kFp8) loader_fp8<kFp8, kD, kTerms, kToken>(a, smem, B, abort);
       } else if (warp == 12) {
         issue_half<kFp8, kD, kTerms>(a, smem, B, tmem, 0, abort);
       } else if (warp == 14) {

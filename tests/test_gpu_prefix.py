@@ -335,6 +335,39 @@ def test_values_of_any_magnitude(power, dim, out):
     assert not st.any() and (err <= tol).all(), (err / tol).max()
 
 
+@pytest.mark.parametrize("out", list(OUT))
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("odd", ["zeros", "one large"])
+@pytest.mark.parametrize("heavy", [False, True])
+def test_v_scales_far_apart(heavy, odd, dim, out):
+    """Per-token V scales of 2^-23 .. 2^-17 in a prefix, and beside them rows of
+    zeros, whose scale is 1, or early rows 2^12 times as large under small
+    weights: the others' weights keep their bits.  heavy: the first token
+    outweighs the others."""
+    c = PrefixCase(26, [0] * 6 + [1] * 5, [64, 19], [5 * i + 1 for i in range(11)], q_heads=16, kv_heads=2, dim=dim,
+                   page=16, cache=FP8_TOKEN)
+    ks, vs = c.ref.k_scale.reshape(c.P, 2, 16), c.ref.v_scale.reshape(c.P, 2, 16)
+    k, v = c.ref.k_pool.reshape(c.P, 2, 16, dim), c.ref.v_pool.reshape(c.P, 2, 16, dim)
+    vs *= np.float32(2.0 ** -14)
+    own_max = vs.max()
+    base = c.rng.standard_normal(dim).astype(np.float32)
+    c.q = synth.bf16_bits((1.5 * base + 0.3 * c.rng.standard_normal((11, 16, dim))).astype(np.float32))
+    for p in (c.table[0], c.table[6]):
+        if heavy:
+            k[p[0], :, 0], ks[p[0], :, 0] = oracle.e4m3_encode(64 * base), 1 / 64
+        for page, slot in ((p[0], 3), (p[8], 0), (p[13], 9), (p[18], 15)):
+            if odd == "zeros":
+                v[page, :, slot], vs[page, :, slot] = 0, 1.0
+            else:
+                k[page, :, slot], ks[page, :, slot] = oracle.e4m3_encode(-64 * base), 1 / 64
+                vs[page, :, slot] = own_max * 2.0 ** 12
+    got, st = c.call(OUT[out])
+    want, _, mag = c.want()
+    tol = c.tolerance(want, mag, OUT[out]) + weight_floor(c, 35 if out == "fp32" else 25, own_max) * (1 + 2.0 ** -8)
+    err = np.abs(got.float().cpu().numpy() - want)
+    assert not st.any() and (err <= tol).all(), (err / tol).max()
+
+
 @pytest.mark.parametrize("cache", [FP8, FP8_TOKEN, BF16])
 @pytest.mark.parametrize("tau", [0.0, -0.2])
 def test_scales_that_are_not_positive(cache, tau):
