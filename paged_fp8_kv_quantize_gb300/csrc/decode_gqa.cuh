@@ -154,17 +154,15 @@ __device__ __noinline__ void clear_dead_rows(uint32_t tile, int row_bytes, bool 
   __syncwarp();
 }
 
-// kJoin: see DecodeArgs::skip.
-template <bool kFp8, int kD, int kG, int kNCW, bool kJoin>
+// kToken: FP8 with per-token scales.  kJoin: see DecodeArgs::skip.
+template <bool kFp8, bool kToken, int kD, int kG, int kNCW, bool kJoin>
 __global__ void __launch_bounds__(Cfg<kFp8, kD, kG, kNCW>::kThreads, Cfg<kFp8, kD, kG, kNCW>::kMinBlocks)
     gqa_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                      const DecodeArgs a, const int nst) {
   using C = Cfg<kFp8, kD, kG, kNCW>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  const bool per_token = kFp8 && a.scale_mode == PFKV_SCALE_PER_TOKEN;
-  constexpr bool kRef = kFp8 && kJoin;
-  const SmemPlan sp = smem_plan(a.S, C::kRowBytes, per_token, nst, kNCW, kG, kD);
+  const SmemPlan sp = smem_plan(a.S, C::kRowBytes, kToken, nst, kNCW, kG, kD);
   uint64_t *full = reinterpret_cast<uint64_t *>(smem + sp.bars_off);
   uint64_t *empty = full + nst;
   uint64_t *item_full = empty + nst;
@@ -283,7 +281,7 @@ __global__ void __launch_bounds__(Cfg<kFp8, kD, kG, kNCW>::kThreads, Cfg<kFp8, k
       if (nv_lane) {
         nv = *reinterpret_cast<const uint4 *>((nv_part ? a.v_new : a.k_new) +
                                               ((size_t)b * a.cache.num_kv_heads + g) * kD + nv_k);
-        if (kFp8 && !per_token) nv_scale = __ldg(&(nv_part ? a.v_scale : a.k_scale)[g]);
+        if (kFp8 && !kToken) nv_scale = __ldg(&(nv_part ? a.v_scale : a.k_scale)[g]);
       }
       // ... and the destination page's id, loaded now as well: the row is
       // stored as soon as the first batch's copies are out (before them if
@@ -294,7 +292,7 @@ __global__ void __launch_bounds__(Cfg<kFp8, kD, kG, kNCW>::kThreads, Cfg<kFp8, k
       auto store_row = [&]() {  // whole warp
         bool bad = pid_new < 0 || pid_new >= a.P;
         if (tag_check && !bad) bad = __ldg(&a.page_tags[pid_new]) != __ldg(&tagrow[i_new]);
-        store_new_row<kFp8, kD>(a, nv, nv_scale, nv_lane, nv_part, nv_k, pid_new, bad, g, (L - 1) % S, per_token);
+        store_new_row<kFp8, kD>(a, nv, nv_scale, nv_lane, nv_part, nv_k, pid_new, bad, g, (L - 1) % S, kToken);
         row_stored = true;
       };
       int kb = 0;  // batch number within the piece
@@ -340,7 +338,7 @@ __global__ void __launch_bounds__(Cfg<kFp8, kD, kG, kNCW>::kThreads, Cfg<kFp8, k
                 tma_load_4d_stream(stage, &tmK, &full[st], 0, 0, g, pid, stream_pol);
                 tma_load_4d_stream(stage + S * C::kRowBytes, &tmV, &full[st], 0, 0, g, pid, stream_pol);
               }
-              if (per_token) {
+              if (kToken) {
                 const size_t rr = ((size_t)pid * a.cache.num_kv_heads + g) * S;
                 bulk_load_stream(stage + 2 * S * C::kRowBytes, a.k_scale + rr, 4u * S, &full[st], stream_pol);
                 bulk_load_stream(stage + 2 * S * C::kRowBytes + 4 * S, a.v_scale + rr, 4u * S, &full[st], stream_pol);
@@ -457,7 +455,7 @@ __global__ void __launch_bounds__(Cfg<kFp8, kD, kG, kNCW>::kThreads, Cfg<kFp8, k
           }
         }
         float base = a.sm_scale_log2;
-        if (kFp8 && !per_token) base *= __ldg(&a.k_scale[hg.kv]);
+        if (kFp8 && !kToken) base *= __ldg(&a.k_scale[hg.kv]);
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           const int ec = __shfl_sync(0xffffffffu, e, ((2 * tq + c) & 7) * 4);
@@ -466,7 +464,7 @@ __global__ void __launch_bounds__(Cfg<kFp8, kD, kG, kNCW>::kThreads, Cfg<kFp8, k
       }
 
       float m[2] = {kNegInf, kNegInf}, l[2] = {0.f, 0.f};
-      uint32_t vref = 16;  // biased exponent of the V scales' reference (kRef), and what takes a scale to it
+      uint32_t vref = 16;  // biased exponent of the V scales' reference and what takes a scale to it
       float vfac = ldexpf(C::kPScale, 127 - 16);
       float o[C::kKsteps][C::kNP][4];
 #pragma unroll
@@ -496,7 +494,7 @@ __global__ void __launch_bounds__(Cfg<kFp8, kD, kG, kNCW>::kThreads, Cfg<kFp8, k
           tbase[t] = smem_base + stg[t] * sp.stage_bytes + (uint32_t)(mt_in_page * 16 * C::kRowBytes);
           if (kJoin && live[t] && tok_base[t] + 16 > d.L && alive)
             clear_dead_rows(tbase[t] + S * C::kRowBytes, C::kRowBytes, C::kSwz, d.L - tok_base[t],
-                            per_token ? smem_base + stg[t] * sp.stage_bytes + 2 * S * C::kRowBytes + 4 * S +
+                            kToken ? smem_base + stg[t] * sp.stage_bytes + 2 * S * C::kRowBytes + 4 * S +
                                             4 * (mt_in_page * 16)
                                       : 0u);
         }
@@ -533,7 +531,7 @@ __global__ void __launch_bounds__(Cfg<kFp8, kD, kG, kNCW>::kThreads, Cfg<kFp8, k
           }
           z[t][0] = sacc[0] * mult[0]; z[t][1] = sacc[1] * mult[1];
           z[t][2] = sacc[2] * mult[0]; z[t][3] = sacc[3] * mult[1];
-          if (per_token && live[t]) {
+          if (kToken && live[t]) {
             const uint32_t sks = smem_base + stg[t] * sp.stage_bytes + 2 * S * C::kRowBytes +
                                  4 * ((tok_base[t] - (tok_base[t] / S) * S) + gid);
             const float k0 = lds_f32(sks), k1 = lds_f32(sks + 32);
@@ -579,9 +577,9 @@ __global__ void __launch_bounds__(Cfg<kFp8, kD, kG, kNCW>::kThreads, Cfg<kFp8, k
             }
         }
         // ---- per-token V scales, relative to a power of two not below any of them so far, so that weights times
-        // scales stay inside f16 at any magnitude of V; O is rescaled where it moves
+        // scales stay inside f16 at any magnitude of V; O is rescaled where it moves.  (1.5 to 3% of a call.)
         float vs[2][2] = {{C::kPScale, C::kPScale}, {C::kPScale, C::kPScale}};
-        if (kRef && per_token) {
+        if (kToken) {
           uint32_t e = 0;  // biased exponent of the largest
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
@@ -592,9 +590,8 @@ __global__ void __launch_bounds__(Cfg<kFp8, kD, kG, kNCW>::kThreads, Cfg<kFp8, k
             vs[t][1] = lds_f32(svs + 32);
             e = max(e, max(__float_as_uint(vs[t][0]) >> 23 & 255u, __float_as_uint(vs[t][1]) >> 23 & 255u));
           }
-          e = __reduce_max_sync(0xffffffffu, e);
-          if (e > vref) {
-            const uint32_t next = e + 3;  // room for scales that grow
+          if (__any_sync(0xffffffffu, e > vref)) {
+            const uint32_t next = __reduce_max_sync(0xffffffffu, e) + 3;  // room for scales that grow
             const float f = ldexpf(1.f, (int)vref - (int)next);
 #pragma unroll
             for (int i = 0; i < C::kKsteps; ++i)
@@ -623,13 +620,6 @@ __global__ void __launch_bounds__(Cfg<kFp8, kD, kG, kNCW>::kThreads, Cfg<kFp8, k
 #pragma unroll
             for (int k = 0; k < 4; ++k) pv[k] = __shfl_sync(0xffffffffu, p[t][k], src_lane);
           }
-          float vs0 = 1.f, vs1 = 1.f;
-          if (!kRef && per_token) {
-            const uint32_t svs = smem_base + stg[t] * sp.stage_bytes + 2 * S * C::kRowBytes + 4 * S +
-                                 4 * ((tok_base[t] - (tok_base[t] / S) * S) + gid);
-            vs0 = lds_f32(svs);
-            vs1 = lds_f32(svs + 32);
-          }
           uint32_t pb[C::kNP][2];
 #pragma unroll
           for (int nt = 0; nt < C::kNP; ++nt) {
@@ -638,7 +628,7 @@ __global__ void __launch_bounds__(Cfg<kFp8, kD, kG, kNCW>::kThreads, Cfg<kFp8, k
             for (int k = 0; k < 4; ++k) {
               const int e = k & 1;
               const int v = 8 * nt + 2 * tq + e;
-              const float pp = kRef ? pv[k] * vs[t][k >> 1] : pv[k] * C::kPScale * ((k < 2) ? vs0 : vs1);
+              const float pp = pv[k] * vs[t][k >> 1];
               const float hi = round16<kFp8>(pp);
               const bool lo_part = (kG == 1) ? (e == 1) : (v >= kG);
               val[k] = (v < 2 * kG) ? (lo_part ? pp - hi : hi) : 0.f;
@@ -686,7 +676,7 @@ __global__ void __launch_bounds__(Cfg<kFp8, kD, kG, kNCW>::kThreads, Cfg<kFp8, k
       }
       // ---- per-warp state -> shared memory
       // (the reference and the weights' scale taken out, each warp having its own)
-      const float wfac = kRef && per_token ? ldexpf(1.f / C::kPScale, (int)vref - 127) : 1.f;
+      const float wfac = kToken ? ldexpf(1.f / C::kPScale, (int)vref - 127) : 1.f;
 #pragma unroll
       for (int off = 4; off < 32; off <<= 1) {
         l[0] += __shfl_xor_sync(0xffffffffu, l[0], off);
@@ -720,8 +710,8 @@ __global__ void __launch_bounds__(Cfg<kFp8, kD, kG, kNCW>::kThreads, Cfg<kFp8, k
         for (int e = 0; e < 2; ++e) {
           const int hh = 2 * tq + e;
           if (hh < kG && !(kG == 1 && e == 1)) {
-            sm_o[(warp * kG + hh) * kD + d0] = kRef ? hv[e] * wfac : hv[e];
-            sm_o[(warp * kG + hh) * kD + d0 + 1] = kRef ? hv[2 + e] * wfac : hv[2 + e];
+            sm_o[(warp * kG + hh) * kD + d0] = hv[e] * wfac;
+            sm_o[(warp * kG + hh) * kD + d0 + 1] = hv[2 + e] * wfac;
           }
         }
       }
@@ -750,8 +740,7 @@ __global__ void __launch_bounds__(Cfg<kFp8, kD, kG, kNCW>::kThreads, Cfg<kFp8, k
       named_bar_sync(1, kCT);
       const uint32_t item_st = (uint32_t)sm_ctl[0];
       float ofac = 1.f;
-      if constexpr (kFp8) ofac = (per_token ? 1.f : __ldg(&a.v_scale[hg.kv])) / C::kPScale;
-      if (kRef && per_token) ofac = 1.f;
+      if constexpr (kFp8) ofac = kToken ? 1.f : __ldg(&a.v_scale[hg.kv]) / C::kPScale;
       float *out_bg = a.out + ((size_t)d.b * a.Hq + hg.first) * kD;  // rows of this (request, head group)
       if (!kJoin && d.nb == 1) {
         // the item covers the whole request: finish it here
@@ -830,19 +819,17 @@ constexpr int kNCW = 4;
 // (many pieces, each with its own set-up and finish) gets fewer pages.
 constexpr int kPieceCost = 16;
 
-// Launch shape of one split-kernel instantiation for one (page size, scale
-// mode), worked out on its first use and reused afterwards, so that later
+// Launch shape of one split-kernel instantiation for one page size, worked out on its first use and reused afterwards, so that later
 // calls -- including calls under stream capture -- only enqueue kernels.
 struct SplitShape {
-  int S = 0, per_token = -1, dev = -1, nst = 0, grid = 0;
+  int S = 0, dev = -1, nst = 0, grid = 0;
   uint32_t smem = 0;
 };
 
-template <bool kFp8, int kD, int kG, bool kJoin>
+template <bool kFp8, bool kToken, int kD, int kG, bool kJoin>
 int run_split(DecodeArgs &a, cudaStream_t s, const CUtensorMap &mk, const CUtensorMap &mv) {
   using C = Cfg<kFp8, kD, kG, kNCW>;
-  const bool per_token = kFp8 && a.scale_mode == PFKV_SCALE_PER_TOKEN;
-  auto kern = gqa_split_kernel<kFp8, kD, kG, kNCW, kJoin>;
+  auto kern = gqa_split_kernel<kFp8, kToken, kD, kG, kNCW, kJoin>;
   static SplitShape cache[4];
   static std::mutex mu;
   int dev = 0;
@@ -852,19 +839,19 @@ int run_split(DecodeArgs &a, cudaStream_t s, const CUtensorMap &mk, const CUtens
     std::lock_guard<std::mutex> lock(mu);
     bool found = false;
     for (auto &e : cache)
-      if (e.S == a.S && e.per_token == (int)per_token && e.dev == dev) {
+      if (e.S == a.S && e.dev == dev) {
         sh = e;
         found = true;
         break;
       }
     if (!found) {
       // stage ring of roughly 64 KB (at least 4 pages) so that two or three CTAs share an SM
-      const SmemPlan one = smem_plan(a.S, C::kRowBytes, per_token, 1, kNCW, kG, kD);
+      const SmemPlan one = smem_plan(a.S, C::kRowBytes, kToken, 1, kNCW, kG, kD);
       int nst = (int)(65536u / one.stage_bytes);
       if (nst < 4) nst = 4;
       if (nst > 32) nst = 32;
-      SmemPlan sp = smem_plan(a.S, C::kRowBytes, per_token, nst, kNCW, kG, kD);
-      while (sp.total > 200u * 1024u && nst > 2) sp = smem_plan(a.S, C::kRowBytes, per_token, --nst, kNCW, kG, kD);
+      SmemPlan sp = smem_plan(a.S, C::kRowBytes, kToken, nst, kNCW, kG, kD);
+      while (sp.total > 200u * 1024u && nst > 2) sp = smem_plan(a.S, C::kRowBytes, kToken, --nst, kNCW, kG, kD);
       // The attribute is a per-kernel cap on the device: only ever raise it, so
       // that a shape with a larger ring, cached earlier, keeps launching.
       static uint32_t attr_set[64] = {};
@@ -877,7 +864,7 @@ int run_split(DecodeArgs &a, cudaStream_t s, const CUtensorMap &mk, const CUtens
       const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, C::kThreads, sp.total);
       if (e != cudaSuccess) return cuda_fail(e, "occupancy query (split kernel)");
       if (per_sm < 1) return cuda_fail(cudaErrorInvalidConfiguration, "split kernel does not fit on an SM");
-      sh.S = a.S; sh.per_token = (int)per_token; sh.dev = dev; sh.nst = nst; sh.smem = sp.total;
+      sh.S = a.S; sh.dev = dev; sh.nst = nst; sh.smem = sp.total;
       sh.grid = num_sms() * per_sm;
       int slot = 0;
       for (int i = 0; i < 4; ++i)
@@ -933,7 +920,7 @@ int run_split(DecodeArgs &a, cudaStream_t s, const CUtensorMap &mk, const CUtens
 // page mostly meet in L2).  The kernel is instantiated for 1, 2, 4 or 8
 // head slots; a group of Gs heads takes the next of these and leaves the
 // other slots as zero-query padding whose results are never written.
-template <bool kFp8, int kD, bool kJoin>
+template <bool kFp8, bool kToken, int kD, bool kJoin>
 int dispatch_g(DecodeArgs &a, cudaStream_t s, const CUtensorMap &mk, const CUtensorMap &mv) {
   a.kv_sub = (a.G + 7) / 8;
   a.Gs = (a.G + a.kv_sub - 1) / a.kv_sub;
@@ -941,10 +928,10 @@ int dispatch_g(DecodeArgs &a, cudaStream_t s, const CUtensorMap &mk, const CUten
   a.Hkv *= a.kv_sub;
   const int slots = a.Gs <= 1 ? 1 : a.Gs <= 2 ? 2 : a.Gs <= 4 ? 4 : 8;
   switch (slots) {
-    case 1: return run_split<kFp8, kD, 1, kJoin>(a, s, mk, mv);
-    case 2: return run_split<kFp8, kD, 2, kJoin>(a, s, mk, mv);
-    case 4: return run_split<kFp8, kD, 4, kJoin>(a, s, mk, mv);
-    default: return run_split<kFp8, kD, 8, kJoin>(a, s, mk, mv);
+    case 1: return run_split<kFp8, kToken, kD, 1, kJoin>(a, s, mk, mv);
+    case 2: return run_split<kFp8, kToken, kD, 2, kJoin>(a, s, mk, mv);
+    case 4: return run_split<kFp8, kToken, kD, 4, kJoin>(a, s, mk, mv);
+    default: return run_split<kFp8, kToken, kD, 8, kJoin>(a, s, mk, mv);
   }
 }
 
@@ -955,10 +942,15 @@ int dispatch_split(DecodeArgs &a, cudaStream_t s) {
   if (rc) return rc;
   rc = make_pool_map(&mv, a.v_pool, a.dtype, a.D, a.S, a.Hkv, a.P);
   if (rc) return rc;
-  const bool fp8 = a.dtype == PFKV_DTYPE_FP8_E4M3;
-  if (a.D == 128) return fp8 ? dispatch_g<true, 128, kJoin>(a, s, mk, mv) : dispatch_g<false, 128, kJoin>(a, s, mk, mv);
-  if (a.D == 64) return fp8 ? dispatch_g<true, 64, kJoin>(a, s, mk, mv) : dispatch_g<false, 64, kJoin>(a, s, mk, mv);
-  return PFKV_ERR_UNSUPPORTED;
+  if (a.D != 64 && a.D != 128) return PFKV_ERR_UNSUPPORTED;
+  if (a.dtype != PFKV_DTYPE_FP8_E4M3)
+    return a.D == 128 ? dispatch_g<false, false, 128, kJoin>(a, s, mk, mv)
+                      : dispatch_g<false, false, 64, kJoin>(a, s, mk, mv);
+  if (a.scale_mode == PFKV_SCALE_PER_TOKEN)
+    return a.D == 128 ? dispatch_g<true, true, 128, kJoin>(a, s, mk, mv)
+                      : dispatch_g<true, true, 64, kJoin>(a, s, mk, mv);
+  return a.D == 128 ? dispatch_g<true, false, 128, kJoin>(a, s, mk, mv)
+                    : dispatch_g<true, false, 64, kJoin>(a, s, mk, mv);
 }
 
 }  // namespace

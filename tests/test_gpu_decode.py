@@ -10,6 +10,7 @@ import oracle
 from gpu_helpers import DeviceCase, assert_close, dev_i32
 from oracle_helpers import oracle_cache
 from paged_fp8_kv_quantize_gb300 import abi, synth
+from prefix_helpers import FP8_TOKEN, PrefixCase
 
 pytestmark = pytest.mark.gpu
 FP8, BF16 = abi.DTYPE_FP8_E4M3, abi.DTYPE_BF16
@@ -134,6 +135,24 @@ def test_self_split_many_requests(max_splits):
 def test_per_token_scales_gqa():
     w = _work(401, G=4, Hkv=8, D=128, S=16, lens=[33, 900, 4000], scale_mode=synth.PER_TOKEN)
     _check(w, FP8)
+
+
+@pytest.mark.parametrize("power", [40, 14, -14, -60])
+@pytest.mark.parametrize("G,Hkv,D", [(1, 2, 64), (2, 2, 128), (4, 2, 128), (8, 2, 64), (8, 1, 128)])
+def test_per_token_v_scales_of_any_magnitude(G, Hkv, D, power):
+    """V scales up to 2^(power - 3).  Weights are carried to 22 bits (the
+    tolerance's) or 2^-36 of the largest scale where f16 is subnormal, times
+    codes of at most 448."""
+    c = PrefixCase(91, [-1] * 6, [], [1, 16, 77, 300, 1000, 2100], q_heads=G * Hkv, kv_heads=Hkv, dim=D, page=16,
+                   cache=FP8_TOKEN)
+    c.ref.v_scale[:] = np.ldexp(c.ref.v_scale, power)
+    c.device()
+    a = c.args()
+    got, st = abi.paged_decode_attention(c.gpu, a["q"], a["seq_lens"], a["block_table"], a["block_tags"], c.tau)
+    want, _, mag = c.want()
+    tol = c.tolerance(want, mag, torch.float32) + c.lens[:, None, None] * 448 * c.ref.v_scale.max() * 2.0 ** -36
+    err = np.abs(got.cpu().numpy() - want)
+    assert not st.any() and (err <= tol).all(), (err / tol).max()
 
 
 def test_tiny_config_tag_check():
