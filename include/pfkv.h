@@ -169,8 +169,9 @@ size_t pfkv_decode_workspace_bytes(const pfkv_cache *cache, int32_t batch, int32
  *   z_t = softmax_scale * q[b][h] . k^[g][t],  p = softmax(z over t < L_b),
  *   out[b][h] = sum_t p_t v^[g][t],  where k^, v^ are the dequantized rows
  *   (code value * scale for FP8).
- * Slots of the last page past L_b do not count, but must not hold NaN (a code
- * 0x7F or 0xFF, or a NaN value): a pool is filled with finite values once.
+ * Slots past L_b may hold anything, NaN among it.  (The latent stream: they do
+ * not count, but must not hold NaN codes, 0x7F or 0xFF; a pool is filled with
+ * other codes once.)
  * Only logical pages i < ceil(L_b / page_size) are inspected.  A request
  * with a data-fault bit gets zero output.  batch * max_pages may not exceed
  * 2^40 (PFKV_ERR_SHAPE).  max_splits (1..256) bounds how many
@@ -301,7 +302,6 @@ int pfkv_paged_decode_step(const pfkv_cache *cache, const void *k_new, const voi
  *   As elsewhere, a request with a data fault gets zeros and does not touch
  *   the others of its group; an unused row of the batch may keep its group
  *   with a length of 0.
- * Slots past a request's length may hold anything here, NaN among it.
  * The other arguments are those of paged_decode_attention.  Supported: its
  * grouped-query shapes (head_dim 64 or 128, FP8 with either scale mode, or
  * BF16) with up to 4096 groups of up to 65535 requests in all.  The latent

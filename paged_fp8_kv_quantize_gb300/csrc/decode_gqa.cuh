@@ -138,12 +138,11 @@ __device__ __forceinline__ void drain_wait_full(uint64_t *bar, uint32_t parity) 
     if (global_timer_ns() - t0 > kWaitLimitNs) return;
 }
 
-// Slots past a request's length hold anything, NaN among it, which a weight of
-// zero does not silence: zeros over rows first .. 15 of a 16-row V tile in
-// shared memory (and their scales, where scales is not 0).  Whole warp; once
-// per request and head.  kJoin only: in the plain decode, whose pools are
-// filled with finite values, even the branch to it costs 2% of a ragged batch
-// (108.6 -> 110.5 us).
+// Slots past a request's length hold anything, NaN among it (a page's former
+// owner may have left it), which a weight of zero does not silence: zeros over
+// rows first .. 15 of a 16-row V tile in shared memory (and their scales, where
+// scales is not 0).  Whole warp; once per request and head, yet the branch to it
+// costs 0.8% of a ragged batch (106.2 -> 107.0 us) and up to 4% of a long context.
 __device__ __noinline__ void clear_dead_rows(uint32_t tile, int row_bytes, bool swz, int first, uint32_t scales) {
   const int lane = threadIdx.x & 31;
   for (int off = first * row_bytes + 16 * lane; off < 16 * row_bytes; off += 512)
@@ -492,7 +491,7 @@ __global__ void __launch_bounds__(Cfg<kFp8, kD, kG, kNCW>::kThreads, Cfg<kFp8, k
           tok_base[t] = (d.p0 + page_local) * S + mt_in_page * 16;
           live[t] = valid[t] && tok_base[t] < d.L;
           tbase[t] = smem_base + stg[t] * sp.stage_bytes + (uint32_t)(mt_in_page * 16 * C::kRowBytes);
-          if (kJoin && live[t] && tok_base[t] + 16 > d.L && alive)
+          if (live[t] && tok_base[t] + 16 > d.L && alive)
             clear_dead_rows(tbase[t] + S * C::kRowBytes, C::kRowBytes, C::kSwz, d.L - tok_base[t],
                             kToken ? smem_base + stg[t] * sp.stage_bytes + 2 * S * C::kRowBytes + 4 * S +
                                             4 * (mt_in_page * 16)

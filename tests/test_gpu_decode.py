@@ -10,6 +10,8 @@ import oracle
 from gpu_helpers import DeviceCase, assert_close, dev_i32
 from oracle_helpers import oracle_cache
 from paged_fp8_kv_quantize_gb300 import abi, synth
+from prefix_helpers import BF16 as BF16_CACHE
+from prefix_helpers import FP8 as FP8_HEAD
 from prefix_helpers import FP8_TOKEN, PrefixCase
 
 pytestmark = pytest.mark.gpu
@@ -153,6 +155,37 @@ def test_per_token_v_scales_of_any_magnitude(G, Hkv, D, power):
     tol = c.tolerance(want, mag, torch.float32) + c.lens[:, None, None] * 448 * c.ref.v_scale.max() * 2.0 ** -36
     err = np.abs(got.cpu().numpy() - want)
     assert not st.any() and (err <= tol).all(), (err / tol).max()
+
+
+@pytest.mark.parametrize("page", [16, 64])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("cache", [FP8_HEAD, FP8_TOKEN, BF16_CACHE])
+def test_slots_past_the_length_hold_anything(cache, D, page):
+    """NaN and infinity in the rest of a request's last page, as a former owner
+    may have left them: the decode and the fused step give the same bits."""
+    c = PrefixCase(92, [-1] * 7, [], [1, 15, 16, 63, 65, 500, 1001], q_heads=8, kv_heads=2, dim=D, page=page, cache=cache)
+    c.device()
+    a = c.args()
+    k_new, v_new = (torch.randn((7, 2, D), device="cuda").bfloat16() for _ in range(2))
+
+    def both():
+        x, st1 = abi.paged_decode_attention(c.gpu, a["q"], a["seq_lens"], a["block_table"], None, c.tau)
+        y, st2 = abi.paged_decode_step(c.gpu, k_new, v_new, a["q"], a["seq_lens"], a["block_table"], None, c.tau)
+        assert not st1.any() and not st2.any()
+        return x.clone(), y.clone()
+
+    both()  # the step has written its tokens
+    want = both()
+    for bad in (0x7F, 0xFF) if cache != BF16_CACHE else (float("nan"), float("inf")):
+        for b in range(7):
+            n = int(c.lens[b])
+            p, s = int(c.table[b, (n - 1) // page]), (n - 1) % page + 1
+            for x in (c.gpu.k_rows(), c.gpu.v_rows()):
+                x[p, :, s:] = bad
+            if cache == FP8_TOKEN:
+                for x in (c.gpu.k_scale, c.gpu.v_scale):
+                    x.view(c.P, 2, page)[p, :, s:] = float("nan") if bad == 0x7F else float("inf")
+        assert all(torch.equal(x, y) for x, y in zip(both(), want))
 
 
 def test_tiny_config_tag_check():
