@@ -5,8 +5,8 @@
 namespace pfkv {
 
 int launch_gqa_decode(const DecodeArgs &a, cudaStream_t s) {
-  DecodeArgs own = a;
-  return dispatch_split<false>(own, s);
+  SplitLaunch l;
+  return dispatch_split<false>(a, l, s);
 }
 
 }  // namespace pfkv

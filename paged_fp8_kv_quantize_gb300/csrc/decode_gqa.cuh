@@ -825,8 +825,27 @@ struct SplitShape {
   uint32_t smem = 0;
 };
 
+// The split kernel is a programmatic dependent of the stream's previous
+// kernel: its CTAs take SMs as that kernel's blocks drain and wait for it to
+// finish (griddepcontrol.wait) before touching memory.
+int enqueue_split(SplitLaunch &l, cudaStream_t s) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(l.a.n_ctas);
+  cfg.blockDim = dim3(l.threads);
+  cfg.dynamicSmemBytes = l.smem;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  void *args[] = {&l.map_k, &l.map_v, &l.a, &l.stages};
+  return cuda_ok(cudaLaunchKernelExC(&cfg, l.kernel, args), "split kernel launch");
+}
+
 template <bool kFp8, bool kToken, int kD, int kG, bool kJoin>
-int run_split(DecodeArgs &a, cudaStream_t s, const CUtensorMap &mk, const CUtensorMap &mv) {
+int prepare_split(SplitLaunch &l) {
+  DecodeArgs &a = l.a;
   using C = Cfg<kFp8, kD, kG, kNCW>;
   auto kern = gqa_split_kernel<kFp8, kToken, kD, kG, kNCW, kJoin>;
   static SplitShape cache[4];
@@ -883,33 +902,31 @@ int run_split(DecodeArgs &a, cudaStream_t s, const CUtensorMap &mk, const CUtens
   // against 35 with 16 pages)
   a.piece_cost = kJoin ? max(1, 16 * kPieceCost / a.S) : kPieceCost;
   if (a.n_ctas > kMaxCtas) return PFKV_ERR_UNSUPPORTED;  // more KV heads than abort words
-  // The split kernel is a programmatic dependent of the stream's previous
-  // kernel: its CTAs take SMs as that kernel's blocks drain and wait for it
-  // to finish (griddepcontrol.wait) before touching memory.
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(a.n_ctas);
-  cfg.blockDim = dim3(C::kThreads);
-  cfg.dynamicSmemBytes = sh.smem;
-  cfg.stream = s;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  int rc = cuda_ok(cudaLaunchKernelEx(&cfg, kern, mk, mv, a, sh.nst), "split kernel launch");
-  if (rc || kJoin) return rc;
+  l.stages = sh.nst;
+  l.threads = C::kThreads;
+  l.smem = sh.smem;
+  l.kernel = reinterpret_cast<const void *>(kern);
+  return PFKV_OK;
+}
+
+template <int kD, int kG>
+int run_merge(const DecodeArgs &a, cudaStream_t s) {
   // the narrow merge shape when the wide one would give fewer than two
   // blocks per SM (a few requests, many pieces each)
   const bool narrow = (long long)a.B * a.Hkv * merge_col_blocks<kD, kG>() < 2LL * num_sms();
-  cudaLaunchConfig_t mcfg = {};
-  mcfg.gridDim = dim3(a.B * a.Hkv, narrow ? merge_col_blocks<kD, kG, 0>() : merge_col_blocks<kD, kG>());
-  mcfg.blockDim = dim3(256);
-  mcfg.stream = s;
-  mcfg.attrs = attr;
-  mcfg.numAttrs = 1;
-  return cuda_ok(narrow ? cudaLaunchKernelEx(&mcfg, merge_kernel<kD, kG, 0>, a)
-                        : cudaLaunchKernelEx(&mcfg, merge_kernel<kD, kG>, a),
+  const dim3 grid(a.B * a.Hkv, narrow ? merge_col_blocks<kD, kG, 0>() : merge_col_blocks<kD, kG>());
+  return cuda_ok(narrow ? launch_dependent(merge_kernel<kD, kG, 0>, grid, 256, 0, s, a)
+                        : launch_dependent(merge_kernel<kD, kG>, grid, 256, 0, s, a),
                  "merge kernel launch");
+}
+
+// kJoin: prepared, for the caller to launch; else launched, with its merge.
+template <bool kFp8, bool kToken, int kD, int kG, bool kJoin>
+int run_split(SplitLaunch &l, cudaStream_t s) {
+  int rc = prepare_split<kFp8, kToken, kD, kG, kJoin>(l);
+  if (rc || kJoin) return rc;
+  rc = enqueue_split(l, s);
+  return rc ? rc : run_merge<kD, kG>(l.a, s);
 }
 
 // Any group size: up to 8 query heads per CTA group (the register-operand
@@ -919,37 +936,36 @@ int run_split(DecodeArgs &a, cudaStream_t s, const CUtensorMap &mk, const CUtens
 // page mostly meet in L2).  The kernel is instantiated for 1, 2, 4 or 8
 // head slots; a group of Gs heads takes the next of these and leaves the
 // other slots as zero-query padding whose results are never written.
+// (dispatch_split cuts the groups.)
 template <bool kFp8, bool kToken, int kD, bool kJoin>
-int dispatch_g(DecodeArgs &a, cudaStream_t s, const CUtensorMap &mk, const CUtensorMap &mv) {
-  a.kv_sub = (a.G + 7) / 8;
-  a.Gs = (a.G + a.kv_sub - 1) / a.kv_sub;
-  if ((long long)a.Hkv * a.kv_sub > kMaxCtas) return PFKV_ERR_UNSUPPORTED;
-  a.Hkv *= a.kv_sub;
-  const int slots = a.Gs <= 1 ? 1 : a.Gs <= 2 ? 2 : a.Gs <= 4 ? 4 : 8;
+int dispatch_g(SplitLaunch &l, cudaStream_t s) {
+  const int slots = l.a.Gs <= 1 ? 1 : l.a.Gs <= 2 ? 2 : l.a.Gs <= 4 ? 4 : 8;
   switch (slots) {
-    case 1: return run_split<kFp8, kToken, kD, 1, kJoin>(a, s, mk, mv);
-    case 2: return run_split<kFp8, kToken, kD, 2, kJoin>(a, s, mk, mv);
-    case 4: return run_split<kFp8, kToken, kD, 4, kJoin>(a, s, mk, mv);
-    default: return run_split<kFp8, kToken, kD, 8, kJoin>(a, s, mk, mv);
+    case 1: return run_split<kFp8, kToken, kD, 1, kJoin>(l, s);
+    case 2: return run_split<kFp8, kToken, kD, 2, kJoin>(l, s);
+    case 4: return run_split<kFp8, kToken, kD, 4, kJoin>(l, s);
+    default: return run_split<kFp8, kToken, kD, 8, kJoin>(l, s);
   }
 }
 
 template <bool kJoin>
-int dispatch_split(DecodeArgs &a, cudaStream_t s) {
-  CUtensorMap mk, mv;
-  int rc = make_pool_map(&mk, a.k_pool, a.dtype, a.D, a.S, a.Hkv, a.P);
-  if (rc) return rc;
-  rc = make_pool_map(&mv, a.v_pool, a.dtype, a.D, a.S, a.Hkv, a.P);
-  if (rc) return rc;
+int dispatch_split(const DecodeArgs &args, SplitLaunch &l, cudaStream_t s = nullptr) {
+  l.a = args;
+  DecodeArgs &a = l.a;
   if (a.D != 64 && a.D != 128) return PFKV_ERR_UNSUPPORTED;
+  a.kv_sub = (a.G + 7) / 8;
+  a.Gs = (a.G + a.kv_sub - 1) / a.kv_sub;
+  if ((long long)a.Hkv * a.kv_sub > kMaxCtas) return PFKV_ERR_UNSUPPORTED;
+  int rc = make_pool_map(&l.map_k, a.k_pool, a.dtype, a.D, a.S, a.Hkv, a.P);
+  if (rc) return rc;
+  rc = make_pool_map(&l.map_v, a.v_pool, a.dtype, a.D, a.S, a.Hkv, a.P);
+  if (rc) return rc;
+  a.Hkv *= a.kv_sub;
   if (a.dtype != PFKV_DTYPE_FP8_E4M3)
-    return a.D == 128 ? dispatch_g<false, false, 128, kJoin>(a, s, mk, mv)
-                      : dispatch_g<false, false, 64, kJoin>(a, s, mk, mv);
+    return a.D == 128 ? dispatch_g<false, false, 128, kJoin>(l, s) : dispatch_g<false, false, 64, kJoin>(l, s);
   if (a.scale_mode == PFKV_SCALE_PER_TOKEN)
-    return a.D == 128 ? dispatch_g<true, true, 128, kJoin>(a, s, mk, mv)
-                      : dispatch_g<true, true, 64, kJoin>(a, s, mk, mv);
-  return a.D == 128 ? dispatch_g<true, false, 128, kJoin>(a, s, mk, mv)
-                    : dispatch_g<true, false, 64, kJoin>(a, s, mk, mv);
+    return a.D == 128 ? dispatch_g<true, true, 128, kJoin>(l, s) : dispatch_g<true, true, 64, kJoin>(l, s);
+  return a.D == 128 ? dispatch_g<true, false, 128, kJoin>(l, s) : dispatch_g<true, false, 64, kJoin>(l, s);
 }
 
 }  // namespace

@@ -4,6 +4,8 @@
 
 namespace pfkv {
 
-int launch_gqa_split(DecodeArgs &a, cudaStream_t s) { return dispatch_split<true>(a, s); }
+int prepare_gqa_split(const DecodeArgs &a, SplitLaunch &launch) { return dispatch_split<true>(a, launch); }
+
+int launch_gqa_split(SplitLaunch &launch, cudaStream_t s) { return enqueue_split(launch, s); }
 
 }  // namespace pfkv

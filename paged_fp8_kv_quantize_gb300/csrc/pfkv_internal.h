@@ -93,8 +93,17 @@ int num_sms();
 
 // launchers (return PFKV_* codes)
 int launch_gqa_decode(const DecodeArgs &a, cudaStream_t s);
-// The split kernel alone (see DecodeArgs::skip); fills in the launch's n_ctas and st_groups.
-int launch_gqa_split(DecodeArgs &a, cudaStream_t s);
+// The split kernel alone (see DecodeArgs::skip), in two steps, so that a caller
+// of several kernels knows what is refused before it launches the first.
+struct SplitLaunch {
+  CUtensorMap map_k, map_v;
+  DecodeArgs a;  // with the launch's n_ctas and st_groups
+  int stages, threads;
+  uint32_t smem;
+  const void *kernel;
+};
+int prepare_gqa_split(const DecodeArgs &a, SplitLaunch &launch);
+int launch_gqa_split(SplitLaunch &launch, cudaStream_t s);
 size_t prefix_ws_bytes(size_t first, int batch, int q_heads, int kv_heads, int dim, int n_groups);
 int launch_prefix_decode(const DecodeArgs &d, size_t ws_first, uint8_t *ws, const int *group_of,
                          const int *group_pages, int n_groups, int out_bf16, cudaStream_t s);

@@ -346,6 +346,25 @@ int make_tile_map(CUtensorMap *map, const void *pool, const DecodeArgs &d) {
 template <bool kFp8, int kD, int kTerms, bool kToken>
 int run_prefix(PrefixArgs a, cudaStream_t s) {
   using C = PCfg<kFp8, kD, kTerms>;
+  a.ctas = a.n_groups == 0 ? 0 : num_sms() < kMaxRanges ? num_sms() : kMaxRanges;
+  const LineUnits units = line_units(a.d.S);
+  a.c0 = units.c0;
+  a.min_units = units.min_units;
+  // all that can be refused comes before the first launch
+  DecodeArgs own = a.d;
+  own.beside = a.ctas > 0;
+  own.seq_lens = a.own_len;
+  SplitLaunch split;
+  int rc = prepare_gqa_split(own, split);
+  if (rc) return rc;
+  a.d.n_ctas = split.a.n_ctas;
+  a.d.st_groups = split.a.st_groups;
+  CUtensorMap map_k{}, map_v{};
+  if (!kFp8 && a.ctas > 0) {
+    rc = make_tile_map(&map_k, a.d.k_pool, a.d);
+    if (!rc) rc = make_tile_map(&map_v, a.d.v_pool, a.d);
+    if (rc) return rc;
+  }
   int dev = 0;
   cudaGetDevice(&dev);
   static std::atomic<uint64_t> attr_set{0};  // devices whose shared-memory limit is raised
@@ -355,33 +374,18 @@ int run_prefix(PrefixArgs a, cudaStream_t s) {
     if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(prefix kernel)");
     if (dev < 64) attr_set.fetch_or(1ull << dev);
   }
-  a.ctas = a.n_groups == 0 ? 0 : num_sms() < kMaxRanges ? num_sms() : kMaxRanges;
-  const LineUnits units = line_units(a.d.S);
-  a.c0 = units.c0;
-  a.min_units = units.min_units;
-  int rc = cuda_ok(launch_dependent(prefix_plan_kernel, dim3((unsigned)a.d.B + 1u), kPlanThreads,
-                                    8 * (size_t)a.n_groups, s, a),
-                   "prefix plan launch");
+  rc = cuda_ok(launch_dependent(prefix_plan_kernel, dim3((unsigned)a.d.B + 1u), kPlanThreads, 8 * (size_t)a.n_groups, s,
+                                a),
+               "prefix plan launch");
   if (rc) return rc;
   if (a.ctas > 0) {
-    CUtensorMap map_k{}, map_v{};
-    if (!kFp8) {
-      rc = make_tile_map(&map_k, a.d.k_pool, a.d);
-      if (!rc) rc = make_tile_map(&map_v, a.d.v_pool, a.d);
-      if (rc) return rc;
-    }
-    rc = cuda_ok(launch_dependent(prefix_kernel<kFp8, kD, kTerms, kToken>, dim3(a.ctas), kPThreads, C::kTotal, s, map_k, map_v,
-                                  a),
+    rc = cuda_ok(launch_dependent(prefix_kernel<kFp8, kD, kTerms, kToken>, dim3(a.ctas), kPThreads, C::kTotal, s, map_k,
+                                  map_v, a),
                  "prefix kernel launch");
     if (rc) return rc;
   }
-  DecodeArgs own = a.d;
-  own.beside = a.ctas > 0;
-  own.seq_lens = a.own_len;
-  rc = launch_gqa_split(own, s);
+  rc = launch_gqa_split(split, s);
   if (rc) return rc;
-  a.d.n_ctas = own.n_ctas;
-  a.d.st_groups = own.st_groups;
   // eight warps a row where one each would leave SMs idle
   const long long rows = (long long)a.d.B * a.d.Hq;
   const bool few = rows < 8LL * num_sms();

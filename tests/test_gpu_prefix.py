@@ -402,6 +402,23 @@ def test_stream_argument():
     assert all(torch.equal(x, want) for x in got)
 
 
+def test_a_refused_call_enqueues_nothing():
+    """More KV heads than the split kernel takes: workspace, output and status
+    stay as they were."""
+    H, B = 4097, 2
+    cache = abi.PagedCache(2, 16, H, 64, fill=0)
+    ws = torch.full((abi.prefix_workspace_bytes(cache, B, H, 1, 2),), 0xEE, dtype=torch.uint8, device="cuda")
+    out = torch.full((B, H, 64), 7.0, device="cuda")
+    st = torch.full((B,), -5, dtype=torch.int32, device="cuda")
+    q = torch.zeros((B, H, 64), dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(abi.PfkvError):
+        abi.paged_decode_attention_prefix(cache, q, dev_i32(np.array([20, 20])), dev_i32(np.array([[0, 1], [0, 1]])), None,
+                                          dev_i32(np.array([0, 0])), dev_i32(np.array([1])), 0.1, max_splits=2,
+                                          workspace=ws, out=out, status=st)
+    torch.cuda.synchronize()
+    assert (ws == 0xEE).all() and (out == 7.0).all() and (st == -5).all()
+
+
 def test_fork_decode_release_together():
     """One prompt forked into samples that decode a few steps each, reading the
     prompt's pages once, and are given back: outputs against the oracle, and

@@ -50,6 +50,13 @@ def test_refusals():
     assert call(desc(head_dim=96, v_head_dim=96), ws_bytes=1 << 40) == -3
 
 
+def test_too_many_head_groups_are_refused_first():
+    """More KV heads, or groups of eight query heads, than the split kernel
+    takes: refused before the CUDA runtime is asked for anything."""
+    assert call(desc(num_kv_heads=4097), hq=4097, ws_bytes=1 << 40) == -3
+    assert call(desc(num_kv_heads=2049), hq=2049 * 9, ws_bytes=1 << 40) == -3
+
+
 def test_workspace_bytes():
     f = abi.lib.pfkv_prefix_workspace_bytes
     d = desc()
