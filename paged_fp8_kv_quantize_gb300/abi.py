@@ -246,18 +246,16 @@ class PagedCache:
                          _ptr(self.page_tags))
 
     def _ref(self, dev):
-        """desc() by reference, its struct kept from call to call and the addresses filled in anew."""
-        if self.page_tags.get_device() != dev:
-            raise ValueError(f"the cache is on {self.page_tags.device}, not on the current device")
-        d = self.__dict__.get("_desc")
-        if d is None:
-            d = self._desc = self.desc()
-        d.k_pool = self.k_pool.data_ptr() if self.k_pool is not None else None
-        d.v_pool = self.v_pool.data_ptr() if self.v_pool is not None else None
-        d.k_scale = self.k_scale.data_ptr() if self.k_scale is not None else None
-        d.v_scale = self.v_scale.data_ptr() if self.v_scale is not None else None
-        d.page_tags = self.page_tags.data_ptr()
-        return ctypes.byref(d)
+        """desc() by reference, all of its tensors on device dev."""
+        k, v, ks, vs, tags = self.k_pool, self.v_pool, self.k_scale, self.v_scale, self.page_tags
+        if (tags.get_device() != dev or k is not None and k.get_device() != dev
+                or v is not None and v.get_device() != dev or ks is not None and ks.get_device() != dev
+                or vs is not None and vs.get_device() != dev):
+            raise ValueError(f"the cache's tensors are not all on the current device ({dev})")
+        return ctypes.byref(CacheDesc(
+            self.P, self.S, self.H, self.D, self.Dv, self.kv_shared, self.dtype, self.scale_mode,
+            None if k is None else k.data_ptr(), None if v is None else v.data_ptr(),
+            None if ks is None else ks.data_ptr(), None if vs is None else vs.data_ptr(), tags.data_ptr()))
 
     def k_rows(self):
         return self.k_pool.view(self.P, self.H, self.S, self.D)

@@ -1,8 +1,11 @@
 """CPU-only checks of the page operators: their refusals before any CUDA call,
 and the sequential reference held to what any right one keeps."""
+import copy
 import ctypes
 
 import numpy as np
+import pytest
+import torch
 
 from paged_fp8_kv_quantize_gb300 import abi
 from sharing_oracle import SharedPool
@@ -13,6 +16,26 @@ def desc(**kw):
     for k, v in kw.items():
         setattr(d, k, v)
     return ctypes.byref(d)
+
+
+def test_a_call_takes_the_cache_as_it_is():
+    """A pool that has grown, a copied cache, two calls at once: each call's
+    descriptor is its own and holds what the cache is then."""
+    c = abi.PagedCache(4, 16, 2, 64, device="cpu")
+    cpu = c.page_tags.get_device()
+    first = c._ref(cpu)._obj
+    was = bytes(first)
+    copied = copy.deepcopy(c)
+    assert copied._ref(cpu)._obj.k_pool == copied.k_pool.data_ptr()
+    shallow = copy.copy(c)
+    c.P = 9
+    c.k_pool, c.v_pool = (torch.zeros(9 * 2 * 16 * 64, dtype=torch.uint8) for _ in range(2))
+    c.page_tags = torch.zeros(9, dtype=torch.int32)
+    now = c._ref(cpu)._obj
+    assert (now.num_pages, now.k_pool, now.page_tags) == (9, c.k_pool.data_ptr(), c.page_tags.data_ptr())
+    assert bytes(first) == was and bytes(shallow._ref(cpu)._obj) == was
+    with pytest.raises(ValueError):
+        c._ref(0)  # not where the cache is
 
 
 def test_copy_refusals():
