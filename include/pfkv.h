@@ -310,7 +310,7 @@ int pfkv_paged_decode_step(const pfkv_cache *cache, const void *k_new, const voi
  */
 enum { PFKV_OUT_FP32 = 0, PFKV_OUT_BF16 = 1 };
 
-/* Host-only; SIZE_MAX for sizes a call would refuse. */
+/* Host-only; SIZE_MAX for sizes a call would refuse, 0 where the cache is NULL or a size is negative (or no size). */
 size_t pfkv_prefix_workspace_bytes(const pfkv_cache *cache, int32_t batch, int32_t num_q_heads, int32_t n_groups,
                                    int32_t max_splits);
 

@@ -371,7 +371,7 @@ def paged_decode_attention_prefix(cache, q, seq_lens, block_table, block_tags, p
     if workspace is None:
         n = prefix_workspace_bytes(cache, B, Hq, n_groups, max_splits)
         if n >= 1 << 62:
-            raise PfkvError("pfkv_prefix_workspace_bytes", -2)
+            n = 256  # the call below says what it refuses
         workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
     if out is None:
         out = torch.empty((B, Hq, cache.Dv), dtype=out_dtype, device=q.device)

@@ -108,6 +108,12 @@ int decode_precheck(int want_dtype, const pfkv_cache *c, int32_t Hq, int32_t bat
   return PFKV_OK;
 }
 
+// Shapes that the shared-prefix decode has kernels for, as far as they are its own.
+static bool prefix_shape(const pfkv_cache *c, int32_t batch, int32_t n_groups) {
+  return n_groups <= kMaxPrefixGroups && batch <= kMaxPrefixBatch && !c->kv_shared &&
+         (c->head_dim == 64 || c->head_dim == 128);
+}
+
 // A shared-prefix call's own arguments.
 struct PrefixCall {
   const int32_t *group_of, *group_pages;
@@ -127,7 +133,7 @@ static int decode_common(int want_dtype, const pfkv_cache *c, const void *q, int
   if (prefix) {
     if (prefix->out_dtype != PFKV_OUT_FP32 && prefix->out_dtype != PFKV_OUT_BF16) return PFKV_ERR_DTYPE;
     if (prefix->n_groups < 0 || (int64_t)batch * Hq > 0x7fffffff) return PFKV_ERR_SHAPE;  // rows are counted in int
-    if (prefix->n_groups > kMaxPrefixGroups || batch > kMaxPrefixBatch || c->kv_shared) return PFKV_ERR_UNSUPPORTED;
+    if (!prefix_shape(c, batch, prefix->n_groups)) return PFKV_ERR_UNSUPPORTED;
   }
   if (batch == 0) return PFKV_OK;
   if (prefix && (!prefix->group_of || (prefix->n_groups > 0 && !prefix->group_pages))) return PFKV_ERR_NULL;
@@ -281,9 +287,12 @@ size_t pfkv_prefix_workspace_bytes(const pfkv_cache *cache, int32_t batch, int32
                                    int32_t max_splits) {
   const size_t n = pfkv_decode_workspace_bytes(cache, batch, num_q_heads, max_splits);
   if (n == 0 || n == SIZE_MAX || n_groups < 0) return n == SIZE_MAX ? n : 0;
-  if (n_groups > kMaxPrefixGroups || batch > kMaxPrefixBatch || cache->num_kv_heads < 1 || num_q_heads % cache->num_kv_heads ||
-      cache->head_dim < 1 || cache->head_dim > kMaxHeadDim)
+  if (!prefix_shape(cache, batch, n_groups) || cache->v_head_dim != cache->head_dim || cache->num_kv_heads < 1 ||
+      num_q_heads % cache->num_kv_heads || (int64_t)batch * num_q_heads > 0x7fffffff || cache->page_size < 1 ||
+      cache->page_size % 16 || cache->page_size > 256)
     return SIZE_MAX;
+  const int64_t sub = (num_q_heads / cache->num_kv_heads + 7) / 8;
+  if (cache->num_kv_heads * sub > kMaxCtas) return SIZE_MAX;
   return prefix_ws_bytes(n, batch, num_q_heads, cache->num_kv_heads, cache->head_dim, n_groups);
 }
 

@@ -72,6 +72,17 @@ def test_workspace_bytes():
     assert f(None, 64, 32, 1, 64) == 0 and f(ctypes.byref(d), 64, 32, -1, 64) == 0
 
 
+def test_workspace_bytes_of_what_a_call_refuses():
+    f = abi.lib.pfkv_prefix_workspace_bytes
+    lat = dict(num_kv_heads=1, head_dim=576, v_head_dim=512, kv_shared=1, scale_mode=1, page_size=64)
+    for kw, hq in ((dict(head_dim=96, v_head_dim=96), 32), (dict(v_head_dim=64), 32), (lat, 64), (dict(page_size=24), 32),
+                   (dict(page_size=272), 32), (dict(page_size=0), 32), (dict(num_kv_heads=4097), 4097),
+                   (dict(num_kv_heads=2049), 2049 * 9)):
+        assert f(ctypes.byref(desc(**kw)), 4, hq, 1, 64) == SIZE_MAX, kw
+    assert f(ctypes.byref(desc()), 65535, 65536, 1, 64) == SIZE_MAX  # rows are counted in int
+    assert f(ctypes.byref(desc(num_kv_heads=4096)), 4, 4096 * 8, 1, 64) < SIZE_MAX
+
+
 ROWS, HALF, FULL = 256, 4, 7  # rows of an item; a page's cost in a block of at most half the rows, and in others
 
 
