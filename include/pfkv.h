@@ -299,8 +299,11 @@ int pfkv_paged_decode_step(const pfkv_cache *cache, const void *k_new, const voi
  *     PREFIX_DIFFERS an entry of the prefix is another page than the group's
  *                    first request (in batch order, of those whose length
  *                    covers the prefix) has there
- *   As elsewhere, a request with a data fault gets zeros and does not touch
- *   the others of its group; an unused row of the batch may keep its group
+ *   As elsewhere, a request with a data fault gets zeros.  It does not touch
+ *   the others of its group, unless it is that first request: its entries say
+ *   which pages are the group's, so that a wrong one among them (outside the
+ *   pool, or another page) refuses all the others with PREFIX_DIFFERS; its
+ *   tags are its own affair.  An unused row of the batch may keep its group
  *   with a length of 0.
  * The other arguments are those of paged_decode_attention.  Supported: its
  * grouped-query shapes (head_dim 64 or 128, FP8 with either scale mode, or

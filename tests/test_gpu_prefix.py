@@ -190,6 +190,31 @@ def test_first_request_with_a_page_outside_the_pool():
         c.table[:3, 1] = keep
 
 
+def test_first_request_with_another_page():
+    """A wrong entry in the group's first row refuses the others, and only that
+    group; a stale tag there refuses nobody else; in a later row it is that
+    row's alone."""
+    c = PrefixCase(27, [1, 0, 0, 0, 1, -1], [4, 2], [5, 6, 7, 8, 9, 10], q_heads=4, kv_heads=1, dim=64, page=16)
+    spare = int(np.setdiff1d(np.arange(c.P), c.table)[0])
+    right, diff = c.table[1, 2], abi.ST_PREFIX_DIFFERS
+
+    def status(row, page, tag=0):
+        c.table[row, 2] = page
+        c.tags[row, 2] = c.page_tags[page] ^ np.uint32(tag)
+        got, st = c.call(flags=abi.FLAG_TAG_CHECK)
+        out, _, mag = c.want()
+        tol = c.tolerance(out, mag, torch.float32)
+        fine = np.flatnonzero(st.cpu().numpy() == 0)
+        assert (np.abs(got.cpu().numpy() - out) <= tol)[fine].all() and not got[st != 0].any()
+        c.table[row, 2], c.tags[row, 2] = right, c.page_tags[right]
+        return st.tolist()
+
+    assert status(1, spare) == [0, 0, diff, diff, 0, 0]
+    assert status(1, right, 1) == [0, abi.ST_STALE_TAG, 0, 0, 0, 0]
+    assert status(2, spare) == [0, 0, diff, 0, 0, 0]
+    assert status(2, right) == [0] * 6
+
+
 @pytest.mark.parametrize("cache,page", [(FP8, 16), (FP8_TOKEN, 32), (BF16, 16)])
 def test_step_appends_then_attends(cache, page):
     c = PrefixCase(14, [0, 0, -1, 1, 0], [3, 2], [1, page, 2 * page + 3, 40, 0], q_heads=8, kv_heads=2, dim=128,
