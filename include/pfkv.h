@@ -72,8 +72,9 @@ enum {
   PFKV_ST_BAD_ROW = 128u, /* fork: a row outside the block table           */
   PFKV_ST_BAD_GROUP = 256u,     /* shared prefix: no such group, or its
                                    prefix does not fit the table           */
-  PFKV_ST_PREFIX_DIFFERS = 512u /* shared prefix: a page that is not the
+  PFKV_ST_PREFIX_DIFFERS = 512u, /* shared prefix: a page that is not the
                                    group's                                 */
+  PFKV_ST_RANGE = 1024u          /* shared prefix: scores too large         */
 };
 
 /* Return codes. */
@@ -299,6 +300,10 @@ int pfkv_paged_decode_step(const pfkv_cache *cache, const void *k_new, const voi
  *     PREFIX_DIFFERS an entry of the prefix is another page than the group's
  *                    first request (in batch order, of those whose length
  *                    covers the prefix) has there
+ *     RANGE          the prefix has softmax_scale q . k log2(e) beyond what
+ *                    its weights resolve: 2^24 and more in magnitude (BF16
+ *                    caches 2^29), infinite ones among them.  (fp32 rounds
+ *                    such scores to whole powers of two of a weight.)
  *   As elsewhere, a request with a data fault gets zeros.  It does not touch
  *   the others of its group, unless it is that first request: its entries say
  *   which pages are the group's, so that a wrong one among them (outside the

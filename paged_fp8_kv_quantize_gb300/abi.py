@@ -32,6 +32,7 @@ ST_DUPLICATE = 64
 ST_BAD_ROW = 128
 ST_BAD_GROUP = 256
 ST_PREFIX_DIFFERS = 512
+ST_RANGE = 1024
 
 EXPORTS = (
     "pfkv_kv_append_quantize",

@@ -585,6 +585,14 @@ __device__ __forceinline__ void issue_half(const PrefixArgs &a, uint8_t *smem, c
 
 // ---------------------------------------------------------------- softmax (warps 0-7)
 
+// A reference is rounded up, by as much as its last bit; up to this size the
+// largest weight then keeps its place in f16 (bf16: in fp32's range).  A
+// request whose reference passes it is refused.  (Rounding the scores as the
+// reference was would resolve them, as the plain decode does, but a branch to
+// that costs 2 to 9% of the kernel.)
+template <bool kFp8>
+constexpr float kMostRef = kFp8 ? 16777216.f : 536870912.f;  // 2^24, 2^29
+
 template <bool kFp8, int kD, int kTerms, bool kToken>
 __device__ __forceinline__ void softmax_rows(const PrefixArgs &a, uint8_t *smem, const PBars &B, uint32_t tmem,
                                              volatile int *abort) {
@@ -694,11 +702,11 @@ __device__ __forceinline__ void softmax_rows(const PrefixArgs &a, uint8_t *smem,
       for (int j = 0; j < 64; j += 2)  // three operands at a time
         part[j >> 1 & 1] = fmaxf(fmaxf(part[j >> 1 & 1], __uint_as_float(z[j])), __uint_as_float(z[j + 1]));
       float mx = fmaxf(part[0], part[1]);
-      mx = mx == kNegInf ? kNegInf : mx * mult;
+      mx = mx == kNegInf ? kNegInf : __fmul_ru(mx, mult);  // no score is above it
       // move the reference
-      const bool grow = mx > m + C::kGrow || first;
+      const bool grow = mx - m > C::kGrow || first;
       if (__any_sync(0xffffffffu, grow || moved != 1.f)) {
-        const float mn = grow ? mx - C::kLead : m;
+        const float mn = grow ? __fsub_ru(mx, C::kLead) : m;
         const float al = first ? 0.f : fast_exp2(m - mn);
         l *= al;
         if (!first) {
@@ -789,7 +797,11 @@ __device__ __forceinline__ void softmax_rows(const PrefixArgs &a, uint8_t *smem,
           stg256(a.o + at * kD + 32 * i + j, v);
         }
     }
-    if (mine) a.ml[at] = make_float2(first ? kNegInf : m, l);
+    if (mine) {
+      a.ml[at] = make_float2(first ? kNegInf : m, l);
+      if (!first && fabsf(m) >= kMostRef<kFp8>)  // references only rise: none between was larger
+        atomicOr(&a.check_st[a.members[it.first + (it.row0 + row) / a.G]], PFKV_ST_RANGE);
+    }
     tc_fence_before();
     tile0 += (uint32_t)(n_tok + kTok - 1) / kTok;
   }

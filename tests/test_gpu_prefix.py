@@ -1,5 +1,7 @@
 """Shared-prefix decode attention against the fp64 oracle, which knows nothing
 of groups: every request by itself over its whole table."""
+import math
+
 import numpy as np
 import pytest
 import torch
@@ -328,6 +330,52 @@ def test_first_token_that_outweighs_the_others(cache, out):
         extra = c.want()[2] * c.lens[:, None, None] * 2.0 ** (-35 if out == "fp32" else -25)
         tol = tol + extra * (1 + 2.0 ** -8)
     assert not st.any() and (np.abs(got.float().cpu().numpy() - want) <= tol).all()
+
+
+@pytest.mark.parametrize("out", list(OUT))
+@pytest.mark.parametrize("cache", [FP8, FP8_TOKEN, BF16])
+@pytest.mark.parametrize("most", [23.9, 35.0])
+def test_largest_scores(most, cache, out):
+    """Scores up to 2^23.9 (BF16 2^28.9), whose rounding is as large as the
+    exponents that f16 holds, are right, of either sign; those of 2^24 and more
+    (2^29) refuse their requests.  The largest score of a row leaves the others
+    behind by far more than their rounding, so the output is its value: off by
+    the rounding of one weight's terms and of the output.  (Half a step: a value
+    between 2^e and 2^(e + 1) has steps of 2^(e - 10) in f16, so one term is off
+    by 2^-11 of it, two by 2^-22; bf16 2^-8 a term, two 2^-16, three 2^-24.)"""
+    c = PrefixCase(28, [0] * 6 + [1] * 5 + [-1], [40, 9], [9 * i + 1 for i in range(12)], q_heads=16, kv_heads=2,
+                   dim=64, page=16, cache=cache)
+    if cache == BF16 and most < 24:
+        most += 5
+    c.tau = 1.0
+    z = scores(c)
+    c.tau = float(2.0 ** most / np.abs(z[np.isfinite(z)]).max())
+    for c.tau in (c.tau, -c.tau):
+        got, st = c.call(OUT[out])
+        if most == 35:  # every row of the groups is far beyond, in each of its pieces
+            assert st.tolist() == [abi.ST_RANGE] * 11 + [0] and not got[:11].any()
+        want, _, mag = c.want()
+        z = np.sort(scores(c), axis=-1)
+        largest = np.abs(np.where(np.isfinite(z), z, 0.0)).max(-1)
+        assert (z[..., -1] - z[..., -2] > 64 + 2.0 ** -16 * largest).all()
+        drop = {(True, "fp32"): -22, (True, "bf16"): -11, (False, "fp32"): -24, (False, "bf16"): -16}[cache != BF16, out]
+        tol = mag * (2.0 ** drop + 2.0 ** -20)
+        tol += 2.0 ** -8 * (mag + tol) if out == "bf16" else 0.0
+        err = np.abs(got.float().cpu().numpy() - want)
+        fine = st.cpu().numpy() == 0
+        assert fine.all() or most == 35
+        assert (err <= tol)[fine].all(), (np.isnan(err).sum(), np.nanmax((err / tol)[fine]))
+
+
+def scores(c):
+    """tau log2(e) q . k of every request and head in 64 bits; -inf past a request's length."""
+    k, q = c.values("k"), synth.bf16_to_f32(c.q).astype(np.float64)
+    z = np.full((c.B, c.Hq, int(c.lens.max())), -np.inf)
+    for b in range(c.B):
+        n = int(c.lens[b])
+        kb = k[c.table[b, : -(-n // c.S)]].transpose(1, 0, 2, 3).reshape(c.H, -1, c.D)[:, :n]
+        z[b, :, :n] = c.tau * math.log2(math.e) * np.einsum("hgd,htd->hgt", q[b].reshape(c.H, -1, c.D), kb).reshape(c.Hq, n)
+    return z
 
 
 def weight_floor(c, bits, own_max):
