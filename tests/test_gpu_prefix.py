@@ -475,6 +475,35 @@ def test_stream_argument():
     assert all(torch.equal(x, want) for x in got)
 
 
+@pytest.mark.parametrize("cache", [FP8, FP8_TOKEN, BF16])
+def test_pages_past_four_gigabytes(cache):
+    """The same batch in a small pool and at the end of one whose byte offsets
+    (and, in elements, BF16 ones) pass 32 bits: the same bits."""
+    c = PrefixCase(32, [0] * 9 + [1] * 3 + [-1], [10, 3], [30 * i + 1 for i in range(13)], q_heads=32, kv_heads=8,
+                   dim=128, page=64, cache=cache)
+    c.device()
+    want, st = c.call(flags=abi.FLAG_TAG_CHECK)
+    out, _, mag = c.want()
+    small, far = c.gpu, 70000
+    big = abi.PagedCache(far, 64, 8, 128, dtype=small.dtype, scale_mode=small.scale_mode)
+    big.page_tags[-c.P:] = small.page_tags
+    for name in ("k_pool", "v_pool", "k_scale", "v_scale"):
+        x, y = getattr(small, name), getattr(big, name)
+        if x is not None:
+            y[-x.numel():] = x
+    c.gpu = big
+    c.table = np.where(c.table >= 0, c.table + far - c.P, -1).astype(np.int32)
+    got, st2 = c.call(flags=abi.FLAG_TAG_CHECK)
+    assert not st.any() and not st2.any() and torch.equal(got, want)
+    # the first request's pages copied to the pool's start and read there
+    n = -(-int(c.lens[0]) // 64)
+    assert not abi.page_copy(big, dev_i32(c.table[0, :n]), dev_i32(np.arange(n))).any()
+    c.table[0, :n], c.group[0] = np.arange(n), -1
+    got, st2 = c.call()
+    assert not st2.any()
+    c.assert_close(got, out, mag, torch.float32)
+
+
 def test_a_refused_call_enqueues_nothing():
     """More KV heads than the split kernel takes: workspace, output and status
     stay as they were."""
