@@ -285,12 +285,17 @@ int pfkv_paged_decode_step(const pfkv_cache *cache, const void *k_new, const voi
  *                  seq_lens[b] - 1 first, as by paged_decode_step; that
  *                  position must lie past the prefix.
  *   out          : [batch][num_q_heads][head_dim], fp32 or bf16 (out_dtype,
- *                  PFKV_OUT_*).  fp32 keeps what paged_decode_attention does
- *                  (probabilities carried to about 22 bits); a bf16 output
- *                  carries them to 11 (FP8 cache) or 16 (BF16 cache) bits,
- *                  below its own rounding.
+ *                  PFKV_OUT_*).  Probabilities of the prefix are carried to
+ *                  22 bits for fp32 (BF16 cache 24), as in
+ *                  paged_decode_attention; for a bf16 output to 11 (BF16
+ *                  cache 16), below its own rounding.  FP8 caches hold them in
+ *                  f16, so that small ones are off by up to 2^-35 (bf16 output:
+ *                  2^-25) of the row's largest instead; with per-token scales
+ *                  a token whose V scale is below 2^-18 of the largest in the
+ *                  prefix counts there as if it were 2^-18 of it.
  *   workspace    : pfkv_prefix_workspace_bytes(cache, batch, num_q_heads,
- *                  n_groups, max_splits) bytes, 256-byte aligned
+ *                  n_groups, max_splits) bytes, 256-byte aligned.  Each group
+ *                  takes at least 256 rows of head_dim floats per KV head.
  *   status[b]    : that of paged_decode_attention, and
  *     BAD_GROUP      prefix_group[b] outside [-1, n_groups), or its
  *                    prefix_pages outside [0, max_pages] or 2^31 - 4096
@@ -313,8 +318,7 @@ int pfkv_paged_decode_step(const pfkv_cache *cache, const void *k_new, const voi
  * The other arguments are those of paged_decode_attention.  Supported: its
  * grouped-query shapes (head_dim 64 or 128, FP8 with either scale mode, or
  * BF16) with up to 4096 groups of up to 65535 requests in all.  The latent
- * stream is not (PFKV_ERR_UNSUPPORTED): its decode is bound by its products,
- * which sharing does not lessen.
+ * stream is not (PFKV_ERR_UNSUPPORTED).
  */
 enum { PFKV_OUT_FP32 = 0, PFKV_OUT_BF16 = 1 };
 

@@ -518,7 +518,7 @@ class PageAllocator:
         n, dev = parents.numel(), torch.cuda.current_device()
         B, MP = block_table.shape
         if fork_status is None:
-                fork_status = torch.empty(n, dtype=torch.int32, device=parents.device)
+            fork_status = torch.empty(n, dtype=torch.int32, device=parents.device)
         rc = _page_fork(
             self.state.data_ptr(), _arg(cache.page_tags, "page_tags", cache.P, dev),
             _arg(self.refs, "refs", self.num_pages, dev), cache._ref(dev), _arg(parents, "parents", n, dev),

@@ -818,8 +818,9 @@ constexpr int kNCW = 4;
 // (many pieces, each with its own set-up and finish) gets fewer pages.
 constexpr int kPieceCost = 16;
 
-// Launch shape of one split-kernel instantiation for one page size, worked out on its first use and reused afterwards, so that later
-// calls -- including calls under stream capture -- only enqueue kernels.
+// Launch shape of one split-kernel instantiation for one page size, worked out
+// on its first use and reused afterwards, so that later calls -- including
+// calls under stream capture -- only enqueue kernels.
 struct SplitShape {
   int S = 0, dev = -1, nst = 0, grid = 0;
   uint32_t smem = 0;

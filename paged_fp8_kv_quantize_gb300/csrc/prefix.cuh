@@ -87,7 +87,10 @@ __host__ __device__ __forceinline__ int range_of(const PrefixHdr &h, long long u
   return (int)div_floor((u + 1) * h.R - 1, h.T);
 }
 
-constexpr int kCostHalf = 4, kCostFull = 7;  // a page's cost: about 1.1 us and 1.8 us per 128 tokens (FP8, D 128)
+// A page's cost: about 1.1 us and 1.8 us per 128 tokens for FP8 caches of head
+// dimension 128, and used for all.  (They only weigh blocks of at most half the
+// rows against the others, on a line that has both.)
+constexpr int kCostHalf = 4, kCostFull = 7;
 
 // Units of an item's set-up and read-out, about what 512 tokens of a small
 // block cost, and units that a range holds at least: 256 such tokens, and one

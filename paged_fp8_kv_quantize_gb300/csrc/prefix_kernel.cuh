@@ -21,8 +21,9 @@
 //                   maxima and sums need no exchange; P overwrites S.
 //   warps 8-11      FP8: operands e4m3 -> f16 from staged codes, once per CTA,
 //                   into a ring of K and V tiles of 128 tokens in the 128-byte-
-//                   swizzled layout.  (BF16: the planner's tensor copies land
-//                   in that ring by themselves.)
+//                   swizzled layout; per-token scales parted between V operands
+//                   and weights (hand_scales).  (BF16: the planner's tensor
+//                   copies land in that ring by themselves.)
 //   warps 12, 14    issue the MMAs of half 0 and 1.
 //   warp 13         planner: works out the CTA's items and where each tile's
 //                   rows lie (bounds-checked page ids), so that nobody else
@@ -41,7 +42,8 @@
 // first units hardly happens; O is then rescaled in tensor memory by the row's
 // own softmax warp, after the products it has handed over and before the next.
 // f16 weights below 2^-14 are subnormal: off by at most 2^-25, alone or (second
-// term) together.
+// term) together, where the largest weight starts at 2^0 or, with two terms, at
+// 2^10 (PCfg::kLead).
 #pragma once
 
 #include "prefix.cuh"
@@ -611,7 +613,8 @@ __device__ __forceinline__ void softmax_rows(const PrefixArgs &a, uint8_t *smem,
     const int n_tok = (it.p1 - it.p0) * S;
     const int row = it.split ? r : t * (kRows / 2) + r;  // row of the item's block
     const bool mine = row < it.n_rows;
-    // this thread's query row into the operand; f16: scaled by 2^e into [2^14, 2^15), exact; the sign of the
+    // this thread's query row into the operand; f16: scaled by 2^e, its largest value into [2^14, 2^15), exact down to
+    // 2^-31 of that (smaller values are rounded to steps of 2^-24); the sign of the
     // factor that turns products into scores goes with it, so that the largest product is the largest score
     float mult = a.d.sm_scale_log2;
     if (kFp8 && !kToken) mult *= a.d.k_scale[it.h];
