@@ -10,6 +10,7 @@ from __future__ import annotations
 import ctypes
 import functools
 import os
+import struct
 
 import torch
 
@@ -84,6 +85,10 @@ class CacheDesc(ctypes.Structure):
         ("v_scale", ctypes.c_void_p),
         ("page_tags", ctypes.c_void_p),
     ]
+
+
+_DESC = struct.Struct("8i5P")  # CacheDesc, packed
+assert _DESC.size == ctypes.sizeof(CacheDesc)
 
 
 def _load():
@@ -253,10 +258,10 @@ class PagedCache:
                 or v is not None and v.get_device() != dev or ks is not None and ks.get_device() != dev
                 or vs is not None and vs.get_device() != dev):
             raise ValueError(f"the cache's tensors are not all on the current device ({dev})")
-        return ctypes.byref(CacheDesc(
+        return ctypes.byref(CacheDesc.from_buffer_copy(_DESC.pack(  # half the time of the constructor
             self.P, self.S, self.H, self.D, self.Dv, self.kv_shared, self.dtype, self.scale_mode,
-            None if k is None else k.data_ptr(), None if v is None else v.data_ptr(),
-            None if ks is None else ks.data_ptr(), None if vs is None else vs.data_ptr(), tags.data_ptr()))
+            0 if k is None else k.data_ptr(), 0 if v is None else v.data_ptr(), 0 if ks is None else ks.data_ptr(),
+            0 if vs is None else vs.data_ptr(), tags.data_ptr())))
 
     def k_rows(self):
         return self.k_pool.view(self.P, self.H, self.S, self.D)
