@@ -307,8 +307,9 @@ int pfkv_paged_decode_step(const pfkv_cache *cache, const void *k_new, const voi
  *                    covers the prefix) has there
  *     RANGE          the prefix has softmax_scale q . k log2(e) beyond what
  *                    its weights resolve: 2^24 and more in magnitude (BF16
- *                    caches 2^29), infinite ones among them.  (fp32 rounds
- *                    such scores to whole powers of two of a weight.)
+ *                    caches 2^29; fp32 rounds such scores to whole powers of
+ *                    two of a weight).  Infinite and NaN ones give NaN in
+ *                    their head's row.
  *   As elsewhere, a request with a data fault gets zeros.  It does not touch
  *   the others of its group, unless it is that first request: its entries say
  *   which pages are the group's, so that a wrong one among them (outside the

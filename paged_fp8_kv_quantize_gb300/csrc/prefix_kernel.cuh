@@ -802,7 +802,8 @@ __device__ __forceinline__ void softmax_rows(const PrefixArgs &a, uint8_t *smem,
     }
     if (mine) {
       a.ml[at] = make_float2(first ? kNegInf : m, l);
-      if (!first && fabsf(m) >= kMostRef<kFp8>)  // references only rise: none between was larger
+      // references only rise: none between was larger.  (Infinite ones give NaN, as in the plain decode.)
+      if (!first && fabsf(m) >= kMostRef<kFp8> && fabsf(m) < INFINITY)
         atomicOr(&a.check_st[a.members[it.first + (it.row0 + row) / a.G]], PFKV_ST_RANGE);
     }
     tc_fence_before();

@@ -367,6 +367,26 @@ def test_largest_scores(most, cache, out):
         assert (err <= tol)[fine].all(), (np.isnan(err).sum(), np.nanmax((err / tol)[fine]))
 
 
+@pytest.mark.parametrize("out", list(OUT))
+@pytest.mark.parametrize("cache", [FP8, FP8_TOKEN, BF16])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+def test_query_that_is_not_finite(bad, cache, out):
+    """One element of one head's query: that row is NaN, as in the plain decode,
+    the other rows of its product, its request and its group keep their bits."""
+    c = PrefixCase(29, [0] * 6 + [1] * 5 + [-1], [40, 9], [9 * i + 1 for i in range(12)], q_heads=16, kv_heads=2,
+                   dim=64, page=16, cache=cache)
+    want = c.call(OUT[out])[0].clone()
+    a = c.args()
+    a["q"][2, 5, 33] = bad
+    got, st = c.call(OUT[out], **a)
+    rows = torch.ones(12, 16, dtype=torch.bool, device="cuda")
+    rows[2, 5] = False
+    assert not st.any() and torch.equal(got[rows], want[rows])
+    assert got[2, 5].isnan().all()
+    plain, _ = abi.paged_decode_attention(c.gpu, a["q"], a["seq_lens"], a["block_table"], None, c.tau)
+    assert plain[2, 5].isnan().all()
+
+
 def scores(c):
     """tau log2(e) q . k of every request and head in 64 bits; -inf past a request's length."""
     k, q = c.values("k"), synth.bf16_to_f32(c.q).astype(np.float64)
