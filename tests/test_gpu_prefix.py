@@ -524,6 +524,34 @@ def test_pages_past_four_gigabytes(cache):
     c.assert_close(got, out, mag, torch.float32)
 
 
+@pytest.mark.parametrize("batch,n_groups,Hq,H", [(65535, 4096, 1, 1), (4096, 4096, 12, 2), (300, 1, 512, 1)])
+def test_largest_batches_groups_and_head_groups(batch, n_groups, Hq, H):
+    """Against the plain decode of the same tables: fp32 sums of products of
+    either, each within the tolerance of the other tests (here, as bounds of
+    all rows: scores of at most 2^6, contexts of at most 100 tokens)."""
+    g = torch.Generator(device="cuda").manual_seed(6)
+    D, S = 64, 16
+    pages = torch.randint(0, 3, (n_groups,), generator=g, device="cuda", dtype=torch.int32)
+    group = torch.randint(-1, n_groups, (batch,), generator=g, device="cuda", dtype=torch.int32)
+    skip = torch.where(group < 0, 0, pages[group.clamp(min=0).long()])
+    lens = (skip * S + torch.randint(1, 3 * S + 1, (batch,), generator=g, device="cuda")).int()
+    P = 2 * n_groups + 3 * batch
+    own = (2 * n_groups + torch.arange(3 * batch, device="cuda", dtype=torch.int32)).view(batch, 3)
+    cols = torch.arange(5, device="cuda")[None]
+    table = torch.where(cols < skip[:, None], 2 * group.clamp(min=0)[:, None] + cols,
+                        own.gather(1, (cols - skip[:, None]).clamp(0, 2).long())).int()
+    cache = abi.PagedCache(P, S, H, D)
+    for pool in (cache.k_pool, cache.v_pool):  # codes of magnitudes below 2, of either sign
+        pool.copy_(torch.randint(0, 64, pool.shape, generator=g, device="cuda", dtype=torch.uint8))
+        pool += 128 * torch.randint(0, 2, pool.shape, generator=g, device="cuda", dtype=torch.uint8)
+    q = torch.randn((batch, Hq, D), generator=g, device="cuda").bfloat16()
+    got, st = abi.paged_decode_attention_prefix(cache, q, lens, table, None, group, pages, 0.125, max_splits=2)
+    want, st2 = abi.paged_decode_attention(cache, q, lens, table, None, 0.125, max_splits=2)
+    assert not st.any() and not st2.any()
+    # |v| < 2; scores off by (64 + 4) 2^-24 x 2^6, twice, weights by 2^-21, sums by 100 x 2^-24, in both calls
+    assert ((got - want).abs() <= 2 * 2 * (2 * 68 * 64 * 2.0 ** -24 * math.log(2) + 2.0 ** -20 + 200 * 2.0 ** -24)).all()
+
+
 def test_a_refused_call_enqueues_nothing():
     """More KV heads than the split kernel takes: workspace, output and status
     stay as they were."""
