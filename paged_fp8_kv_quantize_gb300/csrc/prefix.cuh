@@ -81,7 +81,9 @@ struct PrefixArgs {
 };
 
 // floor(k T / R): first unit of range k.
-__host__ __device__ __forceinline__ long long range_start(const PrefixHdr &h, long long k) { return div_floor(k * h.T, h.R); }
+__host__ __device__ __forceinline__ long long range_start(const PrefixHdr &h, long long k) {
+  return div_floor(k * h.T, h.R);
+}
 // The range that holds unit u.
 __host__ __device__ __forceinline__ int range_of(const PrefixHdr &h, long long u) {
   return (int)div_floor((u + 1) * h.R - 1, h.T);
